@@ -1,0 +1,435 @@
+"""The operators of a mixture-of-experts layer around the grouped FP8 products: cases and plain forms.
+
+Four operators, each one call (or a forward and its backward call) of the package:
+
+  route     moe_route (and moe_route_backward): router logits -> the k chosen experts of each token
+            and their weights; logits' gradient from the weights' gradient.
+  dispatch  moe_plan + moe_dispatch: the chosen experts -> tokens sorted by expert, quantized to
+            e4m3 codes with 1x128 scales (and, for training, copied in bf16).
+  product   gemm_1x128_128x128_routed: every expert's FP8 product for the few rows routed to it, read
+            through the plan; with swiglu, the gate and up halves joined in the same pass.
+  combine   moe_combine (and moe_combine_backward): the experts' rows back to their tokens, weighted;
+            gradients of the rows and of the weights.
+
+Run where ``own`` is false, the same results come from elementary torch operations.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+BLOCK = 128
+FP8_MAX = 448.0
+AMAX_FLOOR = 1e-12
+SUM_FLOOR = 2.0 ** -126     # a sum of chosen sigmoid scores below the smallest normal counts as that
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def listed():
+    return [
+        # one token of a decode step, sigmoid scores with a balance bias and expert groups
+        dict(name="route 1 token", op="route", tokens=1, experts=256, k=8, score="sigmoid", bias=True, groups=8, top_groups=4,
+             renormalize=True, scale=2.5, dtype="f32", backward=False),
+        # a long prompt through the same router
+        dict(name="route 16384 tokens", op="route", tokens=16384, experts=256, k=8, score="sigmoid", bias=True, groups=8, top_groups=4,
+             renormalize=True, scale=2.5, dtype="f32", backward=False),
+        # a training step of a softmax router whose weights are the plain probabilities
+        dict(name="route train softmax", op="route", tokens=8191, experts=64, k=6, score="softmax", bias=False, groups=1, top_groups=1,
+             renormalize=False, scale=1.0, dtype="bf16", backward=True),
+        # a decode batch of 64 requests
+        dict(name="dispatch 64 tokens", op="dispatch", tokens=64, experts=64, k=8, features=4096, dropped=0.0, copy=False),
+        # a prompt chunk on one of several expert-parallel ranks: an eighth of the choices live elsewhere
+        dict(name="dispatch 1000 dropped", op="dispatch", tokens=1000, experts=56, k=6, features=1280, dropped=0.125, copy=False),
+        # a training batch: codes for the products and the bf16 rows for the weight gradient
+        dict(name="dispatch train 8192", op="dispatch", tokens=8192, experts=64, k=8, features=4096, dropped=0.0, copy=True),
+        # one token: 8 experts' weights are read for one row each
+        dict(name="product 1 token", op="product", tokens=1, experts=64, k=8, n=2048, features=4096, swiglu=False, skew=0.5),
+        # a decode batch over few wide experts, gate and up products joined
+        dict(name="product 32 tokens gated", op="product", tokens=32, experts=8, k=2, n=2048, features=4096, swiglu=True, skew=0.5),
+        # a large decode batch: 16 rows an expert on average, ragged
+        dict(name="product 128 tokens gated", op="product", tokens=128, experts=64, k=8, n=1024, features=4096, swiglu=True, skew=0.5),
+        # a prompt chunk: 60 rows an expert on average, a short odd inner dimension
+        dict(name="product 480 tokens", op="product", tokens=480, experts=64, k=8, n=5120, features=1280, swiglu=False, skew=0.5),
+        # a decode batch
+        dict(name="combine 33 tokens", op="combine", tokens=33, k=8, features=5120, dropped=0.0, backward=False),
+        # a training batch, forward and backward
+        dict(name="combine train 8192", op="combine", tokens=8192, k=8, features=4096, dropped=0.0, backward=True),
+    ]
+
+
+def _between(rng, low, high):
+    """A whole number between the two, spread evenly over its logarithm."""
+    return max(low, min(high, int(round(math.exp(rng.uniform(math.log(low), math.log(high + 1)))))))
+
+
+def draw(rng):
+    op = rng.choice(["route", "dispatch", "product", "combine"])
+    if op == "route":
+        experts = rng.choice([8, 16, 60, 64, 72, 96, 128, 160, 256, 384])
+        k = min(experts, rng.choice([1, 2, 4, 6, 8]))
+        grouped = experts % 8 == 0 and experts >= 64 and rng.random() < 0.5
+        score = rng.choice(["softmax", "sigmoid"])
+        return dict(op=op, tokens=_between(rng, 1, 16384), experts=experts, k=k, score=score, bias=rng.random() < 0.5, groups=8 if grouped else 1,
+                    top_groups=rng.choice([2, 3, 4]) if grouped else 1, renormalize=rng.random() < 0.5, scale=rng.choice([1.0, 2.5]),
+                    dtype=rng.choice(["bf16", "f32"]), backward=rng.random() < 0.5)
+    if op == "product":
+        swiglu = rng.random() < 0.5
+        experts = rng.choice([8, 16, 40, 64])
+        n = rng.choice([512, 1024, 1408, 2048]) if swiglu else rng.choice([512, 1000, 1280, 2048, 4096])
+        features = rng.choice([512, 1280, 1408, 2048, 4096])
+        experts = min(experts, 64 * 5120 * 1280 // (n * features * (2 if swiglu else 1)))
+        return dict(op=op, tokens=_between(rng, 1, 60 * experts // 8), experts=experts, k=rng.choice([1, 2, 4, 8]), n=n,
+                    features=features, swiglu=swiglu, skew=rng.choice([0.0, 0.5, 1.0]))
+    k = rng.choice([1, 2, 4, 6, 8])
+    features = rng.choice([128, 512, 1000, 1280, 2048, 2056, 4096, 5120])
+    most = max(1, 8192 * 8 * 4096 // (k * features))
+    case = dict(op=op, tokens=_between(rng, 1, min(16384, most)), k=k, features=features, dropped=rng.choice([0.0, 0.0, 0.125, 0.5]))
+    if op == "dispatch":
+        return dict(case, experts=rng.choice([8, 16, 64, 100, 256]), copy=rng.random() < 0.5)
+    return dict(case, backward=rng.random() < 0.5)
+
+
+def work(case):
+    T, k = case["tokens"], case["k"]
+    R = T * k
+    if case["op"] == "route":
+        E, es = case["experts"], 2 if case["dtype"] == "bf16" else 4
+        b = T * E * es + R * 8 + (4 * E if case["bias"] else 0)
+        return {"bytes": b + (T * E * es + R * 4 if case["backward"] else 0), "flops": T * E * (8 if case["backward"] else 4)}
+    if case["op"] == "dispatch":
+        H, E = case["features"], case["experts"]
+        live = R * (1 - case["dropped"])
+        read = R * 4 + (T * H * 2 if live >= T else live * H * 2)
+        return {"bytes": read + R * (H + 4 * -(-H // BLOCK) + (2 * H if case["copy"] else 0)) + R * 8 + (E + 1) * 8, "flops": 3 * R * H}
+    if case["op"] == "combine":
+        H, live = case["features"], R * (1 - case["dropped"])
+        b = live * H * 2 + R * 8 + T * H * 2
+        return {"bytes": b + (T * H * 2 + R * H * 2 + R * 4 if case["backward"] else 0), "flops": 2 * live * H * (3 if case["backward"] else 1)}
+    E, K, N, F = case["experts"], case["features"], case["n"] * (2 if case["swiglu"] else 1), case["n"]
+    active = E * (1 - (1 - min(k, E) / E) ** T)     # experts that have a row, as even choices give them
+    rows = T if case["swiglu"] else R
+    return {"bytes": active * (N * K + 4 * (-(-N // BLOCK)) * (K // BLOCK)) + rows * (K + K // 32) + R * (4 + F * 2) + (E + 1) * 8,
+            "flops": 2 * R * N * K}
+
+
+def _rng(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _chosen(g, T, E, k, skew, dropped=0.0):
+    """Distinct experts of each token, experts unevenly liked; a share of the choices set to -1."""
+    liking = torch.randn(T, E, generator=g, device=DEV) + skew * 2 * torch.randn(E, generator=g, device=DEV)
+    ids = liking.sort(dim=1, descending=True).indices[:, :k].to(torch.int32)
+    if dropped:
+        ids = ids.masked_fill(torch.rand(T, k, generator=g, device=DEV) < dropped, -1)
+    return ids.contiguous()
+
+
+def _plan(ids, E):
+    """offsets, slots, rows of moe_plan."""
+    flat = ids.reshape(-1).long()
+    bins = torch.where((flat >= 0) & (flat < E), flat, E)
+    ranked, order = bins.sort(stable=True)
+    offsets = torch.searchsorted(ranked, torch.arange(E + 1, device=ids.device))
+    place = torch.arange(flat.numel(), device=ids.device)
+    live = place < offsets[E]
+    slots = torch.empty_like(place)
+    slots[order] = torch.where(live, place, -1 - place)
+    return offsets, slots.to(torch.int32).reshape(ids.shape), torch.where(live, order, -1).to(torch.int32)
+
+
+def prepare(case, seed):
+    g, T, k, op = _rng(seed), case["tokens"], case["k"], case["op"]
+    R = T * k
+    s = {"case": case}
+    if op == "route":
+        E = case["experts"]
+        z = 1.5 * torch.randn(T, E, generator=g, device=DEV) + 0.5 * torch.randn(E, generator=g, device=DEV)
+        s["logits"] = z.to(DTYPES[case["dtype"]])
+        s["bias"] = 0.05 * torch.randn(E, generator=g, device=DEV) if case["bias"] else None
+        s["dweights"] = torch.randn(T, k, generator=g, device=DEV) if case["backward"] else None
+        s["weights"] = torch.empty(T, k, device=DEV)
+        s["ids"] = torch.empty(T, k, dtype=torch.int32, device=DEV)
+        s["dlogits"] = torch.empty_like(s["logits"]) if case["backward"] else None
+        return s
+    if op == "dispatch":
+        H, E = case["features"], case["experts"]
+        s["ids"] = _chosen(g, T, max(E, k), k, 0.5, case["dropped"])
+        s["x"] = torch.randn(T, H, generator=g, device=DEV).to(torch.bfloat16)
+        s["q"] = torch.empty(R, H, dtype=torch.uint8, device=DEV)
+        s["a_s"] = torch.empty(-(-H // BLOCK), R, device=DEV)
+        s["copy"] = torch.empty(R, H, dtype=torch.bfloat16, device=DEV) if case["copy"] else None
+        return s
+    if op == "combine":
+        H = case["features"]
+        s["slots"] = _plan(_chosen(g, T, 64, k, 0.5, case["dropped"]), 64)[1]
+        s["rows"] = torch.randn(R, H, generator=g, device=DEV).to(torch.bfloat16)
+        s["weights"] = torch.rand(T, k, generator=g, device=DEV) + 0.05
+        s["dy"] = torch.randn(T, H, generator=g, device=DEV).to(torch.bfloat16) if case["backward"] else None
+        s["y"] = torch.empty(T, H, dtype=torch.bfloat16, device=DEV)
+        s["drows"] = torch.empty_like(s["rows"]) if case["backward"] else None
+        s["dweights"] = torch.empty_like(s["weights"]) if case["backward"] else None
+        return s
+    E, K, F = case["experts"], case["features"], case["n"]
+    N = 2 * F if case["swiglu"] else F
+    s["offsets"], _, s["rows"] = _plan(_chosen(g, T, E, k, case["skew"]), E)
+    A = T if case["swiglu"] else R           # the gated product reads the tokens' rows through the plan
+    s["a"] = (FP8_MAX / 3 * torch.randn(A, K, generator=g, device=DEV)).clamp(-FP8_MAX, FP8_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
+    s["a_s"] = (0.5 + torch.rand(K // BLOCK, A, generator=g, device=DEV)) * (3 / FP8_MAX)
+    s["b"] = torch.empty(E * N, K, dtype=torch.uint8, device=DEV)
+    for e in range(E):
+        w = FP8_MAX / 4 * torch.randn(N, K, generator=g, device=DEV)
+        s["b"][e * N:(e + 1) * N] = w.clamp(-FP8_MAX, FP8_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
+    s["b_s"] = (0.5 + torch.rand(E, -(-N // BLOCK), K // BLOCK, generator=g, device=DEV)) * (0.08 / FP8_MAX)
+    s["c"] = torch.empty(R, F, dtype=torch.bfloat16, device=DEV)
+    return s
+
+
+def run(s):
+    case = s["case"]
+    return (_OWN if own else _PLAIN)[case["op"]](s, case)
+
+
+# ------------------------------------------------------------------ the package's calls
+
+def _own_route(s, c):
+    import blockwise_scaled_fp8_act_amd as bf
+    w, ids = bf.moe_route(s["logits"], c["k"], score=c["score"], bias=s["bias"], groups=c["groups"], top_groups=c["top_groups"],
+                          renormalize=c["renormalize"], scale=c["scale"], weights=s["weights"], ids=s["ids"])
+    if not c["backward"]:
+        return w, ids
+    return w, ids, bf.moe_route_backward(s["logits"], ids, s["dweights"], score=c["score"], renormalize=c["renormalize"], scale=c["scale"],
+                                         dlogits=s["dlogits"])
+
+
+def _own_dispatch(s, c):
+    import blockwise_scaled_fp8_act_amd as bf
+    offsets, slots, rows = bf.moe_plan(s["ids"], c["experts"])
+    q, a_s, copy = bf.moe_dispatch(s["x"], slots, q=s["q"], a_s=s["a_s"], copy=s["copy"])
+    return offsets, slots, rows, q.view(torch.float8_e4m3fn), a_s, copy
+
+
+def _own_product(s, c):
+    import blockwise_scaled_fp8_act_amd as bf
+    Nb, Kb = s["b_s"].shape[1:]
+    N = s["b"].shape[0] // c["experts"]
+    return bf.gemm_1x128_128x128_routed(s["a"], s["a_s"], s["b"], s["b_s"], s["offsets"], c["experts"], b_stride=N * c["features"], bs_stride=Nb * Kb,
+                                        bs_stride_nb=Kb, bs_stride_kb=1, rows=s["rows"] if c["swiglu"] else None, k=c["k"], swiglu=c["swiglu"], c=s["c"])
+
+
+def _own_combine(s, c):
+    import blockwise_scaled_fp8_act_amd as bf
+    y = bf.moe_combine(s["rows"], s["slots"], s["weights"], y=s["y"])
+    if not c["backward"]:
+        return y
+    return (y, *bf.moe_combine_backward(s["dy"], s["rows"], s["slots"], s["weights"], drows=s["drows"], dweights=s["dweights"]))
+
+
+# ------------------------------------------------------------------ the plain forms
+
+def _plain_route(s, c):
+    z = s["logits"]
+    T, E = z.shape
+    z64, z32 = z.double(), z.float()
+    if c["score"] == "softmax":
+        e64, e32 = (z64 - z64.amax(1, keepdim=True)).exp(), (z32 - z32.amax(1, keepdim=True)).exp()
+        p64, p32 = e64 / e64.sum(1, keepdim=True), e32 / e32.sum(1, keepdim=True)
+    else:
+        p64, p32 = 1 / (1 + (-z64).exp()), 1 / (1 + (-z32).exp())
+    keys = z64 if s["bias"] is None else p64 + s["bias"].double()   # in 64 bits: the choice is made between near values
+    if c["groups"] > 1:
+        best = keys.view(T, c["groups"], -1).sort(dim=2, descending=True).values
+        value = best[:, :, 0] if s["bias"] is None else best[:, :, :2].sum(2)
+        kept = value.sort(dim=1, descending=True, stable=True).indices[:, :c["top_groups"]]
+        keep = torch.zeros(T, c["groups"], dtype=torch.bool, device=z.device).scatter_(1, kept, True)
+        keys = keys.masked_fill(~keep.repeat_interleave(E // c["groups"], 1), -math.inf)
+    ids = keys.sort(dim=1, descending=True, stable=True).indices[:, :c["k"]]
+    q, scale = p32.gather(1, ids), c["scale"]
+    if not c["renormalize"]:
+        w = scale * q
+    elif c["score"] == "softmax":
+        zs = z32.gather(1, ids)
+        es = (zs - zs.amax(1, keepdim=True)).exp()
+        share = es / es.sum(1, keepdim=True)
+        w = scale * share
+    else:
+        total = q.sum(1, keepdim=True).clamp_min(SUM_FLOOR)
+        w = scale * q / total
+    if not c["backward"]:
+        return w, ids.to(torch.int32)
+    dw = s["dweights"]
+    dz = torch.zeros(T, E, device=z.device)
+    if c["score"] == "softmax" and c["renormalize"]:
+        dz.scatter_(1, ids, scale * share * (dw - (share * dw).sum(1, keepdim=True)))
+    elif c["score"] == "softmax":
+        dz.scatter_(1, ids, scale * dw)
+        dz = p32 * (dz - (scale * dw * q).sum(1, keepdim=True))
+    else:
+        dq = scale * (dw - (dw * q).sum(1, keepdim=True) / total) / total if c["renormalize"] else scale * dw
+        dz.scatter_(1, ids, dq * q * (1 / (1 + z32.gather(1, ids).exp())))
+    return w, ids.to(torch.int32), dz.to(z.dtype)
+
+
+def _plain_dispatch(s, c):
+    x, k = s["x"], c["k"]
+    offsets, slots, rows = _plan(s["ids"], c["experts"])
+    H = x.shape[1]
+    live = (rows >= 0)[:, None]
+    xr = torch.where(live, x[(rows.clamp_min(0) // k).long()].float(), 0.0)
+    groups = torch.nn.functional.pad(xr, (0, -H % BLOCK)).view(xr.shape[0], -1, BLOCK)
+    amax = groups.abs().amax(2).clamp_min(AMAX_FLOOR)
+    a_s = torch.where(live, amax / FP8_MAX, 0.0).t().contiguous()
+    q = (groups * (FP8_MAX / amax)[:, :, None]).clamp(-FP8_MAX, FP8_MAX).view(xr.shape[0], -1)[:, :H].to(torch.float8_e4m3fn)
+    return offsets, slots, rows, q, a_s, xr.to(torch.bfloat16) if c["copy"] else None
+
+
+def _plain_product(s, c):
+    E, K, F = c["experts"], c["features"], c["n"]
+    N, R, T = s["b"].shape[0] // E, c["tokens"] * c["k"], c["tokens"]
+    a = s["a"].view(torch.float8_e4m3fn).float() * s["a_s"].t().repeat_interleave(BLOCK, 1)
+    if c["swiglu"]:
+        a = a[(s["rows"] // c["k"]).long()]
+    w = s["b"].view(torch.float8_e4m3fn).float().view(E, N, K)
+    w = w * s["b_s"].repeat_interleave(BLOCK, 2).repeat_interleave(BLOCK, 1)[:, :N]
+    row = torch.arange(R, device=a.device)
+    expert = torch.searchsorted(s["offsets"][1:].contiguous(), row, right=True)
+    place = row - s["offsets"][expert]
+    padded = torch.zeros(E, T, K, device=a.device)          # a token chooses an expert once: at most T rows each
+    padded[expert, place] = a
+    out = torch.bmm(padded, w.transpose(1, 2).contiguous())[expert, place]
+    if c["swiglu"]:
+        gate, up = out[:, :F], out[:, F:]
+        out = gate / (1 + (-gate).exp()) * up
+    return out.to(torch.bfloat16)
+
+
+def _plain_combine(s, c):
+    slots, w = s["slots"].long(), s["weights"]
+    live = (slots >= 0)[:, :, None]
+    e = torch.where(live, s["rows"][slots.clamp_min(0)].float(), 0.0)
+    y = (w[:, :, None] * e).sum(1).to(torch.bfloat16)
+    if not c["backward"]:
+        return y
+    dy = s["dy"].float()[:, None, :]
+    drows = torch.zeros(s["rows"].shape, dtype=torch.bfloat16, device=y.device)
+    drows[torch.where(slots >= 0, slots, -1 - slots).reshape(-1)] = torch.where(live, w[:, :, None] * dy, 0.0).to(torch.bfloat16).reshape(-1, dy.shape[2])
+    return y, drows, (dy * e).sum(2)
+
+
+_OWN = {"route": _own_route, "dispatch": _own_dispatch, "product": _own_product, "combine": _own_combine}
+_PLAIN = {"route": _plain_route, "dispatch": _plain_dispatch, "product": _plain_product, "combine": _plain_combine}
+
+
+# ------------------------------------------------------------------ the definitions in 64 bits
+
+def exact(case, seed):
+    return _EXACT[case["op"]](prepare(case, seed), case)
+
+
+def _host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _exact_route(s, c):
+    z, k, scale = _host(s["logits"]), c["k"], c["scale"]
+    T, E = z.shape
+    m = z.max(axis=1, keepdims=True)
+    p = np.exp(z - m) / np.exp(z - m).sum(axis=1, keepdims=True) if c["score"] == "softmax" else 1.0 / (1.0 + np.exp(-z))
+    key = z if s["bias"] is None else p + _host(s["bias"])
+    if c["groups"] > 1:
+        size = E // c["groups"]
+        by = -np.sort(-key.reshape(T, c["groups"], size), axis=2)
+        value = by[:, :, 0] + (by[:, :, 1] if s["bias"] is not None and size > 1 else 0.0)
+        rank = np.argsort(np.argsort(-value, axis=1, kind="stable"), axis=1)
+        key = np.where(np.repeat(rank < c["top_groups"], size, axis=1), key, -np.inf)
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :k]
+    at = np.arange(T)[:, None], ids
+    norm = p[at].sum(axis=1, keepdims=True) if c["renormalize"] else np.ones((T, 1))
+    if c["renormalize"] and c["score"] == "sigmoid":
+        norm = np.maximum(norm, SUM_FLOOR)
+    w = scale * p[at] / norm
+    out = [torch.from_numpy(w), torch.from_numpy(ids.astype(np.int32))]
+    if c["backward"]:
+        dw = _host(s["dweights"])
+        dp = np.zeros((T, E))            # by the chain rule: weights -> chosen scores -> all scores -> logits
+        dp[at] = scale * (dw - (dw * p[at]).sum(axis=1, keepdims=True) / norm) / norm if c["renormalize"] else scale * dw
+        dz = p * (dp - (dp * p).sum(axis=1, keepdims=True)) if c["score"] == "softmax" else dp * p * (1.0 - p)
+        out.append(torch.from_numpy(dz))
+    return tuple(out)
+
+
+def _exact_e4m3(v):
+    """The nearest e4m3 value of numbers within +-448, ties to even."""
+    mag = v.abs().clamp_min(2.0 ** -9)
+    step = torch.exp2(torch.floor(torch.log2(mag)).clamp_min(-6) - 3)
+    return (torch.round(v / step) * step).clamp(-FP8_MAX, FP8_MAX)
+
+
+def _exact_dispatch(s, c):
+    ids, E, H, R = s["ids"].reshape(-1).cpu().numpy(), c["experts"], c["features"], c["tokens"] * c["k"]
+    ok = (ids >= 0) & (ids < E)
+    order = np.concatenate([np.flatnonzero(ids == e) for e in range(E)] + [np.flatnonzero(~ok)])
+    offsets = np.concatenate([[0], np.cumsum([(ids == e).sum() for e in range(E)])]).astype(np.int64)
+    live = int(offsets[-1])
+    slots = np.empty(R, dtype=np.int32)
+    slots[order[:live]] = np.arange(live)
+    slots[order[live:]] = -1 - np.arange(live, R)
+    rows = np.concatenate([order[:live], np.full(R - live, -1)]).astype(np.int32)
+    x = s["x"].double()
+    groups = torch.zeros(x.shape[0], -(-H // BLOCK) * BLOCK, dtype=torch.float64, device=DEV)
+    groups[:, :H] = x
+    groups = groups.reshape(x.shape[0], -1, BLOCK)
+    top = groups.abs().amax(dim=2).clamp_min(AMAX_FLOOR)
+    code = _exact_e4m3(groups * FP8_MAX / top[:, :, None]).reshape(x.shape[0], -1)[:, :H].float()     # e4m3 values: whole in 32 bits
+    token = torch.from_numpy(order[:live] // c["k"]).to(DEV)
+    q = torch.zeros(R, H, device=DEV)
+    q[:live] = code[token]
+    a_s = torch.zeros(top.shape[1], R, dtype=torch.float64, device=DEV)
+    a_s[:, :live] = (top / FP8_MAX)[token].t()
+    copy = None
+    if c["copy"]:
+        copy = torch.zeros(R, H, dtype=torch.bfloat16, device=DEV)
+        copy[:live] = s["x"][token]
+    return torch.from_numpy(offsets), torch.from_numpy(slots).view(-1, c["k"]), torch.from_numpy(rows), q, a_s, copy
+
+
+def _exact_product(s, c):
+    E, K, F = c["experts"], c["features"], c["n"]
+    N = s["b"].shape[0] // E
+    at = s["offsets"].tolist()
+    out = torch.zeros(c["tokens"] * c["k"], F, dtype=torch.float64, device=DEV)
+    codes = s["a"].view(torch.float8_e4m3fn)
+    for e in range(E):
+        lo, hi = at[e], at[e + 1]
+        if lo == hi:
+            continue
+        pick = (s["rows"][lo:hi] // c["k"]).long() if c["swiglu"] else torch.arange(lo, hi, device=DEV)
+        a, b = codes.view(torch.uint8)[pick].view(torch.float8_e4m3fn).double(), s["b"][e * N:(e + 1) * N].view(torch.float8_e4m3fn).double()
+        a = a.view(hi - lo, K // BLOCK, BLOCK) * s["a_s"][:, pick].double().t()[:, :, None]
+        factor = s["b_s"][e].double()[torch.arange(N, device=DEV) // BLOCK]
+        b = b.view(N, K // BLOCK, BLOCK) * factor[:, :, None]
+        v = a.reshape(hi - lo, K) @ b.reshape(N, K).t()
+        out[lo:hi] = v[:, :F] * torch.sigmoid(v[:, :F]) * v[:, F:] if c["swiglu"] else v
+    return out
+
+
+def _exact_combine(s, c):
+    T, k, H = c["tokens"], c["k"], c["features"]
+    y = torch.zeros(T, H, dtype=torch.float64, device=DEV)
+    drows = torch.zeros(T * k, H, dtype=torch.float64, device=DEV) if c["backward"] else None
+    dweights = torch.zeros(T, k, dtype=torch.float64, device=DEV) if c["backward"] else None
+    for j in range(k):
+        t = torch.nonzero(s["slots"][:, j] >= 0).flatten()
+        r = s["slots"][t, j].long()
+        e, w = s["rows"][r].double(), s["weights"][t, j].double()[:, None]
+        y[t] += w * e
+        if c["backward"]:
+            drows[r] = w * s["dy"][t].double()
+            dweights[t, j] = (s["dy"][t].double() * e).sum(dim=1)
+    return (y, drows, dweights) if c["backward"] else y
+
+
+_EXACT = {"route": _exact_route, "dispatch": _exact_dispatch, "product": _exact_product, "combine": _exact_combine}
