@@ -85,7 +85,7 @@ def draw(rng):
                     features=features, swiglu=swiglu, skew=rng.choice([0.0, 0.5, 1.0]))
     k = rng.choice([1, 2, 4, 6, 8])
     features = rng.choice([128, 512, 1000, 1280, 2048, 2056, 4096, 5120])
-    most = max(1, 8192 * 8 * 4096 // (k * features))
+    most = max(1, 8192 * 9 * 4096 // ((k + 1) * features))
     case = dict(op=op, tokens=_between(rng, 1, min(16384, most)), k=k, features=features, dropped=rng.choice([0.0, 0.0, 0.125, 0.5]))
     if op == "dispatch":
         return dict(case, experts=rng.choice([8, 16, 64, 100, 256]), copy=rng.random() < 0.5)
