@@ -17,6 +17,14 @@ from .binding import (  # noqa: F401
     gemm_1x128_128x128,
     gemm_1x128_128x128_grouped,
     gemm_1x128_128x128_noalloc,
+    gemm_1x128_128x128_routed,
+    moe_combine,
+    moe_combine_backward,
+    moe_dispatch,
+    moe_plan,
+    moe_plan_workspace,
+    moe_route,
+    moe_route_backward,
     quantize_lhs,
     quantize_lhs_and_rhs,
     quantize_lhs_and_weight,

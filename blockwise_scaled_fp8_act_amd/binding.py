@@ -16,6 +16,7 @@ Tensor conventions (torch, on the GPU):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -26,6 +27,8 @@ BLOCK = 128
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
+_i32 = ctypes.c_int
+_f32 = ctypes.c_float
 
 _lib = None
 
@@ -65,6 +68,16 @@ def lib():
         L.quantize_rhs_grouped_fnuz.argtypes = L.quantize_rhs_grouped.argtypes
         L.quantize_lhs_and_weight.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
                                               _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+        L.moe_route.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i32, _f32, _vp, _vp, _vp]
+        L.moe_route_backward.argtypes = [_vp, _i32, _i64, _i64, _i64, _i32, _i64, _i32, _f32, _vp, _vp, _vp, _i64, _vp]
+        L.moe_plan_workspace.argtypes = [_i64, _i64, _i64]
+        L.moe_plan_workspace.restype = _i64
+        L.moe_plan.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp]
+        L.moe_dispatch.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
+        L.moe_combine.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp]
+        L.moe_combine_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]
+        L.gemm_1x128_128x128_routed.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
+                                                _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i32, _vp]
         for f in ("quantize_lhs", "quantize_rhs", "quantize_weight_128x128", "gemm_1x128_128x128",
                   "gemm_1x128_128x1", "quantize_lhs_and_rhs", "encode_e4m3_f32",
                   "quantize_lhs_and_weight"):
@@ -77,7 +90,8 @@ def lib():
                   "quantize_lhs_fnuz", "quantize_rhs_fnuz", "quantize_weight_128x128_fnuz",
                   "gemm_1x128_128x128_fnuz", "gemm_1x128_128x1_fnuz", "encode_e4m3fnuz_f32",
                   "quantize_lhs_and_rhs_fnuz", "quantize_lhs_and_weight",
-                  "quantize_lhs_and_weight_fnuz"):
+                  "quantize_lhs_and_weight_fnuz", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch",
+                  "moe_combine", "moe_combine_backward", "gemm_1x128_128x128_routed"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -505,3 +519,249 @@ def quantize_rhs_grouped(x, offsets, E, qT=None, s=None, padded_offsets=None, st
     _call(_entry("quantize_rhs_grouped", fmt), _ptr(x), T, N, _ld(x), _ptr(offsets), E, _ptr(qT), _ld(qT),
           _ptr(s), _ptr(padded_offsets), _stream(stream))
     return qT, s, padded_offsets
+
+
+# ---------------------------------------------------------------- mixture of experts
+MAX_EXPERTS = 1024
+MAX_CHOICES = 64
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream``: its memory belongs to that stream, so it is neither taken
+    from, nor given back to, work that another stream has pending."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _choices(name, t, dtype):
+    """A contiguous [T, k] tensor of ``dtype`` with 1 <= k <= MAX_CHOICES; returns (T, k)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 2 or not 1 <= t.shape[1] <= MAX_CHOICES:
+        raise ValueError(f"{name} must be [T, k] with 1 <= k <= {MAX_CHOICES}, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() >= 2 ** 31:
+        raise ValueError(f"{name} has {t.numel()} pairs, at most 2^31 - 1 are numbered")
+    return t.shape
+
+
+def _route_args(logits, k, score, scale):
+    T, E = _matrix("logits", logits, tuple(_LOGITS)).shape
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"logits has {E} experts, expected 1 to {MAX_EXPERTS}")
+    if not 1 <= k <= min(E, MAX_CHOICES):
+        raise ValueError(f"k = {k} must lie in [1, min(E, {MAX_CHOICES})] = [1, {min(E, MAX_CHOICES)}]")
+    if score not in _SCORES:
+        raise ValueError(f"unsupported score {score!r}: expected one of {tuple(_SCORES)}")
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    return T, E
+
+
+def moe_route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, renormalize=True, scale=1.0,
+              weights=None, ids=None, stream=None):
+    """The k chosen experts of every row of router logits [T, E] (bf16 or fp32) and their weights.
+    Experts are chosen by score + bias (the bias [E] fp32 takes part in the choice only), from the
+    ``top_groups`` best of ``groups`` groups of consecutive experts; equal keys go to the lower index.
+    Returns (weights [T, k] fp32, ids [T, k] int32), largest key first; a choice that finds no expert
+    (logits of -inf) has id -1 and weight 0, a row with NaN has ids -1 and weights NaN."""
+    T, E = _route_args(logits, k, score, scale)
+    if groups < 1 or E % groups != 0 or not 1 <= top_groups <= groups or k > top_groups * (E // groups):
+        raise ValueError(f"groups = {groups} must divide E = {E}, 1 <= top_groups = {top_groups} <= groups, and the "
+                         f"kept groups must hold k = {k} experts")
+    if bias is not None:
+        _dense("bias", bias, torch.float32, (E,))
+    if weights is None:
+        weights = _empty((T, k), torch.float32, logits.device, stream)
+    if ids is None:
+        ids = _empty((T, k), torch.int32, logits.device, stream)
+    _dense("weights", weights, torch.float32, (T, k))
+    _dense("ids", ids, torch.int32, (T, k))
+    _gpu(logits=logits, bias=bias, weights=weights, ids=ids)
+    _call("moe_route", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _ptr(bias), _SCORES[score], k,
+          groups, top_groups, int(bool(renormalize)), scale, _ptr(weights), _ptr(ids), _stream(stream))
+    return weights, ids
+
+
+def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True, scale=1.0, dlogits=None, stream=None):
+    """The gradient of moe_route's weights with respect to the logits, from the ids it chose and the
+    weights' gradient [T, k] fp32. Returns dlogits [T, E] in the logits' type."""
+    T, k = _choices("ids", ids, torch.int32)
+    _, E = _route_args(logits, k, score, scale)
+    if logits.shape[0] != T:
+        raise ValueError(f"logits has {logits.shape[0]} rows, ids {T}")
+    _dense("dweights", dweights, torch.float32, (T, k))
+    if dlogits is None:
+        dlogits = _empty((T, E), logits.dtype, logits.device, stream)
+    _matrix("dlogits", dlogits, (logits.dtype,), (T, E))
+    _gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+    _call("moe_route_backward", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _SCORES[score], k,
+          int(bool(renormalize)), scale, _ptr(ids), _ptr(dweights), _ptr(dlogits), _row_stride(dlogits),
+          _stream(stream))
+    return dlogits
+
+
+def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream=None):
+    """The (token, choice) pairs of ids [T, k] int32 sorted by expert, in order of the pair inside an
+    expert; ids outside [0, E) are dropped. Returns (offsets [E + 1] int64, the boundaries the grouped
+    GEMMs take; slots [T, k] int32, each pair's row, or -1 - r for a dropped pair with padding row r;
+    rows [T k] int32, each row's pair t * k + j, -1 for a padding row). ``workspace``: a uint8 tensor of
+    moe_plan_workspace(T, k, E) bytes that calls in a row may share."""
+    T, k = _choices("ids", ids, torch.int32)
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"E = {E} must lie in [1, {MAX_EXPERTS}]")
+    if offsets is None:
+        offsets = _empty((E + 1,), torch.int64, ids.device, stream)
+    if slots is None:
+        slots = _empty((T, k), torch.int32, ids.device, stream)
+    if rows is None:
+        rows = _empty((T * k,), torch.int32, ids.device, stream)
+    need = moe_plan_workspace(T, k, E)
+    if workspace is None and need > 0:
+        workspace = _empty((need,), torch.uint8, ids.device, stream)
+    _dense("offsets", offsets, torch.int64, (E + 1,))
+    _dense("slots", slots, torch.int32, (T, k))
+    _dense("rows", rows, torch.int32, (T * k,))
+    size = 0
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous uint8 tensor")
+        size = workspace.numel()
+        if size < need:
+            raise ValueError(f"workspace holds {size} bytes, the plan needs {need}")
+    _gpu(ids=ids, offsets=offsets, slots=slots, rows=rows, workspace=workspace)
+    _call("moe_plan", _ptr(ids), T, k, E, _ptr(offsets), _ptr(slots), _ptr(rows), _ptr(workspace), size,
+          _stream(stream))
+    return offsets, slots, rows
+
+
+def moe_plan_workspace(T, k, E):
+    """Bytes of device memory moe_plan needs for T tokens, k choices and E experts."""
+    need = lib().moe_plan_workspace(T, k, E)
+    if need < 0:
+        raise ValueError(f"no plan for T = {T}, k = {k}, E = {E}")
+    return need
+
+
+def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=None):
+    """x [T, H] bf16 in the row order of a plan's slots [T, k], quantized in 1x128 groups. Returns
+    (q [T k, H] uint8, a_s (ceil(H/128), T k) fp32, copy [T k, H] bf16 or None); rows of dropped pairs
+    are zero."""
+    T, k = _choices("slots", slots, torch.int32)
+    H = _matrix("x", x, _BF16, (T, None)).shape[1]
+    R = T * k
+    if q is None:
+        q = _empty((R, H), torch.uint8, x.device, stream)
+    if a_s is None:
+        a_s = _empty((cdiv(H, BLOCK), R), torch.float32, x.device, stream)
+    if copy is None and want_copy:
+        copy = _empty((R, H), torch.bfloat16, x.device, stream)
+    _codes("q", q, "e4m3fn", (R, H))
+    _dense("a_s", a_s, torch.float32, (cdiv(H, BLOCK), R))
+    if copy is not None:
+        _matrix("copy", copy, _BF16, (R, H))
+    _gpu(x=x, slots=slots, q=q, a_s=a_s, copy=copy)
+    _call("moe_dispatch", _ptr(x), T, H, _row_stride(x), _ptr(slots), k, _ptr(q), _row_stride(q), _ptr(a_s), _ptr(copy),
+          _row_stride(copy) if copy is not None else 0, _stream(stream))
+    return q, a_s, copy
+
+
+def moe_combine(rows, slots, weights=None, y=None, stream=None):
+    """y[t] = sum over j of weights[t, j] * rows[slots[t, j]] (rows [R, H] bf16, weights fp32 or None for
+    1), in fp32 with one rounding. Returns y [T, H] bf16."""
+    T, k = _choices("slots", slots, torch.int32)
+    R, H = _matrix("rows", rows, _BF16).shape
+    if weights is not None:
+        _dense("weights", weights, torch.float32, (T, k))
+    if y is None:
+        y = _empty((T, H), torch.bfloat16, rows.device, stream)
+    _matrix("y", y, _BF16, (T, H))
+    _gpu(rows=rows, slots=slots, weights=weights, y=y)
+    _call("moe_combine", _ptr(rows), R, _row_stride(rows), _ptr(slots), _ptr(weights), T, k, H, _ptr(y), _row_stride(y),
+          _stream(stream))
+    return y
+
+
+def moe_combine_backward(dy, rows, slots, weights, drows=None, dweights=None, stream=None):
+    """Gradients of moe_combine: returns (drows [T k, H] bf16, weights * dy in row order, zero for
+    padding rows; dweights [T, k] fp32)."""
+    T, k = _choices("slots", slots, torch.int32)
+    H = _matrix("dy", dy, _BF16, (T, None)).shape[1]
+    R = T * k
+    _matrix("rows", rows, _BF16, (R, H))
+    _dense("weights", weights, torch.float32, (T, k))
+    if drows is None:
+        drows = _empty((R, H), torch.bfloat16, dy.device, stream)
+    if dweights is None:
+        dweights = _empty((T, k), torch.float32, dy.device, stream)
+    _matrix("drows", drows, _BF16, (R, H))
+    _dense("dweights", dweights, torch.float32, (T, k))
+    _gpu(dy=dy, rows=rows, slots=slots, weights=weights, drows=drows, dweights=dweights)
+    _call("moe_combine_backward", _ptr(dy), _row_stride(dy), _ptr(rows), _row_stride(rows), _ptr(slots), _ptr(weights), T, k,
+          H, _ptr(drows), _row_stride(drows), _ptr(dweights), _stream(stream))
+    return drows, dweights
+
+
+def _row_stride(t):
+    """Row stride of a matrix that _matrix has passed (a stride no row uses counts as the row's length)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, bs_stride_nb, bs_stride_kb, ldb=None,
+                              rows=None, k=1, swiglu=False, c=None, N=None, stream=None):
+    """gemm_1x128_128x128_grouped for few rows an expert. ``rows``: a moe_plan's rows [M] int32, and row
+    r of C multiplies A's row rows[r] // k (its token); None: row r of A. ``swiglu``: B_e holds N gate
+    rows, then N up rows, and C = silu(gate) * up. N defaults to the output columns of the experts'
+    rows stacked in b ([E * N, K], or [E * 2 N, K] with swiglu). Returns c [M, N] bf16."""
+    A, K = _codes("a", a, "e4m3fn").shape
+    _codes("b", b, "e4m3fn")
+    if E < 0 or E > MAX_EXPERTS:
+        raise ValueError(f"E = {E} must lie in [0, {MAX_EXPERTS}]")
+    if K == 0 or K % BLOCK != 0:
+        raise ValueError(f"a has {K} columns, expected a positive multiple of {BLOCK}")
+    if rows is not None:
+        if not isinstance(rows, torch.Tensor) or rows.dtype != torch.int32:
+            raise TypeError("rows must be an int32 tensor")
+        if rows.dim() != 1 or not rows.is_contiguous():
+            raise ValueError("rows must be a contiguous 1-D tensor")
+        if not 1 <= k <= MAX_CHOICES:
+            raise ValueError(f"k = {k} must lie in [1, {MAX_CHOICES}]")
+    M = A if rows is None else rows.numel()
+    if ldb is None:
+        ldb = _row_stride(b)
+    halves = 2 if swiglu else 1
+    if N is None:
+        N = b.shape[0] // max(E, 1) // halves
+    if swiglu and N % BLOCK != 0:
+        raise ValueError(f"N = {N} must be a multiple of {BLOCK} with swiglu")
+    if min(ldb, b_stride, bs_stride, bs_stride_nb, bs_stride_kb, N) < 0:
+        raise ValueError("strides and N must be >= 0")
+    if c is None:
+        c = _empty((M, N), torch.bfloat16, a.device, stream)
+    _dense("a_s", a_s, torch.float32, (cdiv(K, BLOCK), A))
+    if not isinstance(b_s, torch.Tensor) or b_s.dtype != torch.float32 or not b_s.is_contiguous():
+        raise TypeError("b_s must be a contiguous float32 tensor")
+    _offsets(offsets, E)
+    _matrix("c", c, (torch.bfloat16,), (M, N))
+    if E > 0 and M > 0 and N > 0:
+        need = (E - 1) * b_stride + (halves * N - 1) * ldb + K
+        have = b.untyped_storage().nbytes() - b.storage_offset()
+        if need > have:
+            raise ValueError(f"b holds {have} bytes, E, N, K and the strides read {need}")
+        need = (E - 1) * bs_stride + (cdiv(halves * N, BLOCK) - 1) * bs_stride_nb + (K // BLOCK - 1) * bs_stride_kb + 1
+        if need > b_s.numel():
+            raise ValueError(f"b_s holds {b_s.numel()} floats, E, N, K and the strides read {need}")
+    _gpu(a=a, a_s=a_s, b=b, b_s=b_s, offsets=offsets, rows=rows, c=c)
+    _call("gemm_1x128_128x128_routed", _ptr(a), _row_stride(a), _ptr(a_s), A, _ptr(rows), k, _ptr(b), ldb, b_stride,
+          _ptr(b_s), bs_stride, bs_stride_nb, bs_stride_kb, _ptr(offsets), E, _ptr(c), _row_stride(c), M, N, K,
+          int(bool(swiglu)), _stream(stream))
+    return c

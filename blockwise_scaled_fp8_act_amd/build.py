@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libbsfp8.so")
 
-SOURCES = ["capi.cpp", "quantize.hip", "gemm.hip"]
+SOURCES = ["capi.cpp", "quantize.hip", "gemm.hip", "moe.hip", "gemm_routed.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

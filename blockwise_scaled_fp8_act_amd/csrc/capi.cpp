@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -326,6 +327,23 @@ int gemm_128x1_impl(const void* a, int64_t lda, const float* a_s, const void* b,
     return run_gemm(a, lda, a_s, b, ldb, bs, c, ldc, M, N, K, fnuz, use_scratch, static_cast<hipStream_t>(stream));
 }
 
+// Limits of the mixture-of-experts entry points: one lane holds a choice, and the experts of a row
+// (of a bin) fit a wave's registers (a workgroup's LDS).
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxChoices = 64;
+constexpr int64_t kMaxPairs = 0x7FFFFFFF;
+
+// The pairs of T tokens with k choices each are numbered in 32 bits.
+bool pairs_ok(int64_t T, int64_t k) { return T >= 0 && k >= 1 && k <= kMaxChoices && T <= kMaxPairs / k; }
+
+int validate_route(int dtype, int64_t T, int64_t E, int64_t ld, int score, int64_t k, float scale) {
+    if (!pairs_ok(T, k) || E < 1 || E > kMaxExperts || k > E) return BSFP8_EINVAL;
+    if ((dtype != BSFP8_BF16 && dtype != BSFP8_F32) || (score != BSFP8_SOFTMAX && score != BSFP8_SIGMOID))
+        return BSFP8_EINVAL;
+    if (ld < E || !std::isfinite(scale)) return BSFP8_EINVAL;
+    return BSFP8_OK;
+}
+
 int encode_impl(const float* x, void* q, int64_t n, bool fnuz, void* stream) {
     if (n < 0) return BSFP8_EINVAL;
     if (n == 0) return BSFP8_OK;
@@ -498,6 +516,113 @@ int encode_e4m3_f32(const float* x, void* q, int64_t n, void* stream) {
 
 int encode_e4m3fnuz_f32(const float* x, void* q, int64_t n, void* stream) {
     return encode_impl(x, q, n, true, stream);
+}
+
+int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int score,
+              int64_t k, int64_t groups, int64_t top_groups, int renormalize, float scale, float* weights,
+              int32_t* ids, void* stream) {
+    if (int rc = validate_route(dtype, T, E, ld, score, k, scale)) return rc;
+    if (groups < 1 || E % groups != 0 || top_groups < 1 || top_groups > groups || k > top_groups * (E / groups))
+        return BSFP8_EINVAL;
+    if (T == 0) return BSFP8_OK;
+    if (logits == nullptr || weights == nullptr || ids == nullptr) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::RouteRule rule{score == BSFP8_SOFTMAX, static_cast<int>(k), static_cast<int>(groups),
+                                static_cast<int>(top_groups), renormalize != 0, scale};
+    return finish(bsfp8::launch_route(logits, dtype == BSFP8_F32, T, static_cast<int>(E), ld, rule, bias, weights, ids,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int score, int64_t k,
+                       int renormalize, float scale, const int32_t* ids, const float* dweights, void* dlogits,
+                       int64_t lddl, void* stream) {
+    if (int rc = validate_route(dtype, T, E, ld, score, k, scale)) return rc;
+    if (lddl < E) return BSFP8_EINVAL;
+    if (T == 0) return BSFP8_OK;
+    if (logits == nullptr || ids == nullptr || dweights == nullptr || dlogits == nullptr) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::RouteRule rule{score == BSFP8_SOFTMAX, static_cast<int>(k), 1, 1, renormalize != 0, scale};
+    return finish(bsfp8::launch_route_backward(logits, dtype == BSFP8_F32, T, static_cast<int>(E), ld, rule, ids,
+                                               dweights, dlogits, lddl, static_cast<hipStream_t>(stream)));
+}
+
+int64_t moe_plan_workspace(int64_t T, int64_t k, int64_t E) {
+    if (!pairs_ok(T, k) || E < 1 || E > kMaxExperts) return -1;
+    const int64_t blocks = bsfp8::sched::plan_blocks(T * k);
+    return blocks > 1 ? blocks * (E + 1) * static_cast<int64_t>(sizeof(int32_t)) : 0;
+}
+
+int moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t* offsets, int32_t* slots, int32_t* rows,
+             void* workspace, int64_t workspace_bytes, void* stream) {
+    const int64_t need = moe_plan_workspace(T, k, E);
+    if (need < 0 || offsets == nullptr) return BSFP8_EINVAL;
+    if (T > 0 && (ids == nullptr || slots == nullptr || rows == nullptr)) return BSFP8_EINVAL;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BSFP8_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 3) != 0) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_plan(ids, T * k, static_cast<int>(E), offsets, slots, rows,
+                                     static_cast<int32_t*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+int moe_dispatch(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int64_t k, void* q, int64_t ldq,
+                 float* a_s, void* copy, int64_t ldcopy, void* stream) {
+    if (!pairs_ok(T, k) || H < 0) return BSFP8_EINVAL;
+    if (T == 0 || H == 0) return BSFP8_OK;
+    if (x == nullptr || slots == nullptr || q == nullptr || a_s == nullptr) return BSFP8_EINVAL;
+    if (ldx < H || ldq < H || (copy != nullptr && ldcopy < H)) return BSFP8_EINVAL;
+    if (cdiv(H, 1024) > 0x7FFFFFFFLL / T) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_dispatch(static_cast<const uint16_t*>(x), T, H, ldx, slots, static_cast<int>(k),
+                                         static_cast<uint8_t*>(q), ldq, a_s, static_cast<uint16_t*>(copy), ldcopy,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine(const void* rows, int64_t R, int64_t ldr, const int32_t* slots, const float* weights, int64_t T,
+                int64_t k, int64_t H, void* y, int64_t ldy, void* stream) {
+    if (!pairs_ok(T, k) || H < 0 || R < 0) return BSFP8_EINVAL;
+    if (T == 0 || H == 0) return BSFP8_OK;
+    if ((rows == nullptr && R > 0) || slots == nullptr || y == nullptr) return BSFP8_EINVAL;
+    if (ldr < H || ldy < H || cdiv(H, 512) > 0x7FFFFFFFLL / T) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_combine(static_cast<const uint16_t*>(rows), R, ldr, slots, weights, T,
+                                        static_cast<int>(k), H, static_cast<uint16_t*>(y), ldy,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t ldr, const int32_t* slots,
+                         const float* weights, int64_t T, int64_t k, int64_t H, void* drows, int64_t lddr,
+                         float* dweights, void* stream) {
+    if (!pairs_ok(T, k) || H < 0) return BSFP8_EINVAL;
+    if (T == 0) return BSFP8_OK;
+    if (slots == nullptr || weights == nullptr || dweights == nullptr) return BSFP8_EINVAL;
+    if (H > 0 && (dy == nullptr || rows == nullptr || drows == nullptr)) return BSFP8_EINVAL;
+    if (lddy < H || ldr < H || lddr < H) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_combine_backward(
+        static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(rows), ldr, slots, weights, T,
+        static_cast<int>(k), H, static_cast<uint16_t*>(drows), lddr, dweights, static_cast<hipStream_t>(stream)));
+}
+
+int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int64_t a_rows, const int32_t* rows,
+                              int64_t k, const void* b, int64_t ldb, int64_t b_stride, const float* b_s,
+                              int64_t bs_stride, int64_t bs_stride_nb, int64_t bs_stride_kb, const int64_t* offsets,
+                              int64_t E, void* c, int64_t ldc, int64_t M, int64_t N, int64_t K, int swiglu,
+                              void* stream) {
+    if (E < 0 || M < 0 || N < 0 || K < 0 || a_rows < 0) return BSFP8_EINVAL;
+    if (E == 0 || M == 0 || N == 0) return BSFP8_OK;
+    if (K == 0 || K % kGroupEdge != 0 || (swiglu != 0 && N % kGroupEdge != 0)) return BSFP8_EINVAL;
+    if (a == nullptr || a_s == nullptr || b == nullptr || b_s == nullptr || offsets == nullptr || c == nullptr)
+        return BSFP8_EINVAL;
+    if (E > kMaxExperts || M > kMaxPairs || a_rows < 1 || k < 1 || k > kMaxChoices) return BSFP8_EINVAL;
+    if (rows == nullptr && a_rows < M) return BSFP8_EINVAL;
+    if (lda < K || ldb < K || ldc < N || b_stride < 0 || bs_stride < 0 || bs_stride_nb < 0 || bs_stride_kb < 0)
+        return BSFP8_EINVAL;
+    if (!aligned16(a) || !aligned16(b) || lda % 16 != 0 || ldb % 16 != 0 || b_stride % 16 != 0) return BSFP8_EALIGN;
+    if (int rc = check_device()) return rc;
+    const bsfp8::RoutedArgs args{static_cast<const uint8_t*>(a), lda, a_s, a_rows, rows, k,
+                                 static_cast<const uint8_t*>(b), ldb, b_stride, b_s, bs_stride, bs_stride_nb,
+                                 bs_stride_kb, offsets, E, static_cast<uint16_t*>(c), ldc, M, N, K, 0, 0};
+    return finish(bsfp8::launch_gemm_routed(args, swiglu != 0, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -71,4 +71,49 @@ hipError_t launch_gemm_grouped_k(const uint8_t* a, int64_t lda, const float* a_s
                                  uint16_t* c, int64_t ldc, int64_t c_stride, int64_t M, int64_t N,
                                  int64_t K, int32_t* status, hipStream_t stream);
 
+// Routing of a mixture-of-experts layer (moe.hip); the rule's fields as in moe_route.
+struct RouteRule {
+    bool softmax;
+    int k, groups, top_groups;
+    bool renormalize;
+    float scale;
+};
+hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int64_t ld, const RouteRule& r, const float* bias,
+                        float* weights, int32_t* ids, hipStream_t stream);
+hipError_t launch_route_backward(const void* logits, bool f32, int64_t T, int E, int64_t ld, const RouteRule& r,
+                                 const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd,
+                                 hipStream_t stream);
+// workspace: sched::plan_blocks(P) * (E + 1) int32 when plan_blocks(P) > 1, else unused
+hipError_t launch_plan(const int32_t* ids, int64_t P, int E, int64_t* offsets, int32_t* slots, int32_t* rows,
+                       int32_t* workspace, hipStream_t stream);
+hipError_t launch_dispatch(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int k, uint8_t* q,
+                           int64_t ldq, float* a_s, uint16_t* copy, int64_t ldcopy, hipStream_t stream);
+hipError_t launch_combine(const uint16_t* rows, int64_t R, int64_t ldr, const int32_t* slots, const float* weights,
+                          int64_t T, int k, int64_t H, uint16_t* y, int64_t ldy, hipStream_t stream);
+hipError_t launch_combine_backward(const uint16_t* dy, int64_t lddy, const uint16_t* rows, int64_t ldr,
+                                   const int32_t* slots, const float* weights, int64_t T, int k, int64_t H,
+                                   uint16_t* drows, int64_t lddr, float* dweights, hipStream_t stream);
+
+// Expert products for few rows an expert (gemm_routed.hip). N: output columns (with swiglu B_e has
+// 2 N rows). col_tiles and c_vec are set by the launcher.
+struct RoutedArgs {
+    const uint8_t* a;
+    int64_t lda;
+    const float* a_s;
+    int64_t a_rows;
+    const int32_t* rows;  // nullptr: row r of C reads row r of A
+    int64_t k;
+    const uint8_t* b;
+    int64_t ldb, b_stride;
+    const float* b_s;
+    int64_t bs_stride, bs_nb, bs_kb;
+    const int64_t* offsets;
+    int64_t E;
+    uint16_t* c;
+    int64_t ldc, M, N, K;
+    int64_t col_tiles;
+    int c_vec;
+};
+hipError_t launch_gemm_routed(RoutedArgs a, bool swiglu, hipStream_t stream);
+
 }  // namespace bsfp8

@@ -242,4 +242,30 @@ inline ColumnSplit gemm_column_split(int64_t M, int64_t N, int64_t K, int cus, i
     return ColumnSplit{n1, tail};
 }
 
+namespace sched {
+
+// Workgroups of the plan's counting sort and the pairs each takes (a multiple of 512: eight waves of
+// whole 64-pair steps): one workgroup and no counting pass up to 4096 pairs, else at most 512 of at
+// least 2048 pairs.
+inline int64_t plan_segment(int64_t P) {
+    if (P <= 4096) return cdiv(P > 0 ? P : 1, 512) * 512;
+    const int64_t per = cdiv(P, 512);
+    return cdiv(per < 2048 ? 2048 : per, 512) * 512;
+}
+inline int64_t plan_blocks(int64_t P) { return P > 0 ? cdiv(P, plan_segment(P)) : 1; }
+
+// Row tiles of tm rows that any boundaries can give: sum over the experts that have rows of
+// ceil(rows / tm), at most (M - n) / tm + n with n of them, n <= min(E, M).
+inline int64_t routed_row_tiles(int64_t M, int64_t E, int64_t tm) {
+    const int64_t n = E < M ? E : M;
+    return (M - n) / tm + n;
+}
+
+// 16-row subtiles of the routed product's tile: by the mean rows of the experts that can have any.
+inline int routed_subtiles(int64_t M, int64_t E) {
+    const int64_t mean = cdiv(M, E < M ? E : M);
+    return mean <= 8 ? 1 : mean <= 20 ? 2 : 4;
+}
+
+}  // namespace sched
 }  // namespace bsfp8

@@ -351,6 +351,129 @@ int quantize_rhs_grouped_fnuz(const void* x, int64_t T, int64_t N, int64_t ldx,
                               const int64_t* offsets, int64_t E,
                               void* qT, int64_t ldqT, float* s, int64_t* padded_offsets, void* stream);
 
+/*
+ * Mixture-of-experts operators around the expert-grouped GEMMs: routing, the plan that sorts the
+ * choices by expert, dispatch (gather and quantize), the experts' products for few rows, and the
+ * weighted return; routing, dispatch and return with their gradients. Shared terms:
+ *   T tokens of H features; each has k choices among E experts, 1 <= k <= 64, 1 <= E <= 1024.
+ *   pair p = t * k + j is token t's j-th choice; R = T k pairs, at most 2^31 - 1.
+ *   A dropped pair is one whose expert id lies outside [0, E) (an expert of another rank, or a
+ *   choice that could not be made).
+ * All are deterministic, allocate nothing and may be captured into a graph.
+ */
+enum { BSFP8_BF16 = 0, BSFP8_F32 = 1 };       /* type of the router's logits */
+enum { BSFP8_SOFTMAX = 0, BSFP8_SIGMOID = 1 }; /* score of an expert */
+
+/*
+ * moe_route: the k chosen experts of every token and their weights.
+ *   logits  [T, E] bf16 or fp32 (dtype), row stride ld >= E.   bias  [E] fp32 or NULL.
+ *   p_e     softmax of the row, or the sigmoid of the logit.
+ *   key_e   p_e + bias_e; without a bias the logit itself (the order of p_e).
+ *   groups  E / groups consecutive experts form a group, valued by its largest key, or with a bias by
+ *           the sum of its two largest; only the top_groups best groups are kept.
+ *   ids     [T, k] int32: the experts with the largest keys in the kept groups, largest first.
+ *   weights [T, k] fp32: scale * p of the chosen experts (without the bias); renormalize != 0: divided
+ *           by their sum (for softmax that is the softmax over the chosen logits; for sigmoid a sum
+ *           below 2^-126 counts as 2^-126).
+ * Keys are formed and compared in 64 bits; equal keys (and groups) go to the lower index. An expert
+ * whose logit is -inf, or whose bias is -inf or NaN, is never chosen; a choice that finds no expert has
+ * id -1 and weight 0. A row with a NaN logit (softmax: or +inf) has ids -1 and weights NaN.
+ * Requirements (else BSFP8_EINVAL): E a multiple of groups, 1 <= top_groups <= groups,
+ * k <= top_groups * E / groups, scale finite.
+ */
+int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int score,
+              int64_t k, int64_t groups, int64_t top_groups, int renormalize, float scale,
+              float* weights, int32_t* ids, void* stream);
+
+/*
+ * moe_route_backward: the gradient of moe_route's weights with respect to the logits (the choice
+ * itself has none). ids [T, k] as moe_route gave them (ids outside [0, E) have no gradient),
+ * dweights [T, k] fp32, dlogits [T, E] in the logits' type with row stride lddl >= E; every element is
+ * written. A row without a chosen expert has zero gradient. score, renormalize and scale as in the
+ * forward call. Sums in fp32, one rounding.
+ */
+int moe_route_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int score, int64_t k,
+                       int renormalize, float scale, const int32_t* ids, const float* dweights,
+                       void* dlogits, int64_t lddl, void* stream);
+
+/*
+ * moe_plan: the pairs sorted by expert, equal experts in order of the pair (a stable counting sort).
+ *   ids      [T, k] int32, contiguous.
+ *   offsets  [E + 1] int64, written: expert e owns the rows [offsets[e], offsets[e+1]) -- the
+ *            boundaries the grouped GEMMs and quantize_rhs_grouped take. offsets[E] is the number of
+ *            pairs that are not dropped.
+ *   slots    [T, k] int32, written: the pair's row; a dropped pair has -1 - r with r its padding row,
+ *            r >= offsets[E].
+ *   rows     [T k] int32, written: the row's pair, -1 for a padding row.
+ *   workspace  device memory of moe_plan_workspace(T, k, E) bytes (0 for small plans; -1: invalid
+ *            sizes), 4-byte aligned, not in use by another call.
+ */
+int64_t moe_plan_workspace(int64_t T, int64_t k, int64_t E);
+int moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t* offsets, int32_t* slots,
+             int32_t* rows, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * moe_dispatch: the tokens in the plan's row order, quantized in 1x128 groups.
+ *   x     [T, H] bf16, row stride ldx >= H.   slots [T, k] from moe_plan.
+ *   q     [T k, H] fp8, row stride ldq >= H, and a_s column-major [T k, ceil(H/128)] with ld T k: row
+ *         r holds exactly what quantize_lhs writes for its token; a padding row holds zeros (codes,
+ *         scales and copy), so every row is written.
+ *   copy  NULL, or [T k, H] bf16, row stride ldcopy >= H: the tokens themselves in row order (what
+ *         quantize_rhs_grouped takes for the weight gradient).
+ * Slots that name no row in [0, T k) are skipped. The gradient with respect to x is moe_combine of the
+ * copy's gradient without weights.
+ */
+int moe_dispatch(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int64_t k,
+                 void* q, int64_t ldq, float* a_s, void* copy, int64_t ldcopy, void* stream);
+
+/*
+ * moe_combine: y[t] = sum over j of weights[t, j] * rows[slots[t, j]], in fp32 in order of j, rounded
+ * to bf16 once.
+ *   rows [R, H] bf16, row stride ldr >= H;  slots [T, k];  weights [T, k] fp32 or NULL (all 1);
+ *   y [T, H] bf16, row stride ldy >= H.
+ * A slot outside [0, R) contributes its weight times 0 (so the NaN weights of a row that could not be
+ * routed show in its output).
+ */
+int moe_combine(const void* rows, int64_t R, int64_t ldr, const int32_t* slots, const float* weights,
+                int64_t T, int64_t k, int64_t H, void* y, int64_t ldy, void* stream);
+
+/*
+ * moe_combine_backward: drows[slots[t, j]] = weights[t, j] * dy[t] (bf16) and dweights[t, j] = the dot
+ * product of dy[t] and rows[slots[t, j]] (fp32).
+ *   dy [T, H], rows [T k, H], drows [T k, H] bf16 with their row strides; slots, weights, dweights [T, k].
+ * A dropped pair's padding row of drows is zero and its dweights 0, so with a moe_plan's slots every
+ * row is written.
+ */
+int moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t ldr, const int32_t* slots,
+                         const float* weights, int64_t T, int64_t k, int64_t H, void* drows, int64_t lddr,
+                         float* dweights, void* stream);
+
+/*
+ * gemm_1x128_128x128_routed: gemm_1x128_128x128_grouped for few rows an expert (a decode step): the
+ * same scaled product per expert, scheduled to stream the experts' weights once, with A read through
+ * the plan and, on request, the gate and up products of a gated layer joined.
+ *   a, lda, a_s   A [a_rows, K] fp8, a_s column-major [a_rows, K/128] with ld a_rows.
+ *   rows, k       NULL: row r of C multiplies row r of A. Else a moe_plan's rows [M] int32: row r
+ *                 multiplies A's row rows[r] / k (its token); where that is not in [0, a_rows) row r
+ *                 of C is zero.
+ *   b, ldb, b_stride, b_s, bs_stride, bs_stride_nb, bs_stride_kb, offsets, E   as in
+ *                 gemm_1x128_128x128_grouped; with swiglu != 0, B_e has 2 N rows: N gate rows, then
+ *                 N up rows.
+ *   c, ldc        C [M, N] bf16; swiglu: C = silu(gate) * up, formed in fp32 and rounded once. Rows
+ *                 outside every expert's range are not written.
+ * Requirements (else BSFP8_EINVAL): K a positive multiple of 128, N a multiple of 128 with swiglu,
+ * a_rows >= M without rows, M < 2^31; alignment as gemm_1x128_128x128 (b_stride too). The K range is
+ * summed in parts in a fixed order, so results can differ from the grouped GEMM's in the last bits
+ * and are the same on every call. Any row counts are computed; from about 128 rows an expert the
+ * grouped GEMM is the faster one.
+ */
+int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int64_t a_rows,
+                              const int32_t* rows, int64_t k,
+                              const void* b, int64_t ldb, int64_t b_stride,
+                              const float* b_s, int64_t bs_stride, int64_t bs_stride_nb, int64_t bs_stride_kb,
+                              const int64_t* offsets, int64_t E,
+                              void* c, int64_t ldc, int64_t M, int64_t N, int64_t K, int swiglu, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
