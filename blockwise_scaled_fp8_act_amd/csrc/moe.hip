@@ -46,32 +46,37 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 // ------------------------------------------------------------------------------------- routing
-// One wave a token; lane l holds the experts l, l + 64, ... . Scores and keys are in 64 bits: the
-// choice is made between values that may lie closer together than fp32 rounding, and the chosen
-// experts are whole numbers, so the comparison must not depend on how a score was rounded.
-template <typename LT, int V>
-__global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, int64_t T, int E, int64_t ld,
-                                                            const float* bias, int softmax, int k, int groups,
-                                                            int top_groups, int renormalize, float scale,
-                                                            float* weights, int32_t* ids) {
-    extern __shared__ double lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
-    if (t >= T) return;
-    const LT* row = logits + t * ld;
+// Scores and keys that decide a choice are compared in 64 bits: the choice is made between values
+// that may lie closer together than fp32 rounding, and its results are whole numbers.
+struct RouteArgs {
+    int64_t T;
+    int E;
+    int64_t ld;
+    const float* bias;
+    int softmax, k, groups, top_groups, renormalize;
+    float scale;
+    float* weights;
+    int32_t* ids;
+    int vec, bias_vec;  // rows of the logits, the bias are 16-byte aligned
+};
 
+// One token, by a whole wave, everything in 64 bits; lane l holds the experts l, l + 64, ... . `lds`:
+// E + groups doubles of this wave's own when groups > 1.
+template <typename LT, int V>
+__device__ __forceinline__ void route_token(const LT* row, int64_t t, const RouteArgs& a, double* lds, int lane) {
+    const int E = a.E, k = a.k;
     float z[V];
     bool bad = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = v * 64 + lane;
         z[v] = e < E ? load_logit(row + e) : -INFINITY;
-        bad = bad || z[v] != z[v] || (softmax && z[v] == INFINITY);
+        bad = bad || z[v] != z[v] || (a.softmax && z[v] == INFINITY);
     }
     if (__any(bad)) {  // no probabilities: no expert, NaN weights
         if (lane < k) {
-            weights[t * k + lane] = NAN;
-            ids[t * k + lane] = -1;
+            a.weights[t * k + lane] = NAN;
+            a.ids[t * k + lane] = -1;
         }
         return;
     }
@@ -80,47 +85,42 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, in
     for (int v = 1; v < V; ++v) top = fmaxf(top, z[v]);
     top = wave_max(top);
     double total = 1.0;
-    if (softmax && (bias != nullptr || !renormalize)) {
+    if (a.softmax && (a.bias != nullptr || !a.renormalize)) {
         total = 0.0;
 #pragma unroll
         for (int v = 0; v < V; ++v) total += z[v] == -INFINITY ? 0.0 : exp(static_cast<double>(z[v]) - top);
         total = wave_sum(total);
     }
     const auto score = [&](float x) -> double {
-        return softmax ? exp(static_cast<double>(x) - top) / total : 1.0 / (1.0 + exp(-static_cast<double>(x)));
+        return a.softmax ? exp(static_cast<double>(x) - top) / total : 1.0 / (1.0 + exp(-static_cast<double>(x)));
     };
     double key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = v * 64 + lane;
         key[v] = z[v];
-        if (bias != nullptr && z[v] != -INFINITY) {
-            key[v] = score(z[v]) + static_cast<double>(bias[e]);
+        if (a.bias != nullptr && z[v] != -INFINITY) {
+            key[v] = score(z[v]) + static_cast<double>(a.bias[e]);
             if (key[v] != key[v]) key[v] = -INFINITY;  // a NaN bias takes its expert out
         }
     }
 
-    if (groups > 1) {
+    if (a.groups > 1) {
         // keys to LDS; lane g values the groups g, g + 64, ... and ranks them
-        double* mine = lds + static_cast<int64_t>(wave) * (E + groups);
-        double* value = mine + E;
+        double* value = lds + E;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (v * 64 + lane < E) mine[v * 64 + lane] = key[v];
+            if (v * 64 + lane < E) lds[v * 64 + lane] = key[v];
         wave_lds_fence();
-        const int size = E / groups;
-        for (int g = lane; g < groups; g += 64) {
-            double a = -INFINITY, b = -INFINITY;  // the two largest keys
+        const int size = E / a.groups;
+        for (int g = lane; g < a.groups; g += 64) {
+            double first = -INFINITY, second = -INFINITY;  // the two largest keys
             for (int i = 0; i < size; ++i) {
-                const double x = mine[g * size + i];
-                if (x > a) {
-                    b = a;
-                    a = x;
-                } else if (x > b) {
-                    b = x;
-                }
+                const double x = lds[g * size + i];
+                second = fmax(second, fmin(first, x));
+                first = fmax(first, x);
             }
-            value[g] = bias != nullptr && b != -INFINITY ? a + b : a;
+            value[g] = a.bias != nullptr && second != -INFINITY ? first + second : first;
         }
         wave_lds_fence();
 #pragma unroll
@@ -130,9 +130,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, in
             const int g = e / size;
             const double x = value[g];
             int rank = 0;
-            for (int i = 0; i < groups; ++i) rank += value[i] > x || (value[i] == x && i < g) ? 1 : 0;
-            if (rank >= top_groups) key[v] = -INFINITY;
+            for (int i = 0; i < a.groups; ++i) rank += value[i] > x || (value[i] == x && i < g) ? 1 : 0;
+            if (rank >= a.top_groups) key[v] = -INFINITY;
         }
+        wave_lds_fence();
     }
 
     int id = -1;  // lane j: the j-th choice
@@ -163,17 +164,447 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, in
 
     const float zc = id >= 0 ? load_logit(row + id) : -INFINITY;
     double w = 0.0;
-    if (softmax && renormalize) {  // softmax over the chosen logits: the row's own sum cancels
+    if (a.softmax && a.renormalize) {  // softmax over the chosen logits: the row's own sum cancels
         const float ztop = wave_max(zc);
         const double x = id >= 0 ? exp(static_cast<double>(zc) - ztop) : 0.0;
         w = x / wave_sum(x);
     } else {
         w = id >= 0 ? score(zc) : 0.0;
-        if (renormalize) w /= fmax(wave_sum(w), static_cast<double>(kSumFloor));
+        const double sum = wave_sum(w);
+        if (a.renormalize) w /= fmax(sum, static_cast<double>(kSumFloor));
     }
     if (lane < k) {
-        weights[t * k + lane] = id >= 0 ? static_cast<float>(scale * w) : 0.0f;
-        ids[t * k + lane] = id;
+        a.weights[t * k + lane] = id >= 0 ? static_cast<float>(a.scale * w) : 0.0f;
+        a.ids[t * k + lane] = id;
+    }
+}
+
+// Every rule the kernel below does not take: more than 16 choices, softmax scores with a bias, more
+// groups than its lanes. One wave a token.
+template <typename LT, int V>
+__global__ __launch_bounds__(64 * kWaves) void route_wide_kernel(const LT* logits, RouteArgs a) {
+    extern __shared__ double lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
+    if (t >= a.T) return;
+    route_token<LT, V>(logits + t * a.ld, t, a, lds + static_cast<int64_t>(wave) * (a.E + a.groups), lane);
+}
+
+// fp32 as an unsigned number of the same order, and back.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+constexpr uint32_t kLeastKey = 0x00800000u;  // below: -inf (and the packed 0 of a taken or missing expert)
+
+template <int L>
+__device__ __forceinline__ uint32_t team_umax(uint32_t v) {
+    v = umax_row16(v);
+    if (L == 64) {
+        auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = max(r[0], r[1]);
+        r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max(r[0], r[1]);
+    }
+    return v;
+}
+
+// Sum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ float sum_row16(float v) {
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0xB1, 0xF, 0xF, false));
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x4E, 0xF, 0xF, false));
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x141, 0xF, 0xF, false));
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x140, 0xF, 0xF, false));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float team_sum(float v) {
+    v = sum_row16(v);
+    if (L == 64) {
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+    }
+    return v;
+}
+
+// How many of the other 15 lanes of the row come before this one: a larger key, or the same and a
+// smaller index.
+template <int R = 1>
+__device__ __forceinline__ int rank_row16(double key, int idx) {
+    if constexpr (R == 16) {
+        return 0;
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, key);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), 0x120 + R, 0xF, 0xF, false);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), 0x120 + R, 0xF, 0xF, false);
+        const int oi = __builtin_amdgcn_update_dpp(0, idx, 0x120 + R, 0xF, 0xF, false);
+        const double ok = __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+        return (ok > key || (ok == key && oi < idx) ? 1 : 0) + rank_row16<R + 1>(key, idx);
+    }
+}
+
+// Descending sort of V values in registers: odd-even merge network.
+template <int V>
+__device__ __forceinline__ void sort_descending(uint32_t (&s)[V]) {
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (j + i + q < V && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+                        const uint32_t x = s[j + i], y = s[j + i + q];
+                        s[j + i] = max(x, y);
+                        s[j + i + q] = min(x, y);
+                    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_run(const float* p, bool vec, int left, float (&z)[V]) {
+    if (V % 4 == 0 && vec) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const float4 f = v < left ? *reinterpret_cast<const float4*>(p + v) : float4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            z[v] = f.x;
+            z[v + 1] = f.y;
+            z[v + 2] = f.z;
+            z[v + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = v < left ? p[v] : -INFINITY;
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_run(const uint16_t* p, bool vec, int left, float (&z)[V]) {
+    if (V % 4 == 0 && vec) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const uint2 w = v < left ? *reinterpret_cast<const uint2*>(p + v) : uint2{0xFF80FF80u, 0xFF80FF80u};
+            z[v] = bf16_lo(w.x);
+            z[v + 1] = bf16_hi(w.x);
+            z[v + 2] = bf16_lo(w.y);
+            z[v + 3] = bf16_hi(w.y);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = v < left ? bf16_to_f32(p[v]) : -INFINITY;
+    }
+}
+
+// The largest error of a sigmoid from the hardware's exp2 and reciprocal (each within one unit of the
+// last place; scores are at most 1) and of adding a bias to it.
+constexpr float kKeyError = 4.8e-7f;   // 2^-21
+constexpr float kKeyRounding = 6e-8f;  // 2^-24, of the key
+
+// L lanes a token (16, four tokens a wave, up to 256 experts; 64 up to 1024), V consecutive experts a
+// lane. Candidates come from fp32 keys cut to make room for the expert's index in the low bits: then
+// one unsigned maximum over the lanes (a DPP step each) yields key and index, and the owner drops
+// the head of its sorted run. Where neighbours among the k + 2 (at most 16) best are too close for the
+// cut keys to order them, the candidates are ranked by their exact keys, one a lane. Where the cut
+// keys cannot tell that the k best are among the candidates (three keys nearly equal at the border),
+// the choices are made one by one from 64-bit keys; where fp32 cannot tell which groups are kept,
+// the groups are valued again in 64 bits. BIAS: keys sigmoid +
+// bias, else the logits, which are exact.
+template <typename LT, int V, int L, bool BIAS>
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, RouteArgs a) {
+    extern __shared__ double lds[];
+    constexpr int kTokens = 64 / L;
+    constexpr uint32_t kIndex = L * V - 1;  // low bits of a packed key
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int team = lane / L, sub = lane % L;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens;
+    if (t0 >= a.T) return;
+    const int64_t t = t0 + team;
+    const bool live = t < a.T;
+    const LT* row = logits + (live ? t : a.T - 1) * a.ld;
+    const int E = a.E, k = a.k, e0 = sub * V;
+    const uint64_t team_lanes = (L == 64 ? ~uint64_t{0} : (uint64_t{1} << L) - 1) << (team * L);
+    const auto team_any = [&](bool x) { return (__ballot(x) & team_lanes) != 0; };
+
+    float z[V];
+    load_run<V>(row + e0, a.vec && E % 4 == 0, E - e0, z);
+    bool bad = false;
+    uint32_t low = 0;  // bits that the cut keys lose
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        z[v] += 0.0f;  // -0 and 0 are the same logit
+        bad = bad || z[v] != z[v] || (a.softmax && z[v] == INFINITY);
+        low |= z[v] == -INFINITY ? 0u : __float_as_uint(z[v]) & kIndex;
+    }
+    bad = team_any(bad);
+    const bool exact = !BIAS && (sizeof(LT) == 2 || !team_any(low != 0));
+
+    float key[V];
+    if (BIAS) load_run<V>(a.bias + e0, a.bias_vec && E % 4 == 0, E - e0, key);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (BIAS) {
+            key[v] += __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[v] * -1.44269504f));
+            key[v] = key[v] != key[v] || z[v] == -INFINITY ? -INFINITY : key[v];
+        } else {
+            key[v] = z[v];
+        }
+    }
+
+    float total = 1.0f, top = 0.0f;
+    if (a.softmax && !a.renormalize) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
+        top = from_ordered(team_umax<L>(m));
+        total = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) total += z[v] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((z[v] - top) * 1.44269504f);
+        total = team_sum<L>(total);
+    }
+
+    // doubles of LDS a token has: its keys, a group's run padded to an odd length, and the groups' values
+    const int size = E / a.groups, pitch = size | 1, area = a.groups * (pitch + 1);
+    uint32_t dropped = 0;  // bit v: the group of expert e0 + v is not kept
+    if (a.groups > 1) {
+        double* const mine64 = lds + static_cast<int64_t>(wave * kTokens + team) * area;
+        float* const mine = reinterpret_cast<float*>(mine64);
+        float* const value = mine + a.groups * pitch;
+        // a group of whole runs, 1, 2, 4, 8 or 16 of them, is valued in registers; any other through LDS
+        const int runs = size / V;
+        const bool regular = size % V == 0 && (runs & (runs - 1)) == 0 && runs <= 16;
+        const int shift = regular ? __builtin_ctz(runs) : 0;
+        float first = -INFINITY, second = -INFINITY;
+        int group = sub;  // the group this lane values
+        if (regular) {
+            group = sub >> shift;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                second = __builtin_amdgcn_fmed3f(first, second, key[v]);
+                first = fmaxf(first, key[v]);
+            }
+            const auto join = [&](int of, int os) {
+                const float x = __uint_as_float(of), y = __uint_as_float(os);
+                second = fmaxf(fminf(first, x), fmaxf(second, y));
+                first = fmaxf(first, x);
+            };
+#define BSFP8_JOIN(ctrl)                                                                              \
+    join(__builtin_amdgcn_update_dpp(0, __float_as_uint(first), ctrl, 0xF, 0xF, false),               \
+         __builtin_amdgcn_update_dpp(0, __float_as_uint(second), ctrl, 0xF, 0xF, false))
+            if (runs >= 2) BSFP8_JOIN(0xB1);
+            if (runs >= 4) BSFP8_JOIN(0x4E);
+            if (runs >= 8) BSFP8_JOIN(0x141);
+            if (runs >= 16) BSFP8_JOIN(0x140);
+#undef BSFP8_JOIN
+        } else {
+            // lane g reads run g, at an odd distance from its neighbours: no bank twice
+            const int spare = 2 * area - 1;  // past the keys and group values: for lanes past E
+            int i = e0 % size, at = e0 / size * pitch + i;
+#pragma unroll 4
+            for (int v = 0; v < V; ++v) {
+                mine[e0 + v < E ? at : spare] = key[v];
+                ++i;
+                ++at;
+                if (i == size) {
+                    i = 0;
+                    at += pitch - size;
+                }
+            }
+            wave_lds_fence();
+            if (sub < a.groups)
+                for (int j = 0; j < size; ++j) {
+                    const float x = mine[sub * pitch + j];
+                    second = fmaxf(second, fminf(first, x));
+                    first = fmaxf(first, x);
+                }
+        }
+        // Ranks of the groups. With exact keys they are exact; a sum of two scores is off by at most two
+        // keys' errors, a difference of two sums by twice that, and a border inside it is open.
+        float tol = 0.0f;
+        if (BIAS) {
+            const float big = fmaxf(fabsf(first), second == -INFINITY ? 0.0f : fabsf(second));
+            tol = first == -INFINITY ? 0.0f : 4.0f * (kKeyError + kKeyRounding * big);
+            if (second != -INFINITY) first += second;
+        }
+        wave_lds_fence();
+        if (group < a.groups) value[group] = first;
+        wave_lds_fence();
+        int before = 0, maybe = 0;
+        const float high = first + tol, low = first - tol;
+#pragma unroll 4
+        for (int j = 0; j < a.groups; ++j) {
+            const float x = value[j];
+            if (BIAS) {
+                before += x > high ? 1 : 0;
+                maybe += x >= low ? 1 : 0;  // itself, at least
+            } else {
+                before += x > first || (x == first && j < group) ? 1 : 0;
+            }
+        }
+        bool keep = group < a.groups && before < a.top_groups;
+        bool lanes_keep = regular;  // keep is about the lane's own experts
+        if (BIAS && __any(keep && maybe > a.top_groups && !bad)) {
+            wave_lds_fence();
+            double* const value64 = mine64 + a.groups * pitch;
+            int g = e0 / size, i = e0 - g * size;
+#pragma unroll 1
+            for (int v = 0; v < V && e0 + v < E; ++v) {
+                const float x = load_logit(row + e0 + v);
+                double y = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(a.bias[e0 + v]);
+                mine64[g * pitch + i] = x == -INFINITY || y != y ? -INFINITY : y;
+                if (++i == size) {
+                    i = 0;
+                    ++g;
+                }
+            }
+            wave_lds_fence();
+            double one = -INFINITY, two = -INFINITY;
+            if (sub < a.groups) {
+#pragma unroll 1
+                for (int j = 0; j < size; ++j) {
+                    const double x = mine64[sub * pitch + j];
+                    two = fmax(two, fmin(one, x));
+                    one = fmax(one, x);
+                }
+                if (two != -INFINITY) one += two;
+                value64[sub] = one;
+            }
+            wave_lds_fence();
+            int rank = 0;
+            if (sub < a.groups)
+#pragma unroll 1
+                for (int j = 0; j < a.groups; ++j) rank += value64[j] > one || (value64[j] == one && j < sub) ? 1 : 0;
+            keep = sub < a.groups && rank < a.top_groups;
+            lanes_keep = false;
+        }
+        if (lanes_keep) {
+            dropped = keep ? 0u : ~0u;
+        } else {
+            const uint64_t kept = (__ballot(keep) & team_lanes) >> (team * L);  // bit g: group g
+            int g = e0 / size, i = e0 - g * size;
+#pragma unroll 1
+            for (int v = 0; v < V; ++v) {
+                dropped |= ((kept >> g) & 1 ? 0u : 1u) << v;
+                if (++i == size) {
+                    i = 0;
+                    ++g;
+                }
+            }
+        }
+    }
+
+    // packed keys; -inf stays below kLeastKey
+    uint32_t run[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) run[v] = (ordered(key[v]) & ~kIndex) | ((kIndex - e0) ^ v);
+    if (dropped != 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if ((dropped >> v) & 1) run[v] = 0;
+    }
+    sort_descending<V>(run);
+
+    const int m = min(k + 2, 16);
+    uint32_t mine = 0, at_k = 0;  // lane j: the j-th candidate; every lane: the k-th
+    for (int j = 0; j < m; ++j) {
+        const uint32_t best = team_umax<L>(run[0]);
+        if (sub == j) mine = best;
+        if (j == k - 1) at_k = best;
+        const uint32_t own = run[0] == best ? ~0u : 0u;  // a bit select: "own ? a : b" becomes an indexed read
+#pragma unroll
+        for (int v = 0; v + 1 < V; ++v) run[v] = (run[v + 1] & own) | (run[v] & ~own);
+        run[V - 1] &= ~own;
+    }
+    const uint32_t next = team_umax<L>(run[0]);
+
+    // Whether two packed keys, x before y, may stand for keys in the other order.
+    const auto close = [&](uint32_t x, uint32_t y) {
+        if (exact || y < kLeastKey) return false;
+        if (!BIAS) return (x & ~kIndex) == (y & ~kIndex);
+        const float f = from_ordered(x & ~kIndex), h = from_ordered(y & ~kIndex), big = fmaxf(fabsf(f), fabsf(h));
+        return !(f - h > 2.0f * (kKeyError + kKeyRounding * big) + big * (2.0f * (kIndex + 1) * 1.1920929e-7f));
+    };
+    const bool open = close(at_k, next);  // an expert that is no candidate may be among the k best
+    const uint32_t after = __builtin_amdgcn_update_dpp(0, mine, 0x101, 0xF, 0xF, false);  // the next lane's
+
+    bool have = sub < 16 && mine >= kLeastKey;
+    int id = have ? static_cast<int>(kIndex - (mine & kIndex)) : 0x7FFFFFFF;
+    float zc = have ? load_logit(row + id) : -INFINITY;
+    int rank = sub;
+    if (__any(have && sub < k && close(mine, after))) {  // by the exact keys
+        double full = zc + 0.0f;
+        if (BIAS && have) full = 1.0 / (1.0 + exp(-static_cast<double>(zc))) + static_cast<double>(a.bias[id]);
+        rank = rank_row16(full, id);  // lanes without a candidate: -inf, last
+    }
+    bool chosen = have && rank < k;
+    if (__any(open && live && !bad)) {  // choice by choice from 64-bit keys in LDS
+        double* const key64 = lds + static_cast<int64_t>(wave * kTokens + team) * area;
+        wave_lds_fence();
+#pragma unroll 1
+        for (int v = 0; v < V && e0 + v < E; ++v) {
+            const float x = load_logit(row + e0 + v);
+            double y = x + 0.0f;
+            if (BIAS) y = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(a.bias[e0 + v]);
+            key64[e0 + v] = x == -INFINITY || y != y || ((dropped >> v) & 1) ? -INFINITY : y;
+        }
+        int found = -1;
+#pragma unroll 1
+        for (int j = 0; j < k; ++j) {
+            wave_lds_fence();
+            double best = -INFINITY;
+            int at = E;
+#pragma unroll 1
+            for (int e = e0; e < min(e0 + V, E); ++e)
+                if (key64[e] > best) {
+                    best = key64[e];
+                    at = e;
+                }
+#pragma unroll 1
+            for (int x = 1; x < L; x <<= 1) {
+                const double ob = __shfl_xor(best, x);
+                const int oa = __shfl_xor(at, x);
+                if (ob > best || (ob == best && oa < at)) {
+                    best = ob;
+                    at = oa;
+                }
+            }
+            if (sub == j && best != -INFINITY) found = at;
+            wave_lds_fence();
+            if (at >= e0 && at < min(e0 + V, E)) key64[at] = -INFINITY;
+        }
+        if (open) {
+            have = chosen = found >= 0;
+            id = found;
+            rank = sub;
+            zc = have ? load_logit(row + id) : -INFINITY;
+        }
+    }
+
+    float w;
+    if (a.softmax && a.renormalize) {
+        const float ztop = from_ordered(umax_row16(chosen ? ordered(zc) : 0u));
+        w = chosen ? expf(zc - ztop) : 0.0f;
+        const float sum = sum_row16(w);
+        w /= sum;
+    } else {
+        w = a.softmax ? expf(zc - top) / total : 1.0f / (1.0f + expf(-zc));
+        if (!chosen) w = 0.0f;
+        const float sum = sum_row16(w);
+        if (a.renormalize) w /= fmaxf(sum, kSumFloor);
+    }
+    if (live && sub < k) {
+        if (bad) {  // no probabilities: no expert, NaN weights
+            a.weights[t * k + sub] = NAN;
+            a.ids[t * k + sub] = -1;
+        } else if (!have) {  // the candidates fill the lanes from 0 on: this choice found no expert
+            a.weights[t * k + sub] = 0.0f;
+            a.ids[t * k + sub] = -1;
+        }
+    }
+    if (live && !bad && chosen) {
+        a.weights[t * k + rank] = a.scale * w;
+        a.ids[t * k + rank] = id;
     }
 }
 
@@ -545,12 +976,22 @@ bool rows16(const void* p, int64_t ld_bytes) { return (reinterpret_cast<uintptr_
 }  // namespace
 
 template <typename LT, int V>
-static hipError_t route_v(const LT* logits, int64_t T, int E, int64_t ld, const RouteRule& r, const float* bias,
-                          float* weights, int32_t* ids, hipStream_t stream) {
-    const int64_t blocks = (T + kWaves - 1) / kWaves;
-    const size_t lds = r.groups > 1 ? sizeof(double) * kWaves * (E + r.groups) : 0;
-    route_kernel<LT, V><<<dim3(static_cast<unsigned>(blocks)), 64 * kWaves, lds, stream>>>(
-        logits, T, E, ld, bias, r.softmax, r.k, r.groups, r.top_groups, r.renormalize, r.scale, weights, ids);
+static hipError_t route_wide(const LT* logits, const RouteArgs& a, hipStream_t stream) {
+    const int64_t blocks = (a.T + kWaves - 1) / kWaves;
+    const size_t lds = a.groups > 1 ? sizeof(double) * kWaves * (a.E + a.groups) : 0;
+    route_wide_kernel<LT, V><<<dim3(static_cast<unsigned>(blocks)), 64 * kWaves, lds, stream>>>(logits, a);
+    return hipGetLastError();
+}
+
+template <typename LT, int V, int L>
+static hipError_t route_teams(const LT* logits, const RouteArgs& a, hipStream_t stream) {
+    const int64_t per = kWaves * (64 / L), blocks = (a.T + per - 1) / per;
+    const size_t lds = sizeof(double) * per * a.groups * ((a.E / a.groups | 1) + 1);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (a.bias != nullptr)
+        route_kernel<LT, V, L, true><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
+    else
+        route_kernel<LT, V, L, false><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
     return hipGetLastError();
 }
 
@@ -572,11 +1013,20 @@ static hipError_t route_backward_v(const LT* logits, int64_t T, int E, int64_t l
                 : call(16))
 
 template <typename LT>
-static hipError_t route_t(const void* logits, int64_t T, int E, int64_t ld, const RouteRule& r, const float* bias,
-                          float* weights, int32_t* ids, hipStream_t stream) {
-#define CALL(V) route_v<LT, V>(static_cast<const LT*>(logits), T, E, ld, r, bias, weights, ids, stream)
-    return BSFP8_BY_EXPERTS(CALL);
+static hipError_t route_t(const LT* logits, const RouteArgs& a, hipStream_t stream) {
+    const int E = a.E;
+    const bool wide = a.k > 16 || (a.softmax && a.bias != nullptr) || a.groups > (E <= 256 ? 16 : 64);
+    if (wide) {
+#define CALL(V) route_wide<LT, V>(logits, a, stream)
+        return BSFP8_BY_EXPERTS(CALL);
 #undef CALL
+    }
+    if (E <= 16) return route_teams<LT, 1, 16>(logits, a, stream);
+    if (E <= 64) return route_teams<LT, 4, 16>(logits, a, stream);
+    if (E <= 128) return route_teams<LT, 8, 16>(logits, a, stream);
+    if (E <= 256) return route_teams<LT, 16, 16>(logits, a, stream);
+    if (E <= 512) return route_teams<LT, 8, 64>(logits, a, stream);
+    return route_teams<LT, 16, 64>(logits, a, stream);
 }
 
 template <typename LT>
@@ -589,8 +1039,9 @@ static hipError_t route_backward_t(const void* logits, int64_t T, int E, int64_t
 
 hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int64_t ld, const RouteRule& r, const float* bias,
                         float* weights, int32_t* ids, hipStream_t stream) {
-    return f32 ? route_t<float>(logits, T, E, ld, r, bias, weights, ids, stream)
-               : route_t<uint16_t>(logits, T, E, ld, r, bias, weights, ids, stream);
+    const RouteArgs a{T, E, ld, bias, r.softmax, r.k, r.groups, r.top_groups, r.renormalize, r.scale, weights, ids,
+                      rows16(logits, ld * (f32 ? 4 : 2)), rows16(bias, 0)};
+    return f32 ? route_t(static_cast<const float*>(logits), a, stream) : route_t(static_cast<const uint16_t*>(logits), a, stream);
 }
 
 hipError_t launch_route_backward(const void* logits, bool f32, int64_t T, int E, int64_t ld, const RouteRule& r,
