@@ -261,10 +261,19 @@ inline int64_t routed_row_tiles(int64_t M, int64_t E, int64_t tm) {
     return (M - n) / tm + n;
 }
 
-// 16-row subtiles of the routed product's tile: by the mean rows of the experts that can have any.
-inline int routed_subtiles(int64_t M, int64_t E) {
-    const int64_t mean = cdiv(M, E < M ? E : M);
-    return mean <= 8 ? 1 : mean <= 20 ? 2 : 4;
+// Kernel of the routed product. Where workgroups are many or rows are, 64-row tiles through LDS; where
+// neither is, so that a workgroup's own latency counts, 16- or 32-row tiles straight into registers,
+// with narrower columns and the waves splitting K. Rows are known to the device only: the rule takes
+// the mean over the experts that can have any, and one tile an expert. Measured, 256 CUs (us, registers
+// against LDS): 1 row each of 8 experts of 2048 x 4096, 128 workgroups of the LDS kernel: 13.7
+// against 17.8; 8 rows of 8 experts, gated 2048 x 4096, 256 workgroups: 27.4, 28.2; 2 rows of 56
+// experts of 2048 x 2048, 896: 29.9, 26.8; 16 rows of 64 experts, gated 1024 x 4096, 1024: 109, 99; 60 rows of
+// 8 experts, gated 2048 x 4096, 256: 54, 36.
+enum RoutedKernel { kRoutedRegisters16, kRoutedRegisters32, kRoutedLds };
+inline RoutedKernel routed_kernel(int64_t M, int64_t N, int64_t E, bool swiglu, int cus) {
+    const int64_t experts = E < M ? E : M, mean = cdiv(M, experts);
+    if (mean > 16 || experts * cdiv(N, swiglu ? 64 : 128) >= 2 * static_cast<int64_t>(cus)) return kRoutedLds;
+    return mean <= 4 ? kRoutedRegisters16 : kRoutedRegisters32;
 }
 
 }  // namespace sched

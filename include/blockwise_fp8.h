@@ -464,8 +464,9 @@ int moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t
  * Requirements (else BSFP8_EINVAL): K a positive multiple of 128, N a multiple of 128 with swiglu,
  * a_rows >= M without rows, M < 2^31; alignment as gemm_1x128_128x128 (b_stride too). The K range is
  * summed in parts in a fixed order, so results can differ from the grouped GEMM's in the last bits
- * and are the same on every call. Any row counts are computed; from about 128 rows an expert the
- * grouped GEMM is the faster one.
+ * and are the same on every call. Any row counts are computed; the grouped GEMM is as fast from about
+ * 256 rows an expert (8 experts of 4096 x 4096: 64 rows each 36 us against 58, 128 rows 39 against
+ * 59, 256 rows 66 against 64).
  */
 int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int64_t a_rows,
                               const int32_t* rows, int64_t k,
