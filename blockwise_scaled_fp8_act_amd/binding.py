@@ -102,16 +102,16 @@ def lib():
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return _vp(_raw_stream(torch.cuda.current_device()))
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
-    return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t):
-    return _vp(t.data_ptr()) if t is not None else _vp(0)
+    return t.data_ptr() if t is not None else None      # an int or None: ctypes' argtypes make the pointer
 
 
 def _ld(t):
@@ -197,7 +197,7 @@ def _dense(name, t, dtype, shape):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -209,14 +209,18 @@ def _codes(name, t, fmt, shape=None):
 
 
 def _gpu(**tensors):
+    """Every tensor (None: skipped) is on the current GPU, whose index is returned."""
     dev = None
     for name, t in tensors.items():
         if t is not None:
-            if not t.is_cuda:
+            at = t.get_device()         # -1: not a GPU tensor
+            if at < 0:
                 raise ValueError(f"{name} must be a GPU tensor, got one on {t.device}")
             if dev is None:
-                dev = torch.cuda.current_device()
-            _on_gpu(name, t, dev)
+                dev = torch._C._cuda_getDevice()    # a GPU tensor exists: torch.cuda is initialised
+            if at != dev:
+                _on_gpu(name, t, dev)
+    return dev
 
 
 def _strided_scales(name, t, Nb, Kb, nb, kb):
@@ -526,17 +530,18 @@ MAX_EXPERTS = 1024
 MAX_CHOICES = 64
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+_LOGIT_TYPES = tuple(_LOGITS)
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on ``stream``: its memory belongs to that stream, so it is neither taken
-    from, nor given back to, work that another stream has pending."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty(like, shape, dtype, stream):
+    """A new tensor on ``like``'s device for a call on ``stream``: its memory belongs to that stream, so
+    it is neither taken from, nor given back to, work that another stream has pending."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _choices(name, t, dtype):
@@ -555,7 +560,7 @@ def _choices(name, t, dtype):
 
 
 def _route_args(logits, k, score, scale):
-    T, E = _matrix("logits", logits, tuple(_LOGITS)).shape
+    T, E = _matrix("logits", logits, _LOGIT_TYPES).shape
     if not 1 <= E <= MAX_EXPERTS:
         raise ValueError(f"logits has {E} experts, expected 1 to {MAX_EXPERTS}")
     if not 1 <= k <= min(E, MAX_CHOICES):
@@ -581,14 +586,16 @@ def moe_route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, ren
     if bias is not None:
         _dense("bias", bias, torch.float32, (E,))
     if weights is None:
-        weights = _empty((T, k), torch.float32, logits.device, stream)
+        weights = _empty(logits, (T, k), torch.float32, stream)
+    else:
+        _dense("weights", weights, torch.float32, (T, k))
     if ids is None:
-        ids = _empty((T, k), torch.int32, logits.device, stream)
-    _dense("weights", weights, torch.float32, (T, k))
-    _dense("ids", ids, torch.int32, (T, k))
-    _gpu(logits=logits, bias=bias, weights=weights, ids=ids)
+        ids = _empty(logits, (T, k), torch.int32, stream)
+    else:
+        _dense("ids", ids, torch.int32, (T, k))
+    dev = _gpu(logits=logits, bias=bias, weights=weights, ids=ids)
     _call("moe_route", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _ptr(bias), _SCORES[score], k,
-          groups, top_groups, int(bool(renormalize)), scale, _ptr(weights), _ptr(ids), _stream(stream))
+          groups, top_groups, int(bool(renormalize)), scale, _ptr(weights), _ptr(ids), _stream(stream, dev))
     return weights, ids
 
 
@@ -601,12 +608,13 @@ def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True,
         raise ValueError(f"logits has {logits.shape[0]} rows, ids {T}")
     _dense("dweights", dweights, torch.float32, (T, k))
     if dlogits is None:
-        dlogits = _empty((T, E), logits.dtype, logits.device, stream)
-    _matrix("dlogits", dlogits, (logits.dtype,), (T, E))
-    _gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+        dlogits = _empty(logits, (T, E), logits.dtype, stream)
+    else:
+        _matrix("dlogits", dlogits, (logits.dtype,), (T, E))
+    dev = _gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
     _call("moe_route_backward", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _SCORES[score], k,
           int(bool(renormalize)), scale, _ptr(ids), _ptr(dweights), _ptr(dlogits), _row_stride(dlogits),
-          _stream(stream))
+          _stream(stream, dev))
     return dlogits
 
 
@@ -620,17 +628,20 @@ def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream
     if not 1 <= E <= MAX_EXPERTS:
         raise ValueError(f"E = {E} must lie in [1, {MAX_EXPERTS}]")
     if offsets is None:
-        offsets = _empty((E + 1,), torch.int64, ids.device, stream)
+        offsets = _empty(ids, E + 1, torch.int64, stream)
+    else:
+        _dense("offsets", offsets, torch.int64, (E + 1,))
     if slots is None:
-        slots = _empty((T, k), torch.int32, ids.device, stream)
+        slots = _empty(ids, (T, k), torch.int32, stream)
+    else:
+        _dense("slots", slots, torch.int32, (T, k))
     if rows is None:
-        rows = _empty((T * k,), torch.int32, ids.device, stream)
+        rows = _empty(ids, T * k, torch.int32, stream)
+    else:
+        _dense("rows", rows, torch.int32, (T * k,))
     need = moe_plan_workspace(T, k, E)
     if workspace is None and need > 0:
-        workspace = _empty((need,), torch.uint8, ids.device, stream)
-    _dense("offsets", offsets, torch.int64, (E + 1,))
-    _dense("slots", slots, torch.int32, (T, k))
-    _dense("rows", rows, torch.int32, (T * k,))
+        workspace = _empty(ids, need, torch.uint8, stream)
     size = 0
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -638,9 +649,9 @@ def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream
         size = workspace.numel()
         if size < need:
             raise ValueError(f"workspace holds {size} bytes, the plan needs {need}")
-    _gpu(ids=ids, offsets=offsets, slots=slots, rows=rows, workspace=workspace)
+    dev = _gpu(ids=ids, offsets=offsets, slots=slots, rows=rows, workspace=workspace)
     _call("moe_plan", _ptr(ids), T, k, E, _ptr(offsets), _ptr(slots), _ptr(rows), _ptr(workspace), size,
-          _stream(stream))
+          _stream(stream, dev))
     return offsets, slots, rows
 
 
@@ -660,18 +671,20 @@ def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=
     H = _matrix("x", x, _BF16, (T, None)).shape[1]
     R = T * k
     if q is None:
-        q = _empty((R, H), torch.uint8, x.device, stream)
+        q = _empty(x, (R, H), torch.uint8, stream)
+    else:
+        _matrix("q", q, _CODES["e4m3fn"], (R, H))
     if a_s is None:
-        a_s = _empty((cdiv(H, BLOCK), R), torch.float32, x.device, stream)
-    if copy is None and want_copy:
-        copy = _empty((R, H), torch.bfloat16, x.device, stream)
-    _codes("q", q, "e4m3fn", (R, H))
-    _dense("a_s", a_s, torch.float32, (cdiv(H, BLOCK), R))
+        a_s = _empty(x, (cdiv(H, BLOCK), R), torch.float32, stream)
+    else:
+        _dense("a_s", a_s, torch.float32, (cdiv(H, BLOCK), R))
     if copy is not None:
         _matrix("copy", copy, _BF16, (R, H))
-    _gpu(x=x, slots=slots, q=q, a_s=a_s, copy=copy)
+    elif want_copy:
+        copy = _empty(x, (R, H), torch.bfloat16, stream)
+    dev = _gpu(x=x, slots=slots, q=q, a_s=a_s, copy=copy)
     _call("moe_dispatch", _ptr(x), T, H, _row_stride(x), _ptr(slots), k, _ptr(q), _row_stride(q), _ptr(a_s), _ptr(copy),
-          _row_stride(copy) if copy is not None else 0, _stream(stream))
+          _row_stride(copy) if copy is not None else 0, _stream(stream, dev))
     return q, a_s, copy
 
 
@@ -683,11 +696,12 @@ def moe_combine(rows, slots, weights=None, y=None, stream=None):
     if weights is not None:
         _dense("weights", weights, torch.float32, (T, k))
     if y is None:
-        y = _empty((T, H), torch.bfloat16, rows.device, stream)
-    _matrix("y", y, _BF16, (T, H))
-    _gpu(rows=rows, slots=slots, weights=weights, y=y)
+        y = _empty(rows, (T, H), torch.bfloat16, stream)
+    else:
+        _matrix("y", y, _BF16, (T, H))
+    dev = _gpu(rows=rows, slots=slots, weights=weights, y=y)
     _call("moe_combine", _ptr(rows), R, _row_stride(rows), _ptr(slots), _ptr(weights), T, k, H, _ptr(y), _row_stride(y),
-          _stream(stream))
+          _stream(stream, dev))
     return y
 
 
@@ -700,14 +714,16 @@ def moe_combine_backward(dy, rows, slots, weights, drows=None, dweights=None, st
     _matrix("rows", rows, _BF16, (R, H))
     _dense("weights", weights, torch.float32, (T, k))
     if drows is None:
-        drows = _empty((R, H), torch.bfloat16, dy.device, stream)
+        drows = _empty(dy, (R, H), torch.bfloat16, stream)
+    else:
+        _matrix("drows", drows, _BF16, (R, H))
     if dweights is None:
-        dweights = _empty((T, k), torch.float32, dy.device, stream)
-    _matrix("drows", drows, _BF16, (R, H))
-    _dense("dweights", dweights, torch.float32, (T, k))
-    _gpu(dy=dy, rows=rows, slots=slots, weights=weights, drows=drows, dweights=dweights)
+        dweights = _empty(dy, (T, k), torch.float32, stream)
+    else:
+        _dense("dweights", dweights, torch.float32, (T, k))
+    dev = _gpu(dy=dy, rows=rows, slots=slots, weights=weights, drows=drows, dweights=dweights)
     _call("moe_combine_backward", _ptr(dy), _row_stride(dy), _ptr(rows), _row_stride(rows), _ptr(slots), _ptr(weights), T, k,
-          H, _ptr(drows), _row_stride(drows), _ptr(dweights), _stream(stream))
+          H, _ptr(drows), _row_stride(drows), _ptr(dweights), _stream(stream, dev))
     return drows, dweights
 
 
@@ -722,8 +738,8 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
     r of C multiplies A's row rows[r] // k (its token); None: row r of A. ``swiglu``: B_e holds N gate
     rows, then N up rows, and C = silu(gate) * up. N defaults to the output columns of the experts'
     rows stacked in b ([E * N, K], or [E * 2 N, K] with swiglu). Returns c [M, N] bf16."""
-    A, K = _codes("a", a, "e4m3fn").shape
-    _codes("b", b, "e4m3fn")
+    A, K = _matrix("a", a, _CODES["e4m3fn"]).shape
+    _matrix("b", b, _CODES["e4m3fn"])
     if E < 0 or E > MAX_EXPERTS:
         raise ValueError(f"E = {E} must lie in [0, {MAX_EXPERTS}]")
     if K == 0 or K % BLOCK != 0:
@@ -746,12 +762,13 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
     if min(ldb, b_stride, bs_stride, bs_stride_nb, bs_stride_kb, N) < 0:
         raise ValueError("strides and N must be >= 0")
     if c is None:
-        c = _empty((M, N), torch.bfloat16, a.device, stream)
+        c = _empty(a, (M, N), torch.bfloat16, stream)
+    else:
+        _matrix("c", c, (torch.bfloat16,), (M, N))
     _dense("a_s", a_s, torch.float32, (cdiv(K, BLOCK), A))
     if not isinstance(b_s, torch.Tensor) or b_s.dtype != torch.float32 or not b_s.is_contiguous():
         raise TypeError("b_s must be a contiguous float32 tensor")
     _offsets(offsets, E)
-    _matrix("c", c, (torch.bfloat16,), (M, N))
     if E > 0 and M > 0 and N > 0:
         need = (E - 1) * b_stride + (halves * N - 1) * ldb + K
         have = b.untyped_storage().nbytes() - b.storage_offset()
@@ -760,8 +777,8 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
         need = (E - 1) * bs_stride + (cdiv(halves * N, BLOCK) - 1) * bs_stride_nb + (K // BLOCK - 1) * bs_stride_kb + 1
         if need > b_s.numel():
             raise ValueError(f"b_s holds {b_s.numel()} floats, E, N, K and the strides read {need}")
-    _gpu(a=a, a_s=a_s, b=b, b_s=b_s, offsets=offsets, rows=rows, c=c)
+    dev = _gpu(a=a, a_s=a_s, b=b, b_s=b_s, offsets=offsets, rows=rows, c=c)
     _call("gemm_1x128_128x128_routed", _ptr(a), _row_stride(a), _ptr(a_s), A, _ptr(rows), k, _ptr(b), ldb, b_stride,
           _ptr(b_s), bs_stride, bs_stride_nb, bs_stride_kb, _ptr(offsets), E, _ptr(c), _row_stride(c), M, N, K,
-          int(bool(swiglu)), _stream(stream))
+          int(bool(swiglu)), _stream(stream, dev))
     return c

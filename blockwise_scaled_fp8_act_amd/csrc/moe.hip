@@ -10,6 +10,7 @@ namespace bsfp8 {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
 
@@ -681,38 +682,44 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* l
 }
 
 // ---------------------------------------------------------------------------------------- plan
-// A stable counting sort of the P = T k pairs into E + 1 bins (bin E: no expert here). Each wave
-// walks its own contiguous run of pairs, 64 at a time; a pair's rank among the equal bins of its 64
-// comes from one ballot per bit of the bin number, and one lane per distinct bin advances the
-// wave's own counter, so no atomics decide an order. With more than one workgroup a first kernel
-// counts each workgroup's bins, and every workgroup sums the counts it needs.
-constexpr int kPlanWaves = 8;
+// A stable counting sort of the P = T k pairs into E + 1 bins (bin E: no expert here). A workgroup
+// takes its pairs in rounds; in a round each wave has kPlanSteps steps of 64 pairs, loaded together. A
+// pair's rank among the equal bins of its 64 comes from one ballot per bit of the bin number, and one
+// lane per distinct bin advances the wave's own counter, so no atomics decide an order. With more
+// than one workgroup a first kernel counts each workgroup's bins, and every workgroup sums the
+// counts it needs.
+constexpr int kPlanWaves = sched::kPlanWaves, kPlanSteps = sched::kPlanRound / (64 * kPlanWaves);
+constexpr int kPlanThreads = 64 * kPlanWaves;
 
 struct PlanArgs {
     const int32_t* ids;
     int64_t P;
     int E;
-    int64_t seg;       // pairs per workgroup, a multiple of 64 * kPlanWaves
+    int64_t seg;       // pairs per workgroup, whole rounds
     int32_t* counts;   // [workgroups][E + 1], used with more than one workgroup
     int64_t* offsets;
     int32_t* slots;
     int32_t* rows;
 };
 
-__device__ __forceinline__ int plan_bin(const PlanArgs& a, int64_t p) {
-    const int id = a.ids[p];
-    return id >= 0 && id < a.E ? id : a.E;
-}
+__device__ __forceinline__ int plan_bin(int32_t id, int E) { return id >= 0 && id < E ? id : E; }
 
-__global__ __launch_bounds__(64 * kPlanWaves) void plan_count_kernel(PlanArgs a) {
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
     extern __shared__ int32_t hist[];
     const int tid = threadIdx.x, bins = a.E + 1;
-    for (int b = tid; b < bins; b += 64 * kPlanWaves) hist[b] = 0;
+    for (int b = tid; b < bins; b += kPlanThreads) hist[b] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * a.seg, hi = min(lo + a.seg, a.P);
-    for (int64_t p = lo + tid; p < hi; p += 64 * kPlanWaves) atomicAdd(&hist[plan_bin(a, p)], 1);
+    for (int64_t p0 = lo; p0 < hi; p0 += sched::kPlanRound) {
+        int32_t id[kPlanSteps];
+#pragma unroll
+        for (int s = 0; s < kPlanSteps; ++s) id[s] = p0 + s * kPlanThreads + tid < hi ? a.ids[p0 + s * kPlanThreads + tid] : 0;
+#pragma unroll
+        for (int s = 0; s < kPlanSteps; ++s)
+            if (p0 + s * kPlanThreads + tid < hi) atomicAdd(&hist[plan_bin(id[s], a.E)], 1);
+    }
     __syncthreads();
-    for (int b = tid; b < bins; b += 64 * kPlanWaves) a.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = hist[b];
+    for (int b = tid; b < bins; b += kPlanThreads) a.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = hist[b];
 }
 
 // Lanes of this wave whose bin equals this lane's, among the lanes of `active`.
@@ -725,153 +732,192 @@ __device__ __forceinline__ uint64_t same_bin(int bin, int bits, uint64_t active)
     return m;
 }
 
-__global__ __launch_bounds__(64 * kPlanWaves) void plan_kernel(PlanArgs a) {
-    extern __shared__ int32_t base[];  // [kPlanWaves][bins] counts, then each wave's next row of a bin
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
+    extern __shared__ int32_t bin_lds[];
     __shared__ int32_t wave_total[kPlanWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = a.E + 1;
     const int bits = 32 - __builtin_clz(a.E);  // E itself needs a place
-    for (int b = tid; b < bins * kPlanWaves; b += 64 * kPlanWaves) base[b] = 0;
-    __syncthreads();
-
-    const int64_t run = a.seg / kPlanWaves;
-    const int64_t lo = blockIdx.x * a.seg + wave * run, hi = min(lo + run, a.P);
-    int32_t* const own = base + wave * bins;
+    int32_t* const wave_bins = bin_lds;                  // [kPlanWaves][bins]: counts, then first rows
+    int32_t* const next = wave_bins + kPlanWaves * bins;       // [bins]: this workgroup's next row of a bin
+    int32_t* const all = next + bins;                    // [bins]: pairs of a bin, with more than one workgroup
+    const int64_t lo = blockIdx.x * a.seg, hi = min(lo + a.seg, a.P);
+    const bool many = gridDim.x > 1, rounds = hi - lo > sched::kPlanRound;
+    int32_t* const own = wave_bins + wave * bins;
     const uint64_t below = (uint64_t{1} << lane) - 1;
-    for (int64_t p0 = lo; p0 < hi; p0 += 64) {
-        const bool in = p0 + lane < hi;
-        const int bin = in ? plan_bin(a, p0 + lane) : 0;
-        const uint64_t m = same_bin(bin, bits, __ballot(in));
-        if (in && (m & below) == 0) own[bin] += __popcll(m);
-        wave_lds_fence();
-    }
-    __syncthreads();
 
-    // first row of each bin for this workgroup: the bins before it, and its own bin in the
-    // workgroups before this one; bins in runs of 64 * kPlanWaves, carried on
-    int32_t carry = 0;
-    for (int b0 = 0; b0 < bins; b0 += 64 * kPlanWaves) {
-        const int b = b0 + tid;
-        int32_t all = 0, before = 0;
-        if (b < bins) {
-            if (gridDim.x == 1) {
-                for (int w = 0; w < kPlanWaves; ++w) all += base[w * bins + b];
-            } else {
-                for (unsigned g = 0; g < gridDim.x; ++g) {
-                    const int32_t c = a.counts[static_cast<int64_t>(g) * bins + b];
-                    all += c;
-                    before += g < blockIdx.x ? c : 0;
+    for (int64_t p0 = lo; p0 == lo || p0 < hi; p0 += sched::kPlanRound) {
+        // a short round is spread over all waves
+        const int steps = static_cast<int>((min(hi - p0, int64_t{sched::kPlanRound}) + kPlanThreads - 1) / kPlanThreads);
+        const int64_t mine = p0 + wave * 64 * steps + lane;
+        int32_t id[kPlanSteps], rank[kPlanSteps];
+#pragma unroll
+        for (int s = 0; s < kPlanSteps; ++s) id[s] = s < steps && mine + 64 * s < hi ? a.ids[mine + 64 * s] : 0;
+        for (int b = tid; b < bins * kPlanWaves; b += kPlanThreads) wave_bins[b] = 0;
+        if (p0 == lo && (many || rounds)) {
+            for (int b = tid; b < bins; b += kPlanThreads) next[b] = all[b] = 0;
+            __syncthreads();
+        }
+        if (p0 == lo && !many && rounds)
+            for (int64_t p = tid; p < hi; p += kPlanThreads) atomicAdd(&all[plan_bin(a.ids[p], a.E)], 1);
+        if (p0 == lo && many) {
+            // bins of all workgroups, and of those before this one: parts of the workgroups side by side
+            const int parts = bins < kPlanThreads ? kPlanThreads / bins : 1, part = bins < kPlanThreads ? tid / bins : 0;
+            if (part < parts)
+                for (int b = bins < kPlanThreads ? tid - part * bins : tid; b < bins; b += kPlanThreads) {
+                    int32_t total = 0, before = 0;
+#pragma unroll 8
+                    for (int g = part; g < static_cast<int>(gridDim.x); g += parts) {
+                        const int32_t c = a.counts[static_cast<int64_t>(g) * bins + b];
+                        total += c;
+                        before += g < static_cast<int>(blockIdx.x) ? c : 0;
+                    }
+                    atomicAdd(&all[b], total);  // whole numbers: the order changes nothing
+                    atomicAdd(&next[b], before);
                 }
+        }
+        __syncthreads();
+        // ranks inside the wave's run
+#pragma unroll
+        for (int s = 0; s < kPlanSteps; ++s) {
+            if (s >= steps) continue;
+            const bool in = mine + 64 * s < hi;
+            id[s] = plan_bin(id[s], a.E);
+            const uint64_t m = same_bin(id[s], bits, __ballot(in));
+            rank[s] = own[id[s]] + __popcll(m & below);
+            wave_lds_fence();
+            if (in && (m & below) == 0) own[id[s]] = rank[s] + __popcll(m);
+            wave_lds_fence();
+        }
+        __syncthreads();
+        // first round: where each bin starts (bins in runs of the workgroup's threads, carried on)
+        if (p0 == lo) {
+            int32_t carry = 0;
+            for (int b0 = 0; b0 < bins; b0 += kPlanThreads) {
+                const int b = b0 + tid;
+                int32_t n = 0;
+                if (b < bins) {
+                    if (many || rounds) n = all[b];
+                    else
+                        for (int w = 0; w < kPlanWaves; ++w) n += wave_bins[w * bins + b];
+                }
+                int32_t sum = n;
+                for (int d = 1; d < 64; d <<= 1) {
+                    const int32_t o = __shfl_up(sum, d);
+                    if (lane >= d) sum += o;
+                }
+                if (lane == 63) wave_total[wave] = sum;
+                __syncthreads();
+                int32_t start = carry + sum - n;
+                for (int w = 0; w < kPlanWaves; ++w) {
+                    if (w < wave) start += wave_total[w];
+                    carry += wave_total[w];
+                }
+                if (b < bins) {
+                    if (blockIdx.x == 0) a.offsets[b] = start;
+                    next[b] = start + (many ? next[b] : 0);
+                }
+                __syncthreads();
             }
         }
-        int32_t sum = all;  // inclusive scan over the workgroup's threads
-        for (int d = 1; d < 64; d <<= 1) {
-            const int32_t o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        if (lane == 63) wave_total[wave] = sum;
-        __syncthreads();
-        int32_t start = carry + sum - all;
-        for (int w = 0; w < kPlanWaves; ++w) {
-            if (w < wave) start += wave_total[w];
-            carry += wave_total[w];
-        }
-        if (b < bins) {
-            if (blockIdx.x == 0) a.offsets[b] = start;
-            int32_t next = start + before;
+        // first rows of the waves
+        for (int b = tid; b < bins; b += kPlanThreads) {
+            int32_t at = next[b];
             for (int w = 0; w < kPlanWaves; ++w) {
-                const int32_t c = base[w * bins + b];
-                base[w * bins + b] = next;
-                next += c;
+                const int32_t c = wave_bins[w * bins + b];
+                wave_bins[w * bins + b] = at;
+                at += c;
             }
+            next[b] = at;
         }
         __syncthreads();
-    }
-
-    for (int64_t p0 = lo; p0 < hi; p0 += 64) {
-        const bool in = p0 + lane < hi;
-        const int64_t p = p0 + lane;
-        const int bin = in ? plan_bin(a, p) : 0;
-        const uint64_t m = same_bin(bin, bits, __ballot(in));
-        const int32_t row = own[bin] + __popcll(m & below);
-        wave_lds_fence();
-        if (in && (m & below) == 0) own[bin] = row + __popcll(m);
-        wave_lds_fence();
-        if (in) {
-            a.slots[p] = bin < a.E ? row : -1 - row;
-            a.rows[row] = bin < a.E ? static_cast<int32_t>(p) : -1;
+#pragma unroll
+        for (int s = 0; s < kPlanSteps; ++s) {
+            const int64_t p = mine + 64 * s;
+            if (s >= steps || p >= hi) continue;
+            const int32_t row = own[id[s]] + rank[s];
+            a.slots[p] = id[s] < a.E ? row : -1 - row;
+            a.rows[row] = id[s] < a.E ? static_cast<int32_t>(p) : -1;
         }
+        __syncthreads();
     }
 }
 
 // ------------------------------------------------------------------------------------ dispatch
-// One wave takes 1024 columns of a token: 16 a lane, so a 1x128 group is 8 lanes. The token is read
-// and quantized once and its codes written to each of its k rows (a pass in row order would read
-// the token k times). A dropped pair's padding row is zeroed by the pair's own token, so every row
-// is written exactly once.
+// Outputs that this launch does not read: past the caches, a wave's instruction whole lines.
+__device__ __forceinline__ void stream_store(u32x4* p, u32x4 v) { __builtin_nontemporal_store(v, p); }
+__device__ __forceinline__ void stream_store(u32x2* p, u32x2 v) { __builtin_nontemporal_store(v, p); }
+
+// One wave takes 1024 columns of a token in two pieces of 512, 8 a lane, so a 1x128 group is a row of
+// 16 lanes and every store of a wave is one run of 512 (codes) or 1024 bytes (copy): with 16 columns a
+// lane the copy's two stores interleaved, and past the caches half-written lines cost 314 us against
+// 184 (8192 tokens x 8, 4096 columns). The token is read and quantized once and written to each of
+// its k rows (in row order it would be read k times). A dropped pair's padding row is zeroed by the
+// pair's own token, so every row is written exactly once. The scales of a column are 4 bytes a
+// token, 32 rows a line: workgroups of one XCD (blockIdx % 8) take consecutive tokens, so that its L2
+// collects the lines (without copy 64 -> 53 us, 6.5 TB/s of 0.34 GB).
 template <bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void dispatch_kernel(const uint16_t* x, int64_t T, int64_t H, int64_t ldx,
                                                                const int32_t* slots, int k, int64_t chunks,
                                                                uint8_t* q, int64_t ldq, float* a_s, uint16_t* copy,
                                                                int64_t ldcopy) {
-    const int lane = threadIdx.x & 63;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t block = static_cast<int64_t>(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    const int64_t unit = block * kWaves + wave;
     if (unit >= T * chunks) return;
-    const int64_t t = unit / chunks, col = (unit - t * chunks) * 1024 + lane * 16;
-    const int64_t R = T * k;
-    const bool in = col < H;
+    const int64_t t = unit / chunks, c0 = (unit - t * chunks) * 1024, R = T * k;
 
-    u32x4 w[2] = {};  // 16 bf16
-    if (VEC) {
-        if (in) {
-            const u32x4* p = reinterpret_cast<const u32x4*>(x + t * ldx + col);
-            w[0] = p[0];
-            w[1] = p[1];
+    u32x4 w[2];  // 8 bf16 of each piece
+    u32x2 code[2];
+    float scale[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int64_t col = c0 + 512 * p + lane * 8;
+        w[p] = u32x4{};
+        if (VEC) {
+            if (col < H) w[p] = *reinterpret_cast<const u32x4*>(x + t * ldx + col);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < H) w[p][i >> 1] |= static_cast<uint32_t>(x[t * ldx + col + i]) << (16 * (i & 1));
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (col + i < H) w[i >> 3][(i >> 1) & 3] |= static_cast<uint32_t>(x[t * ldx + col + i]) << (16 * (i & 1));
     }
-    uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t d = w[i >> 2][i & 3];
-        amax = max(amax, max(abs_bits(bf16_lo(d)), abs_bits(bf16_hi(d))));
-    }
-    amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(amax), 0xB1, 0xF, 0xF, false)));
-    amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(amax), 0x4E, 0xF, 0xF, false)));
-    amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(amax), 0x141, 0xF, 0xF, false)));
-    const GroupScale g = group_scale<false>(__uint_as_float(amax));
-    u32x4 code;
+    for (int p = 0; p < 2; ++p) {
+        uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t d0 = w[i >> 1][(2 * i) & 3], d1 = w[i >> 1][(2 * i + 1) & 3];
-        code[i] = encode4_in_range<false>(bf16_lo(d0) * g.m, bf16_hi(d0) * g.m, bf16_lo(d1) * g.m, bf16_hi(d1) * g.m);
+        for (int i = 0; i < 4; ++i) amax = max(amax, max(abs_bits(bf16_lo(w[p][i])), abs_bits(bf16_hi(w[p][i]))));
+        const GroupScale g = group_scale<false>(__uint_as_float(umax_row16(amax)));
+        scale[p] = g.s;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            code[p][i] = encode4_in_range<false>(bf16_lo(w[p][2 * i]) * g.m, bf16_hi(w[p][2 * i]) * g.m,
+                                                 bf16_lo(w[p][2 * i + 1]) * g.m, bf16_hi(w[p][2 * i + 1]) * g.m);
     }
-    if (!in) return;
+    const int32_t mine = lane < k ? slots[t * k + lane] : 0;
     for (int j = 0; j < k; ++j) {
-        const int32_t slot = slots[t * k + j];
+        const int32_t slot = __builtin_amdgcn_readlane(mine, j);
         const int64_t r = slot >= 0 ? slot : -1 - static_cast<int64_t>(slot);
         if (r >= R) continue;
         const uint32_t keep = slot >= 0 ? 0xFFFFFFFFu : 0u;
-        const u32x4 c = code & keep, w0 = w[0] & keep, w1 = w[1] & keep;
-        if (VEC) {
-            *reinterpret_cast<u32x4*>(q + r * ldq + col) = c;
-            if (copy != nullptr) {
-                u32x4* p = reinterpret_cast<u32x4*>(copy + r * ldcopy + col);
-                p[0] = w0;
-                p[1] = w1;
-            }
-        } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (col + i >= H) continue;
-                q[r * ldq + col + i] = static_cast<uint8_t>(c[i >> 2] >> (8 * (i & 3)));
-                if (copy != nullptr)
-                    copy[r * ldcopy + col + i] = static_cast<uint16_t>((i < 8 ? w0 : w1)[(i >> 1) & 3] >> (16 * (i & 1)));
+        for (int p = 0; p < 2; ++p) {
+            const int64_t col = c0 + 512 * p + lane * 8;
+            if (col >= H) continue;
+            const u32x2 c = code[p] & keep;
+            const u32x4 v = w[p] & keep;
+            if (VEC) {
+                stream_store(reinterpret_cast<u32x2*>(q + r * ldq + col), c);
+                if (copy != nullptr) stream_store(reinterpret_cast<u32x4*>(copy + r * ldcopy + col), v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (col + i >= H) continue;
+                    q[r * ldq + col + i] = static_cast<uint8_t>(c[i >> 2] >> (8 * (i & 3)));
+                    if (copy != nullptr) copy[r * ldcopy + col + i] = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
+                }
             }
+            if ((lane & 15) == 0) a_s[(col >> 7) * R + r] = slot >= 0 ? scale[p] : 0.0f;
         }
-        if ((lane & 7) == 0) a_s[(col >> 7) * R + r] = slot >= 0 ? g.s : 0.0f;
     }
 }
 
@@ -895,14 +941,17 @@ template <bool VEC>
 __device__ __forceinline__ void store8(uint16_t* p, int64_t left, const float (&f)[8]) {
     if (VEC) {
         if (left > 0)
-            *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                                pack_bf16x2(f[6], f[7])};
+            stream_store(reinterpret_cast<u32x4*>(p), u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])});
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < left) p[i] = to_bf16(f[i]);
     }
 }
+
+// Choices whose rows are on the way together (a token's rows lie anywhere: each is a round trip).
+constexpr int kBatch = 8;
 
 // One wave takes 512 columns of a token, 8 a lane, and adds its k rows in order of the choices in
 // fp32. A dropped pair adds weight * 0: nothing, unless its weight is NaN (a token whose logits
@@ -912,24 +961,34 @@ __global__ __launch_bounds__(64 * kWaves) void combine_kernel(const uint16_t* ro
                                                               const int32_t* slots, const float* weights, int64_t T,
                                                               int k, int64_t H, int64_t chunks, uint16_t* y,
                                                               int64_t ldy) {
-    const int lane = threadIdx.x & 63;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
     if (unit >= T * chunks) return;
     const int64_t t = unit / chunks, col = (unit - t * chunks) * 512 + lane * 8;
+    // lane j: the j-th choice
+    const int32_t slot = lane < k ? slots[t * k + lane] : -1;
+    const float weight = lane < k ? (weights != nullptr ? weights[t * k + lane] : 1.0f) : 0.0f;
     float acc[8] = {};
-    for (int j = 0; j < k; ++j) {
-        const int32_t slot = slots[t * k + j];
-        const float w = weights != nullptr ? weights[t * k + j] : 1.0f;
-        float f[8] = {};
-        if (slot >= 0 && slot < R) load8<VEC>(rows + slot * ldr + col, H - col, f);
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+        float f[kBatch][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += w * f[i];
+        for (int j = 0; j < kBatch; ++j) {
+            const int32_t r = j0 + j < k ? __builtin_amdgcn_readlane(slot, j0 + j) : -1;
+            const bool there = r >= 0 && r < R;
+            load8<VEC>(rows + (there ? r * ldr : 0) + col, there ? H - col : 0, f[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float w = j0 + j < k ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j0 + j)) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[j][i], acc[i]);
+        }
     }
     store8<VEC>(y + t * ldy + col, H - col, acc);
 }
 
-// One workgroup a token: drows[slot] = w dy and dweights = <dy, rows[slot]>, choice by choice, so a
-// dot product is one running sum a thread and one reduction.
+// One workgroup a token: drows[slot] = w dy and dweights = <dy, rows[slot]>, a batch of choices at a
+// time: dy is read once a batch, a dot product is one running sum a thread and one reduction.
 template <bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void combine_backward_kernel(const uint16_t* dy, int64_t lddy,
                                                                        const uint16_t* rows, int64_t ldr,
@@ -937,30 +996,42 @@ __global__ __launch_bounds__(64 * kWaves) void combine_backward_kernel(const uin
                                                                        int64_t T, int k, int64_t H, uint16_t* drows,
                                                                        int64_t lddr, float* dweights) {
     __shared__ float part[kWaves][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t t = blockIdx.x, R = T * k;
-    for (int j = 0; j < k; ++j) {
-        const int32_t slot = slots[t * k + j];
-        const int64_t r = slot >= 0 ? slot : -1 - static_cast<int64_t>(slot);
-        if (r >= R) {
-            if (lane == 0) part[wave][j] = 0.0f;
-            continue;
-        }
-        const float w = slot >= 0 ? weights[t * k + j] : 0.0f;
-        float dot = 0.0f;
+    const int32_t slot = lane < k ? slots[t * k + lane] : -1;
+    const float weight = lane < k ? weights[t * k + lane] : 0.0f;
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+        float dot[kBatch] = {};
         for (int64_t col = tid * 8; col < H; col += 64 * kWaves * 8) {
-            float g[8], f[8] = {}, d[8];
+            float g[8], f[kBatch][8];
             load8<VEC>(dy + t * lddy + col, H - col, g);
-            if (slot >= 0) load8<VEC>(rows + r * ldr + col, H - col, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                d[i] = slot >= 0 ? w * g[i] : 0.0f;
-                if (slot >= 0) dot += g[i] * f[i];
+            for (int j = 0; j < kBatch; ++j) {
+                const int32_t r = j0 + j < k ? __builtin_amdgcn_readlane(slot, j0 + j) : -1;
+                const bool there = r >= 0 && r < R;
+                load8<VEC>(rows + (there ? r * ldr : 0) + col, there ? H - col : 0, f[j]);
             }
-            store8<VEC>(drows + r * lddr + col, H - col, d);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (j0 + j >= k) continue;
+                const int32_t sl = __builtin_amdgcn_readlane(slot, j0 + j);
+                const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j0 + j));
+                const int64_t r = sl >= 0 ? sl : -1 - static_cast<int64_t>(sl);
+                if (r >= R) continue;
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    d[i] = sl >= 0 ? w * g[i] : 0.0f;
+                    if (sl >= 0) dot[j] = fmaf(g[i], f[j][i], dot[j]);
+                }
+                store8<VEC>(drows + r * lddr + col, H - col, d);
+            }
         }
-        dot = wave_sum(dot);
-        if (lane == 0) part[wave][j] = dot;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float sum = wave_sum(dot[j]);
+            if (lane == 0 && j0 + j < k) part[wave][j0 + j] = sum;
+        }
     }
     __syncthreads();
     if (tid < k) {
@@ -1056,18 +1127,19 @@ hipError_t launch_plan(const int32_t* ids, int64_t P, int E, int64_t* offsets, i
     const int64_t blocks = sched::plan_blocks(P), seg = sched::plan_segment(P);
     const PlanArgs a{ids, P, E, seg, workspace, offsets, slots, rows};
     if (blocks > 1) {
-        plan_count_kernel<<<dim3(static_cast<unsigned>(blocks)), 64 * kPlanWaves, sizeof(int32_t) * (E + 1), stream>>>(a);
+        plan_count_kernel<<<dim3(static_cast<unsigned>(blocks)), kPlanThreads, sizeof(int32_t) * (E + 1), stream>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    plan_kernel<<<dim3(static_cast<unsigned>(blocks)), 64 * kPlanWaves, sizeof(int32_t) * (E + 1) * kPlanWaves, stream>>>(a);
+    plan_kernel<<<dim3(static_cast<unsigned>(blocks)), kPlanThreads, sizeof(int32_t) * (E + 1) * (kPlanWaves + 2), stream>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_dispatch(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int k, uint8_t* q,
                            int64_t ldq, float* a_s, uint16_t* copy, int64_t ldcopy, hipStream_t stream) {
-    const int64_t chunks = (H + 1023) / 1024, blocks = (T * chunks + kWaves - 1) / kWaves;
+    const int64_t chunks = (H + 1023) / 1024, blocks = (T * chunks + 8 * kWaves - 1) / (8 * kWaves) * 8;
     if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-    const bool vec = H % 16 == 0 && rows16(x, 2 * ldx) && rows16(q, ldq) && (copy == nullptr || rows16(copy, 2 * ldcopy));
+    const bool vec = H % 8 == 0 && rows16(x, 2 * ldx) && reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0 &&
+                     (copy == nullptr || rows16(copy, 2 * ldcopy));
     const dim3 grid(static_cast<unsigned>(blocks));
     if (vec)
         dispatch_kernel<true><<<grid, 64 * kWaves, 0, stream>>>(x, T, H, ldx, slots, k, chunks, q, ldq, a_s, copy, ldcopy);

@@ -244,13 +244,12 @@ inline ColumnSplit gemm_column_split(int64_t M, int64_t N, int64_t K, int cus, i
 
 namespace sched {
 
-// Workgroups of the plan's counting sort and the pairs each takes (a multiple of 512: eight waves of
-// whole 64-pair steps): one workgroup and no counting pass up to 4096 pairs, else at most 512 of at
-// least 2048 pairs.
+// The plan's counting sort: workgroups of eight waves take their pairs in rounds of 2048 (four steps of
+// 64 a wave). One workgroup and no counting pass up to two rounds, else at most 512 workgroups.
+constexpr int kPlanWaves = 8, kPlanRound = 2048;
 inline int64_t plan_segment(int64_t P) {
-    if (P <= 4096) return cdiv(P > 0 ? P : 1, 512) * 512;
-    const int64_t per = cdiv(P, 512);
-    return cdiv(per < 2048 ? 2048 : per, 512) * 512;
+    if (P <= 2 * kPlanRound) return 2 * kPlanRound;
+    return cdiv(cdiv(P, 512), kPlanRound) * kPlanRound;
 }
 inline int64_t plan_blocks(int64_t P) { return P > 0 ? cdiv(P, plan_segment(P)) : 1; }
 
