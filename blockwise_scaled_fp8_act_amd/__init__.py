@@ -5,7 +5,9 @@ bf16 to float8_e4m3fn (or float8_e4m3fnuz, ``fmt="e4m3fnuz"``) with fp32 scales,
 1x128 x 128x128 / 1x128 x 128x1 scaled FP8 GEMMs with bf16 output, as hand-written HIP kernels
 behind the C ABI of include/blockwise_fp8.h. This package is the thin Python binding over that
 library (``binding``), the blockwise-FP8 linear layer composed from those kernels for training
-(``linear``), its in-tree build (``build``) and the seeded input generators (``inputs``).
+(``linear``), the gated mixture-of-experts layer for training and serving composed from the routing,
+dispatch, expert-product and combine kernels (``moe``), its in-tree build (``build``) and the seeded
+input generators (``inputs``).
 """
 from .binding import (  # noqa: F401
     Bsfp8Error,
@@ -33,3 +35,4 @@ from .binding import (  # noqa: F401
     quantize_weight_128x128,
 )
 from .linear import BlockwiseFp8Linear, blockwise_fp8_linear  # noqa: F401
+from .moe import BlockwiseFp8MoE, ServingMoE, blockwise_fp8_moe, route_experts  # noqa: F401

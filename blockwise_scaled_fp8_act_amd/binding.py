@@ -186,7 +186,7 @@ def _matrix(name, t, dtypes, shape=None):
     if shape is not None and any(w is not None and g != w for g, w in zip(t.shape, shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
                          f"{tuple('*' if w is None else w for w in shape)}")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    if t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0] > 0:
         raise ValueError(f"{name} must have contiguous rows (stride {t.stride()})")
     return t
 
