@@ -235,11 +235,14 @@ namespace tiled {
 constexpr int kTM = 64, kTN = 128, kWaves = 8;
 constexpr int kB = kTM * 8, kSA = kB + kTN * 8, kSB = kSA + 16, kStage = kSB + 16;  // in 16-byte units
 
-// A direct load to LDS address lds + BYTES * lane, BYTES (4 or 16) a lane.
-template <int BYTES>
+// A direct load to LDS address lds + BYTES * lane, BYTES (4 or 16) a lane; STREAM: past the caches.
+template <int BYTES, bool STREAM = false>
 __device__ __forceinline__ void dma(uint32_t lds, const void* p) {
     uint32_t saved;
-    if (BYTES == 16)
+    if (BYTES == 16 && STREAM)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %2, off sc1 nt\n\ts_mov_b32 m0, %0"
+                     : "=&s"(saved) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
+    else if (BYTES == 16)
         asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
                      : "=&s"(saved) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
     else
@@ -263,7 +266,8 @@ __device__ __forceinline__ void wait_block(int later) {
     }
 }
 
-template <int S, bool SWIGLU>
+// STREAM: B past the caches, where an expert's rows fit one tile and its weights are read once.
+template <int S, bool SWIGLU, bool STREAM>
 __global__ __launch_bounds__(64 * kWaves) void routed_kernel(RoutedArgs a) {
     __shared__ u32x4 smem[S * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -303,8 +307,8 @@ __global__ __launch_bounds__(64 * kWaves) void routed_kernel(RoutedArgs a) {
         const uint32_t base = lds0 + static_cast<uint32_t>(stage * kStage * 16);
         const int64_t adv = static_cast<int64_t>(kb) * kGroup;
         dma<16>(base + 64 * wave * 16, ap + adv);
-        dma<16>(base + (kB + 128 * wave) * 16, bp[0] + adv);
-        dma<16>(base + (kB + 128 * wave + 64) * 16, bp[1] + adv);
+        dma<16, STREAM>(base + (kB + 128 * wave) * 16, bp[0] + adv);
+        dma<16, STREAM>(base + (kB + 128 * wave + 64) * 16, bp[1] + adv);
         if (wave < 2) dma<4>(base + (wave == 0 ? kSA : kSB) * 16, sp + kb * s_step);
     };
 
@@ -365,12 +369,16 @@ __global__ __launch_bounds__(64 * kWaves) void routed_kernel(RoutedArgs a) {
 }
 
 template <int S, bool SWIGLU>
-hipError_t launch(RoutedArgs a, hipStream_t stream) {
+hipError_t launch(RoutedArgs a, bool once, hipStream_t stream) {
     constexpr int64_t kOut = SWIGLU ? kTN / 2 : kTN;
     a.col_tiles = (a.N + kOut - 1) / kOut;
     const int64_t blocks = sched::routed_row_tiles(a.M, a.E, kTM) * a.col_tiles;
     if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-    routed_kernel<S, SWIGLU><<<dim3(static_cast<unsigned>(blocks)), 64 * kWaves, 0, stream>>>(a);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (once)
+        routed_kernel<S, SWIGLU, true><<<grid, 64 * kWaves, 0, stream>>>(a);
+    else
+        routed_kernel<S, SWIGLU, false><<<grid, 64 * kWaves, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -380,10 +388,11 @@ hipError_t launch(RoutedArgs a, hipStream_t stream) {
 
 hipError_t launch_gemm_routed(RoutedArgs a, bool swiglu, hipStream_t stream) {
     a.c_vec = (reinterpret_cast<uintptr_t>(a.c) % 8 == 0) && a.ldc % 4 == 0;
+    const bool once = sched::routed_reads_once(a.M, a.E);
     switch (sched::routed_kernel(a.M, a.N, a.E, swiglu, device_cus())) {
         case sched::kRoutedRegisters16: return swiglu ? launch<1, 2, 4, 3, true>(a, stream) : launch<1, 2, 4, 3, false>(a, stream);
         case sched::kRoutedRegisters32: return swiglu ? launch<2, 2, 4, 3, true>(a, stream) : launch<2, 2, 4, 3, false>(a, stream);
-        default: return swiglu ? tiled::launch<3, true>(a, stream) : tiled::launch<3, false>(a, stream);
+        default: return swiglu ? tiled::launch<3, true>(a, once, stream) : tiled::launch<3, false>(a, once, stream);
     }
 }
 
