@@ -16,6 +16,7 @@ Tensor conventions (torch, on the GPU):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -657,10 +658,15 @@ def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream
 
 def moe_plan_workspace(T, k, E):
     """Bytes of device memory moe_plan needs for T tokens, k choices and E experts."""
-    need = lib().moe_plan_workspace(T, k, E)
+    need = _plan_bytes(T, k, E)
     if need < 0:
         raise ValueError(f"no plan for T = {T}, k = {k}, E = {E}")
     return need
+
+
+@functools.lru_cache(maxsize=1024)      # sizes alone decide it
+def _plan_bytes(T, k, E):
+    return lib().moe_plan_workspace(T, k, E)
 
 
 def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=None):

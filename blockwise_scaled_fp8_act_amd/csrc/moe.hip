@@ -3,6 +3,8 @@
 // into expert order with their 1x128 quantization, and the weighted return of the experts' rows
 // (forward and backward). Definitions and layouts: blockwise_fp8.h. All are bound by memory traffic
 // or by launch latency; none allocates, and no result depends on the order of atomics.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -59,6 +61,8 @@ struct RouteArgs {
     float* weights;
     int32_t* ids;
     int vec, bias_vec;  // rows of the logits, the bias are 16-byte aligned
+    int size;           // experts a group
+    int shift;          // a group is 2^shift of a kernel's runs; -1: it is not
 };
 
 // One token, by a whole wave, everything in 64 bits; lane l holds the experts l, l + 64, ... . `lds`:
@@ -180,8 +184,8 @@ __device__ __forceinline__ void route_token(const LT* row, int64_t t, const Rout
     }
 }
 
-// Every rule the kernel below does not take: more than 16 choices, softmax scores with a bias, more
-// groups than its lanes. One wave a token.
+// Every rule the kernel below does not take: more than 16 choices, more groups than its lanes. One wave
+// a token.
 template <typename LT, int V>
 __global__ __launch_bounds__(64 * kWaves) void route_wide_kernel(const LT* logits, RouteArgs a) {
     extern __shared__ double lds[];
@@ -300,8 +304,11 @@ __device__ __forceinline__ void load_run(const uint16_t* p, bool vec, int left, 
 
 // The largest error of a sigmoid from the hardware's exp2 and reciprocal (each within one unit of the
 // last place; scores are at most 1) and of adding a bias to it.
-constexpr float kKeyError = 4.8e-7f;   // 2^-21
-constexpr float kKeyRounding = 6e-8f;  // 2^-24, of the key
+enum RouteKey { kKeyLogit, kKeySigmoid, kKeySoftmax };
+constexpr float kSigmoidError = 4.8e-7f;  // 2^-21
+// That of a softmax: its sum's error, at most 10 roundings deep, and its own; scores are at most 1.
+constexpr float kSoftmaxError = 2e-6f;    // 2^-19
+constexpr float kKeyRounding = 6e-8f;     // 2^-24, of the key
 
 // L lanes a token (16, four tokens a wave, up to 256 experts; 64 up to 1024), V consecutive experts a
 // lane. Candidates come from fp32 keys cut to make room for the expert's index in the low bits: then
@@ -310,11 +317,12 @@ constexpr float kKeyRounding = 6e-8f;  // 2^-24, of the key
 // cut keys to order them, the candidates are ranked by their exact keys, one a lane. Where the cut
 // keys cannot tell that the k best are among the candidates (three keys nearly equal at the border),
 // the choices are made one by one from 64-bit keys; where fp32 cannot tell which groups are kept,
-// the groups are valued again in 64 bits. BIAS: keys sigmoid +
-// bias, else the logits, which are exact.
-template <typename LT, int V, int L, bool BIAS>
+// the groups are valued again in 64 bits. KEY: the
+// logits, which are exact, or a score + bias.
+template <typename LT, int V, int L, RouteKey KEY>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, RouteArgs a) {
     extern __shared__ double lds[];
+    constexpr bool BIAS = KEY != kKeyLogit, SOFTMAX_KEY = KEY == kKeySoftmax;
     constexpr int kTokens = 64 / L;
     constexpr uint32_t kIndex = L * V - 1;  // low bits of a packed key
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -330,31 +338,21 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
 
     float z[V];
     load_run<V>(row + e0, a.vec && E % 4 == 0, E - e0, z);
+    float key[V];  // starts as the bias: on the way with the logits
+    if (BIAS) load_run<V>(a.bias + e0, a.bias_vec && E % 4 == 0, E - e0, key);
     bool bad = false;
     uint32_t low = 0;  // bits that the cut keys lose
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        z[v] += 0.0f;  // -0 and 0 are the same logit
+        if (!BIAS) z[v] += 0.0f;  // -0 and 0 are the same key
         bad = bad || z[v] != z[v] || (a.softmax && z[v] == INFINITY);
         low |= z[v] == -INFINITY ? 0u : __float_as_uint(z[v]) & kIndex;
     }
     bad = team_any(bad);
     const bool exact = !BIAS && (sizeof(LT) == 2 || !team_any(low != 0));
 
-    float key[V];
-    if (BIAS) load_run<V>(a.bias + e0, a.bias_vec && E % 4 == 0, E - e0, key);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (BIAS) {
-            key[v] += __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[v] * -1.44269504f));
-            key[v] = key[v] != key[v] || z[v] == -INFINITY ? -INFINITY : key[v];
-        } else {
-            key[v] = z[v];
-        }
-    }
-
-    float total = 1.0f, top = 0.0f;
-    if (a.softmax && !a.renormalize) {
+    float total = 1.0f, top = 0.0f;  // softmax: the row's sum of exp(z - top)
+    if (SOFTMAX_KEY || (!BIAS && a.softmax && !a.renormalize)) {
         uint32_t m = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
@@ -364,22 +362,57 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         for (int v = 0; v < V; ++v) total += z[v] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((z[v] - top) * 1.44269504f);
         total = team_sum<L>(total);
     }
+    constexpr float key_error = SOFTMAX_KEY ? kSoftmaxError : kSigmoidError;
+    if (BIAS) {
+        if (SOFTMAX_KEY) {
+            const float inverse = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] += __builtin_amdgcn_exp2f((z[v] - top) * 1.44269504f) * inverse;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                key[v] += __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[v] * -1.44269504f));
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] != key[v] || z[v] == -INFINITY ? -INFINITY : key[v];
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = z[v];
+    }
+    // The exact key of an expert: score in 64 bits + bias. The softmax's sum in 64 bits is made where a
+    // key is first asked for (wave-uniform: prepare_exact before exact_key).
+    double total64 = 0.0;
+    const auto prepare_exact = [&]() {
+        if (!SOFTMAX_KEY || total64 != 0.0) return;
+        double sum = 0.0;
+#pragma unroll 1
+        for (int v = 0; v < V && e0 + v < E; ++v) {
+            const float x = load_logit(row + e0 + v);
+            sum += x == -INFINITY ? 0.0 : exp(static_cast<double>(x) - top);
+        }
+#pragma unroll 1
+        for (int x = 1; x < L; x <<= 1) sum += __shfl_xor(sum, x);
+        total64 = sum;
+    };
+    const auto exact_key = [&](float x, int e) -> double {
+        if (!BIAS) return x + 0.0f;
+        const double y = exp(SOFTMAX_KEY ? static_cast<double>(x) - top : -static_cast<double>(x));
+        return (SOFTMAX_KEY ? y / total64 : 1.0 / (1.0 + y)) + static_cast<double>(a.bias[e]);
+    };
 
     // doubles of LDS a token has: its keys, a group's run padded to an odd length, and the groups' values
-    const int size = E / a.groups, pitch = size | 1, area = a.groups * (pitch + 1);
+    const int size = a.size, pitch = size | 1, area = a.groups * (pitch + 1);
     uint32_t dropped = 0;  // bit v: the group of expert e0 + v is not kept
     if (a.groups > 1) {
         double* const mine64 = lds + static_cast<int64_t>(wave * kTokens + team) * area;
         float* const mine = reinterpret_cast<float*>(mine64);
         float* const value = mine + a.groups * pitch;
         // a group of whole runs, 1, 2, 4, 8 or 16 of them, is valued in registers; any other through LDS
-        const int runs = size / V;
-        const bool regular = size % V == 0 && (runs & (runs - 1)) == 0 && runs <= 16;
-        const int shift = regular ? __builtin_ctz(runs) : 0;
+        const bool regular = a.shift >= 0;
         float first = -INFINITY, second = -INFINITY;
         int group = sub;  // the group this lane values
         if (regular) {
-            group = sub >> shift;
+            group = sub >> a.shift;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 second = __builtin_amdgcn_fmed3f(first, second, key[v]);
@@ -393,10 +426,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
 #define BSFP8_JOIN(ctrl)                                                                              \
     join(__builtin_amdgcn_update_dpp(0, __float_as_uint(first), ctrl, 0xF, 0xF, false),               \
          __builtin_amdgcn_update_dpp(0, __float_as_uint(second), ctrl, 0xF, 0xF, false))
-            if (runs >= 2) BSFP8_JOIN(0xB1);
-            if (runs >= 4) BSFP8_JOIN(0x4E);
-            if (runs >= 8) BSFP8_JOIN(0x141);
-            if (runs >= 16) BSFP8_JOIN(0x140);
+            if (a.shift >= 1) BSFP8_JOIN(0xB1);
+            if (a.shift >= 2) BSFP8_JOIN(0x4E);
+            if (a.shift >= 3) BSFP8_JOIN(0x141);
+            if (a.shift >= 4) BSFP8_JOIN(0x140);
 #undef BSFP8_JOIN
         } else {
             // lane g reads run g, at an odd distance from its neighbours: no bank twice
@@ -425,7 +458,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         float tol = 0.0f;
         if (BIAS) {
             const float big = fmaxf(fabsf(first), second == -INFINITY ? 0.0f : fabsf(second));
-            tol = first == -INFINITY ? 0.0f : 4.0f * (kKeyError + kKeyRounding * big);
+            tol = first == -INFINITY ? 0.0f : 4.0f * (key_error + kKeyRounding * big);
             if (second != -INFINITY) first += second;
         }
         wave_lds_fence();
@@ -447,12 +480,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         bool lanes_keep = regular;  // keep is about the lane's own experts
         if (BIAS && __any(keep && maybe > a.top_groups && !bad)) {
             wave_lds_fence();
+            prepare_exact();
             double* const value64 = mine64 + a.groups * pitch;
             int g = e0 / size, i = e0 - g * size;
 #pragma unroll 1
             for (int v = 0; v < V && e0 + v < E; ++v) {
                 const float x = load_logit(row + e0 + v);
-                double y = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(a.bias[e0 + v]);
+                const double y = exact_key(x, e0 + v);
                 mine64[g * pitch + i] = x == -INFINITY || y != y ? -INFINITY : y;
                 if (++i == size) {
                     i = 0;
@@ -508,14 +542,19 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
 
     const int m = min(k + 2, 16);
     uint32_t mine = 0, at_k = 0;  // lane j: the j-th candidate; every lane: the k-th
-    for (int j = 0; j < m; ++j) {
+    const auto take = [&](int j, auto depth) {  // the best head; its run moves up, as far as m takes can reach
+        constexpr int kDepth = decltype(depth)::value < V ? decltype(depth)::value : V;
         const uint32_t best = team_umax<L>(run[0]);
         if (sub == j) mine = best;
         if (j == k - 1) at_k = best;
         const uint32_t own = run[0] == best ? ~0u : 0u;  // a bit select: "own ? a : b" becomes an indexed read
 #pragma unroll
-        for (int v = 0; v + 1 < V; ++v) run[v] = (run[v + 1] & own) | (run[v] & ~own);
-        run[V - 1] &= ~own;
+        for (int v = 0; v < kDepth; ++v) run[v] = ((v + 1 < V ? run[v + 1 < V ? v + 1 : v] : 0u) & own) | (run[v] & ~own);
+    };
+    if (m <= 10) {
+        for (int j = 0; j < m; ++j) take(j, std::integral_constant<int, 10>{});
+    } else {
+        for (int j = 0; j < m; ++j) take(j, std::integral_constant<int, 16>{});
     }
     const uint32_t next = team_umax<L>(run[0]);
 
@@ -524,7 +563,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         if (exact || y < kLeastKey) return false;
         if (!BIAS) return (x & ~kIndex) == (y & ~kIndex);
         const float f = from_ordered(x & ~kIndex), h = from_ordered(y & ~kIndex), big = fmaxf(fabsf(f), fabsf(h));
-        return !(f - h > 2.0f * (kKeyError + kKeyRounding * big) + big * (2.0f * (kIndex + 1) * 1.1920929e-7f));
+        return !(f - h > 2.0f * (key_error + kKeyRounding * big) + big * (2.0f * (kIndex + 1) * 1.1920929e-7f));
     };
     const bool open = close(at_k, next);  // an expert that is no candidate may be among the k best
     const uint32_t after = __builtin_amdgcn_update_dpp(0, mine, 0x101, 0xF, 0xF, false);  // the next lane's
@@ -534,19 +573,20 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
     float zc = have ? load_logit(row + id) : -INFINITY;
     int rank = sub;
     if (__any(have && sub < k && close(mine, after))) {  // by the exact keys
-        double full = zc + 0.0f;
-        if (BIAS && have) full = 1.0 / (1.0 + exp(-static_cast<double>(zc))) + static_cast<double>(a.bias[id]);
+        prepare_exact();
+        double full = -INFINITY;
+        if (have) full = exact_key(zc, id);
         rank = rank_row16(full, id);  // lanes without a candidate: -inf, last
     }
     bool chosen = have && rank < k;
     if (__any(open && live && !bad)) {  // choice by choice from 64-bit keys in LDS
         double* const key64 = lds + static_cast<int64_t>(wave * kTokens + team) * area;
         wave_lds_fence();
+        prepare_exact();
 #pragma unroll 1
         for (int v = 0; v < V && e0 + v < E; ++v) {
             const float x = load_logit(row + e0 + v);
-            double y = x + 0.0f;
-            if (BIAS) y = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(a.bias[e0 + v]);
+            const double y = exact_key(x, e0 + v);
             key64[e0 + v] = x == -INFINITY || y != y || ((dropped >> v) & 1) ? -INFINITY : y;
         }
         int found = -1;
@@ -1055,14 +1095,18 @@ static hipError_t route_wide(const LT* logits, const RouteArgs& a, hipStream_t s
 }
 
 template <typename LT, int V, int L>
-static hipError_t route_teams(const LT* logits, const RouteArgs& a, hipStream_t stream) {
+static hipError_t route_teams(const LT* logits, RouteArgs a, hipStream_t stream) {
+    const int runs = a.size / V;
+    a.shift = a.size % V == 0 && (runs & (runs - 1)) == 0 && runs <= 16 ? __builtin_ctz(runs) : -1;
     const int64_t per = kWaves * (64 / L), blocks = (a.T + per - 1) / per;
-    const size_t lds = sizeof(double) * per * a.groups * ((a.E / a.groups | 1) + 1);
+    const size_t lds = sizeof(double) * per * a.groups * ((a.size | 1) + 1);
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (a.bias != nullptr)
-        route_kernel<LT, V, L, true><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
+    if (a.bias == nullptr)
+        route_kernel<LT, V, L, kKeyLogit><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
+    else if (a.softmax)
+        route_kernel<LT, V, L, kKeySoftmax><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
     else
-        route_kernel<LT, V, L, false><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
+        route_kernel<LT, V, L, kKeySigmoid><<<grid, 64 * kWaves, lds, stream>>>(logits, a);
     return hipGetLastError();
 }
 
@@ -1086,7 +1130,7 @@ static hipError_t route_backward_v(const LT* logits, int64_t T, int E, int64_t l
 template <typename LT>
 static hipError_t route_t(const LT* logits, const RouteArgs& a, hipStream_t stream) {
     const int E = a.E;
-    const bool wide = a.k > 16 || (a.softmax && a.bias != nullptr) || a.groups > (E <= 256 ? 16 : 64);
+    const bool wide = a.k > 16 || a.groups > (E <= 256 ? 16 : 64);
     if (wide) {
 #define CALL(V) route_wide<LT, V>(logits, a, stream)
         return BSFP8_BY_EXPERTS(CALL);
@@ -1111,7 +1155,7 @@ static hipError_t route_backward_t(const void* logits, int64_t T, int E, int64_t
 hipError_t launch_route(const void* logits, bool f32, int64_t T, int E, int64_t ld, const RouteRule& r, const float* bias,
                         float* weights, int32_t* ids, hipStream_t stream) {
     const RouteArgs a{T, E, ld, bias, r.softmax, r.k, r.groups, r.top_groups, r.renormalize, r.scale, weights, ids,
-                      rows16(logits, ld * (f32 ? 4 : 2)), rows16(bias, 0)};
+                      rows16(logits, ld * (f32 ? 4 : 2)), rows16(bias, 0), E / r.groups, -1};
     return f32 ? route_t(static_cast<const float*>(logits), a, stream) : route_t(static_cast<const uint16_t*>(logits), a, stream);
 }
 

@@ -447,10 +447,13 @@ def test_layer_on_another_stream_equals_the_current_one():
     args = _layer_inputs(1, 24, 16, 4, 256, 512)
     want = _layer(*args)
     torch.cuda.synchronize()
-    for how in ("stream", "handle", "context"):
-        s = torch.cuda.Stream()
+    for how in ("stream", "handle", "context", "default"):
+        s = torch.cuda.default_stream() if how == "default" else torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
-        if how == "context":
+        if how == "default":
+            with torch.cuda.stream(torch.cuda.Stream()):       # another stream is current
+                got = _layer(*args, stream=s.cuda_stream)
+        elif how == "context":
             with torch.cuda.stream(s):
                 got = _layer(*args)
         else:
