@@ -178,6 +178,12 @@ def _on_gpu(name, t, dev=None):
 
 def _matrix(name, t, dtypes, shape=None):
     """A 2-D tensor of one of ``dtypes`` with contiguous rows; ``shape`` entries of None are free."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes:       # what passes, in few steps
+        got = t.shape
+        if len(got) == 2 and (shape is None or ((shape[0] is None or got[0] == shape[0])
+                                                and (shape[1] is None or got[1] == shape[1]))):
+            if t.stride(1) == 1 or got[1] <= 1 or got[0] == 0:
+                return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -545,19 +551,29 @@ def _empty(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _current(first, *rest):
+    """The current GPU's index if every tensor (None: skipped) is on it, else None."""
+    dev = first.get_device()            # -1: not a GPU tensor
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            return None
+    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else None
+
+
 def _choices(name, t, dtype):
     """A contiguous [T, k] tensor of ``dtype`` with 1 <= k <= MAX_CHOICES; returns (T, k)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or not 1 <= t.shape[1] <= MAX_CHOICES:
-        raise ValueError(f"{name} must be [T, k] with 1 <= k <= {MAX_CHOICES}, got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or not 1 <= shape[1] <= MAX_CHOICES:
+        raise ValueError(f"{name} must be [T, k] with 1 <= k <= {MAX_CHOICES}, got shape {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() >= 2 ** 31:
-        raise ValueError(f"{name} has {t.numel()} pairs, at most 2^31 - 1 are numbered")
-    return t.shape
+    if shape[0] * shape[1] >= 2 ** 31:
+        raise ValueError(f"{name} has {shape[0] * shape[1]} pairs, at most 2^31 - 1 are numbered")
+    return shape
 
 
 def _route_args(logits, k, score, scale):
@@ -594,7 +610,9 @@ def moe_route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, ren
         ids = _empty(logits, (T, k), torch.int32, stream)
     else:
         _dense("ids", ids, torch.int32, (T, k))
-    dev = _gpu(logits=logits, bias=bias, weights=weights, ids=ids)
+    dev = _current(logits, bias, weights, ids)
+    if dev is None:
+        _gpu(logits=logits, bias=bias, weights=weights, ids=ids)          # says which one
     _call("moe_route", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _ptr(bias), _SCORES[score], k,
           groups, top_groups, int(bool(renormalize)), scale, _ptr(weights), _ptr(ids), _stream(stream, dev))
     return weights, ids
@@ -612,7 +630,9 @@ def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True,
         dlogits = _empty(logits, (T, E), logits.dtype, stream)
     else:
         _matrix("dlogits", dlogits, (logits.dtype,), (T, E))
-    dev = _gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+    dev = _current(logits, ids, dweights, dlogits)
+    if dev is None:
+        _gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)          # says which one
     _call("moe_route_backward", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _SCORES[score], k,
           int(bool(renormalize)), scale, _ptr(ids), _ptr(dweights), _ptr(dlogits), _row_stride(dlogits),
           _stream(stream, dev))
@@ -650,7 +670,9 @@ def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream
         size = workspace.numel()
         if size < need:
             raise ValueError(f"workspace holds {size} bytes, the plan needs {need}")
-    dev = _gpu(ids=ids, offsets=offsets, slots=slots, rows=rows, workspace=workspace)
+    dev = _current(ids, offsets, slots, rows, workspace)
+    if dev is None:
+        _gpu(ids=ids, offsets=offsets, slots=slots, rows=rows, workspace=workspace)          # says which one
     _call("moe_plan", _ptr(ids), T, k, E, _ptr(offsets), _ptr(slots), _ptr(rows), _ptr(workspace), size,
           _stream(stream, dev))
     return offsets, slots, rows
@@ -688,7 +710,9 @@ def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=
         _matrix("copy", copy, _BF16, (R, H))
     elif want_copy:
         copy = _empty(x, (R, H), torch.bfloat16, stream)
-    dev = _gpu(x=x, slots=slots, q=q, a_s=a_s, copy=copy)
+    dev = _current(x, slots, q, a_s, copy)
+    if dev is None:
+        _gpu(x=x, slots=slots, q=q, a_s=a_s, copy=copy)          # says which one
     _call("moe_dispatch", _ptr(x), T, H, _row_stride(x), _ptr(slots), k, _ptr(q), _row_stride(q), _ptr(a_s), _ptr(copy),
           _row_stride(copy) if copy is not None else 0, _stream(stream, dev))
     return q, a_s, copy
@@ -705,7 +729,9 @@ def moe_combine(rows, slots, weights=None, y=None, stream=None):
         y = _empty(rows, (T, H), torch.bfloat16, stream)
     else:
         _matrix("y", y, _BF16, (T, H))
-    dev = _gpu(rows=rows, slots=slots, weights=weights, y=y)
+    dev = _current(rows, slots, weights, y)
+    if dev is None:
+        _gpu(rows=rows, slots=slots, weights=weights, y=y)          # says which one
     _call("moe_combine", _ptr(rows), R, _row_stride(rows), _ptr(slots), _ptr(weights), T, k, H, _ptr(y), _row_stride(y),
           _stream(stream, dev))
     return y
@@ -727,7 +753,9 @@ def moe_combine_backward(dy, rows, slots, weights, drows=None, dweights=None, st
         dweights = _empty(dy, (T, k), torch.float32, stream)
     else:
         _dense("dweights", dweights, torch.float32, (T, k))
-    dev = _gpu(dy=dy, rows=rows, slots=slots, weights=weights, drows=drows, dweights=dweights)
+    dev = _current(dy, rows, slots, weights, drows, dweights)
+    if dev is None:
+        _gpu(dy=dy, rows=rows, slots=slots, weights=weights, drows=drows, dweights=dweights)          # says which one
     _call("moe_combine_backward", _ptr(dy), _row_stride(dy), _ptr(rows), _row_stride(rows), _ptr(slots), _ptr(weights), T, k,
           H, _ptr(drows), _row_stride(drows), _ptr(dweights), _stream(stream, dev))
     return drows, dweights
@@ -783,7 +811,9 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
         need = (E - 1) * bs_stride + (cdiv(halves * N, BLOCK) - 1) * bs_stride_nb + (K // BLOCK - 1) * bs_stride_kb + 1
         if need > b_s.numel():
             raise ValueError(f"b_s holds {b_s.numel()} floats, E, N, K and the strides read {need}")
-    dev = _gpu(a=a, a_s=a_s, b=b, b_s=b_s, offsets=offsets, rows=rows, c=c)
+    dev = _current(a, a_s, b, b_s, offsets, rows, c)
+    if dev is None:
+        _gpu(a=a, a_s=a_s, b=b, b_s=b_s, offsets=offsets, rows=rows, c=c)          # says which one
     _call("gemm_1x128_128x128_routed", _ptr(a), _row_stride(a), _ptr(a_s), A, _ptr(rows), k, _ptr(b), ldb, b_stride,
           _ptr(b_s), bs_stride, bs_stride_nb, bs_stride_kb, _ptr(offsets), E, _ptr(c), _row_stride(c), M, N, K,
           int(bool(swiglu)), _stream(stream, dev))
