@@ -728,8 +728,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* l
 // lane per distinct bin advances the wave's own counter, so no atomics decide an order. With more
 // than one workgroup a first kernel counts each workgroup's bins, and every workgroup sums the
 // counts it needs.
-constexpr int kPlanWaves = sched::kPlanWaves, kPlanSteps = sched::kPlanRound / (64 * kPlanWaves);
-constexpr int kPlanThreads = 64 * kPlanWaves;
+using sched::kPlanSteps;
+constexpr int kCountThreads = 512;
 
 struct PlanArgs {
     const int32_t* ids;
@@ -744,27 +744,28 @@ struct PlanArgs {
 
 __device__ __forceinline__ int plan_bin(int32_t id, int E) { return id >= 0 && id < E ? id : E; }
 
-__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
+__global__ __launch_bounds__(kCountThreads) void plan_count_kernel(PlanArgs a) {
     extern __shared__ int32_t hist[];
     const int tid = threadIdx.x, bins = a.E + 1;
-    for (int b = tid; b < bins; b += kPlanThreads) hist[b] = 0;
+    for (int b = tid; b < bins; b += kCountThreads) hist[b] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * a.seg, hi = min(lo + a.seg, a.P);
-    for (int64_t p0 = lo; p0 < hi; p0 += sched::kPlanRound) {
+    for (int64_t p0 = lo; p0 < hi; p0 += kPlanSteps * kCountThreads) {
         int32_t id[kPlanSteps];
 #pragma unroll
-        for (int s = 0; s < kPlanSteps; ++s) id[s] = p0 + s * kPlanThreads + tid < hi ? a.ids[p0 + s * kPlanThreads + tid] : 0;
+        for (int s = 0; s < kPlanSteps; ++s) id[s] = p0 + s * kCountThreads + tid < hi ? a.ids[p0 + s * kCountThreads + tid] : 0;
 #pragma unroll
         for (int s = 0; s < kPlanSteps; ++s)
-            if (p0 + s * kPlanThreads + tid < hi) atomicAdd(&hist[plan_bin(id[s], a.E)], 1);
+            if (p0 + s * kCountThreads + tid < hi) atomicAdd(&hist[plan_bin(id[s], a.E)], 1);
     }
     __syncthreads();
-    for (int b = tid; b < bins; b += kPlanThreads) a.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = hist[b];
+    for (int b = tid; b < bins; b += kCountThreads) a.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = hist[b];
 }
 
 // Lanes of this wave whose bin equals this lane's, among the lanes of `active`.
 __device__ __forceinline__ uint64_t same_bin(int bin, int bits, uint64_t active) {
     uint64_t m = active;
+#pragma unroll 4
     for (int i = 0; i < bits; ++i) {
         const uint64_t one = __ballot((bin >> i) & 1);
         m &= (bin >> i) & 1 ? one : ~one;
@@ -772,38 +773,38 @@ __device__ __forceinline__ uint64_t same_bin(int bin, int bits, uint64_t active)
     return m;
 }
 
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
+template <int W>
+__global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
+    constexpr int kThreads = 64 * W, kRound = sched::plan_round(W);
     extern __shared__ int32_t bin_lds[];
-    __shared__ int32_t wave_total[kPlanWaves];
+    static_assert(kRound <= 0xFFFF, "a wave's place in a bin is kept in 16 bits");
+    __shared__ int32_t wave_total[W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = a.E + 1;
     const int bits = 32 - __builtin_clz(a.E);  // E itself needs a place
-    int32_t* const wave_bins = bin_lds;                  // [kPlanWaves][bins]: counts, then first rows
-    int32_t* const next = wave_bins + kPlanWaves * bins;       // [bins]: this workgroup's next row of a bin
-    int32_t* const all = next + bins;                    // [bins]: pairs of a bin, with more than one workgroup
+    int32_t* const next = bin_lds;     // [bins]: this workgroup's next row of a bin
+    int32_t* const all = next + bins;  // [bins]: pairs of a bin
+    // [W][bins]: a wave's pairs of a bin in this round, then those of the waves before it
+    uint16_t* const wave_bins = reinterpret_cast<uint16_t*>(all + bins);
     const int64_t lo = blockIdx.x * a.seg, hi = min(lo + a.seg, a.P);
-    const bool many = gridDim.x > 1, rounds = hi - lo > sched::kPlanRound;
-    int32_t* const own = wave_bins + wave * bins;
+    const bool many = gridDim.x > 1;
+    uint16_t* const own = wave_bins + wave * bins;
     const uint64_t below = (uint64_t{1} << lane) - 1;
 
-    for (int64_t p0 = lo; p0 == lo || p0 < hi; p0 += sched::kPlanRound) {
+    for (int64_t p0 = lo; p0 == lo || p0 < hi; p0 += kRound) {
         // a short round is spread over all waves
-        const int steps = static_cast<int>((min(hi - p0, int64_t{sched::kPlanRound}) + kPlanThreads - 1) / kPlanThreads);
+        const int steps = static_cast<int>((min(hi - p0, int64_t{kRound}) + kThreads - 1) / kThreads);
         const int64_t mine = p0 + wave * 64 * steps + lane;
         int32_t id[kPlanSteps], rank[kPlanSteps];
 #pragma unroll
         for (int s = 0; s < kPlanSteps; ++s) id[s] = s < steps && mine + 64 * s < hi ? a.ids[mine + 64 * s] : 0;
-        for (int b = tid; b < bins * kPlanWaves; b += kPlanThreads) wave_bins[b] = 0;
-        if (p0 == lo && (many || rounds)) {
-            for (int b = tid; b < bins; b += kPlanThreads) next[b] = all[b] = 0;
-            __syncthreads();
-        }
-        if (p0 == lo && !many && rounds)
-            for (int64_t p = tid; p < hi; p += kPlanThreads) atomicAdd(&all[plan_bin(a.ids[p], a.E)], 1);
+        for (int b = tid; b < bins * W; b += kThreads) wave_bins[b] = 0;
         if (p0 == lo && many) {
             // bins of all workgroups, and of those before this one: parts of the workgroups side by side
-            const int parts = bins < kPlanThreads ? kPlanThreads / bins : 1, part = bins < kPlanThreads ? tid / bins : 0;
+            for (int b = tid; b < bins; b += kThreads) next[b] = all[b] = 0;
+            __syncthreads();
+            const int parts = bins < kThreads ? kThreads / bins : 1, part = bins < kThreads ? tid / bins : 0;
             if (part < parts)
-                for (int b = bins < kPlanThreads ? tid - part * bins : tid; b < bins; b += kPlanThreads) {
+                for (int b = bins < kThreads ? tid - part * bins : tid; b < bins; b += kThreads) {
                     int32_t total = 0, before = 0;
 #pragma unroll 8
                     for (int g = part; g < static_cast<int>(gridDim.x); g += parts) {
@@ -825,20 +826,21 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
             const uint64_t m = same_bin(id[s], bits, __ballot(in));
             rank[s] = own[id[s]] + __popcll(m & below);
             wave_lds_fence();
-            if (in && (m & below) == 0) own[id[s]] = rank[s] + __popcll(m);
+            if (in && (m & below) == 0) own[id[s]] = static_cast<uint16_t>(rank[s] + __popcll(m));
             wave_lds_fence();
         }
         __syncthreads();
         // first round: where each bin starts (bins in runs of the workgroup's threads, carried on)
         if (p0 == lo) {
             int32_t carry = 0;
-            for (int b0 = 0; b0 < bins; b0 += kPlanThreads) {
+            for (int b0 = 0; b0 < bins; b0 += kThreads) {
                 const int b = b0 + tid;
                 int32_t n = 0;
                 if (b < bins) {
-                    if (many || rounds) n = all[b];
+                    if (many) n = all[b];
                     else
-                        for (int w = 0; w < kPlanWaves; ++w) n += wave_bins[w * bins + b];
+#pragma unroll
+                        for (int w = 0; w < W; ++w) n += wave_bins[w * bins + b];
                 }
                 int32_t sum = n;
                 for (int d = 1; d < 64; d <<= 1) {
@@ -848,7 +850,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
                 if (lane == 63) wave_total[wave] = sum;
                 __syncthreads();
                 int32_t start = carry + sum - n;
-                for (int w = 0; w < kPlanWaves; ++w) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
                     if (w < wave) start += wave_total[w];
                     carry += wave_total[w];
                 }
@@ -859,26 +862,28 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
                 __syncthreads();
             }
         }
-        // first rows of the waves
-        for (int b = tid; b < bins; b += kPlanThreads) {
-            int32_t at = next[b];
-            for (int w = 0; w < kPlanWaves; ++w) {
-                const int32_t c = wave_bins[w * bins + b];
-                wave_bins[w * bins + b] = at;
-                at += c;
+        for (int b = tid; b < bins; b += kThreads) {
+            uint16_t c[W], before = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) c[w] = wave_bins[w * bins + b];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                wave_bins[w * bins + b] = before;
+                before += c[w];
             }
-            next[b] = at;
+            all[b] = before;  // of this round
         }
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < kPlanSteps; ++s) {
             const int64_t p = mine + 64 * s;
             if (s >= steps || p >= hi) continue;
-            const int32_t row = own[id[s]] + rank[s];
+            const int32_t row = next[id[s]] + own[id[s]] + rank[s];
             a.slots[p] = id[s] < a.E ? row : -1 - row;
             a.rows[row] = id[s] < a.E ? static_cast<int32_t>(p) : -1;
         }
         __syncthreads();
+        for (int b = tid; b < bins; b += kThreads) next[b] += all[b];
     }
 }
 
@@ -1171,10 +1176,16 @@ hipError_t launch_plan(const int32_t* ids, int64_t P, int E, int64_t* offsets, i
     const int64_t blocks = sched::plan_blocks(P), seg = sched::plan_segment(P);
     const PlanArgs a{ids, P, E, seg, workspace, offsets, slots, rows};
     if (blocks > 1) {
-        plan_count_kernel<<<dim3(static_cast<unsigned>(blocks)), kPlanThreads, sizeof(int32_t) * (E + 1), stream>>>(a);
+        plan_count_kernel<<<dim3(static_cast<unsigned>(blocks)), kCountThreads, sizeof(int32_t) * (E + 1), stream>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    plan_kernel<<<dim3(static_cast<unsigned>(blocks)), kPlanThreads, sizeof(int32_t) * (E + 1) * (kPlanWaves + 2), stream>>>(a);
+    const int waves = sched::plan_waves(P);
+    const size_t lds = (E + 1) * (2 * sizeof(int32_t) + waves * sizeof(uint16_t));
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (waves == 16)
+        plan_kernel<16><<<grid, 64 * 16, lds, stream>>>(a);
+    else
+        plan_kernel<8><<<grid, 64 * 8, lds, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -68,6 +68,35 @@ def test_route(T, E, k, dtype):
         _check_weights(w, want_w)
 
 
+@pytest.mark.parametrize("T,E,k", [(3, 1000, 8), (3, 513, 16), (2, 300, 16), (5, 250, 13), (9, 17, 16), (3, 255, 17)])
+def test_route_odd_expert_counts(T, E, k):
+    """Counts that leave lanes without experts in both team sizes, and the most choices a team ranks."""
+    for score, bias in (("softmax", 0), ("sigmoid", 1), ("softmax", 1)):
+        g = _g(E + k)
+        z, zh = _logits(g, T, E, F32, pad=1)
+        b = torch.from_numpy((0.05 * g.standard_normal(E)).astype(np.float32)).to(DEV) if bias else None
+        w, ids = bf.moe_route(z, k, score=score, bias=b, renormalize=False)
+        want_w, want_ids = ref.route(zh, k, score, None if b is None else _np(b), renormalize=False)
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        _check_weights(w, want_w)
+
+
+@pytest.mark.parametrize("E", [16, 256, 1024])
+def test_route_of_quantized_logits_with_many_ties(E):
+    """Logits of a few distinct values (the top ones tie by the dozen) in both types and signs, -0 beside
+    0: ties go to the lower index."""
+    g = _g(E)
+    zh = np.round(g.standard_normal((40, E)) * 2) / 2
+    zh[::2] *= -1.0                                     # leaves -0.0 among the zeros
+    zh[5] = np.where(np.arange(E) % 2, 0.0, -0.0)
+    for dtype in (F32, BF):
+        z = torch.from_numpy(zh.astype(np.float32)).to(DEV).to(dtype)
+        for bias in (None, np.zeros(E, np.float32), np.round(g.standard_normal(E) * 4).astype(np.float32) / 64):
+            b = None if bias is None else torch.from_numpy(bias).to(DEV)
+            _, ids = bf.moe_route(z, 8, score="sigmoid", bias=b)
+            assert np.array_equal(ids.cpu().numpy(), ref.route(zh + 0.0, 8, "sigmoid", bias)[1])
+
+
 @pytest.mark.parametrize("E,groups,top,k", [(256, 8, 4, 8), (64, 8, 2, 6), (64, 4, 3, 8), (160, 8, 3, 6), (96, 8, 1, 8), (128, 16, 4, 8), (12, 3, 2, 8),
                                             (64, 64, 9, 9), (1024, 32, 5, 8), (200, 100, 30, 16), (256, 2, 1, 8), (384, 8, 4, 8)])
 def test_route_groups(E, groups, top, k):
