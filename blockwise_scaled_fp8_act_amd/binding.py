@@ -613,8 +613,9 @@ def moe_route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, ren
     dev = _current(logits, bias, weights, ids)
     if dev is None:
         _gpu(logits=logits, bias=bias, weights=weights, ids=ids)          # says which one
-    _call("moe_route", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _ptr(bias), _SCORES[score], k,
-          groups, top_groups, int(bool(renormalize)), scale, _ptr(weights), _ptr(ids), _stream(stream, dev))
+    _call("moe_route", logits.data_ptr(), _LOGITS[logits.dtype], T, E, logits.stride(0) if T > 1 else E, _ptr(bias),
+          _SCORES[score], k, groups, top_groups, 1 if renormalize else 0, scale, weights.data_ptr(), ids.data_ptr(),
+          _stream(stream, dev))
     return weights, ids
 
 
@@ -633,9 +634,9 @@ def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True,
     dev = _current(logits, ids, dweights, dlogits)
     if dev is None:
         _gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)          # says which one
-    _call("moe_route_backward", _ptr(logits), _LOGITS[logits.dtype], T, E, _row_stride(logits), _SCORES[score], k,
-          int(bool(renormalize)), scale, _ptr(ids), _ptr(dweights), _ptr(dlogits), _row_stride(dlogits),
-          _stream(stream, dev))
+    _call("moe_route_backward", logits.data_ptr(), _LOGITS[logits.dtype], T, E, logits.stride(0) if T > 1 else E,
+          _SCORES[score], k, 1 if renormalize else 0, scale, ids.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
+          dlogits.stride(0) if T > 1 else E, _stream(stream, dev))
     return dlogits
 
 
@@ -673,7 +674,7 @@ def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream
     dev = _current(ids, offsets, slots, rows, workspace)
     if dev is None:
         _gpu(ids=ids, offsets=offsets, slots=slots, rows=rows, workspace=workspace)          # says which one
-    _call("moe_plan", _ptr(ids), T, k, E, _ptr(offsets), _ptr(slots), _ptr(rows), _ptr(workspace), size,
+    _call("moe_plan", ids.data_ptr(), T, k, E, offsets.data_ptr(), slots.data_ptr(), rows.data_ptr(), _ptr(workspace), size,
           _stream(stream, dev))
     return offsets, slots, rows
 
@@ -713,8 +714,9 @@ def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=
     dev = _current(x, slots, q, a_s, copy)
     if dev is None:
         _gpu(x=x, slots=slots, q=q, a_s=a_s, copy=copy)          # says which one
-    _call("moe_dispatch", _ptr(x), T, H, _row_stride(x), _ptr(slots), k, _ptr(q), _row_stride(q), _ptr(a_s), _ptr(copy),
-          _row_stride(copy) if copy is not None else 0, _stream(stream, dev))
+    _call("moe_dispatch", x.data_ptr(), T, H, x.stride(0) if T > 1 else H, slots.data_ptr(), k, q.data_ptr(),
+          q.stride(0) if R > 1 else H, a_s.data_ptr(), _ptr(copy), 0 if copy is None else copy.stride(0) if R > 1 else H,
+          _stream(stream, dev))
     return q, a_s, copy
 
 
@@ -732,8 +734,8 @@ def moe_combine(rows, slots, weights=None, y=None, stream=None):
     dev = _current(rows, slots, weights, y)
     if dev is None:
         _gpu(rows=rows, slots=slots, weights=weights, y=y)          # says which one
-    _call("moe_combine", _ptr(rows), R, _row_stride(rows), _ptr(slots), _ptr(weights), T, k, H, _ptr(y), _row_stride(y),
-          _stream(stream, dev))
+    _call("moe_combine", rows.data_ptr(), R, rows.stride(0) if R > 1 else H, slots.data_ptr(), _ptr(weights), T, k, H,
+          y.data_ptr(), y.stride(0) if T > 1 else H, _stream(stream, dev))
     return y
 
 
@@ -756,14 +758,10 @@ def moe_combine_backward(dy, rows, slots, weights, drows=None, dweights=None, st
     dev = _current(dy, rows, slots, weights, drows, dweights)
     if dev is None:
         _gpu(dy=dy, rows=rows, slots=slots, weights=weights, drows=drows, dweights=dweights)          # says which one
-    _call("moe_combine_backward", _ptr(dy), _row_stride(dy), _ptr(rows), _row_stride(rows), _ptr(slots), _ptr(weights), T, k,
-          H, _ptr(drows), _row_stride(drows), _ptr(dweights), _stream(stream, dev))
+    _call("moe_combine_backward", dy.data_ptr(), dy.stride(0) if T > 1 else H, rows.data_ptr(),
+          rows.stride(0) if R > 1 else H, slots.data_ptr(), weights.data_ptr(), T, k, H, drows.data_ptr(),
+          drows.stride(0) if R > 1 else H, dweights.data_ptr(), _stream(stream, dev))
     return drows, dweights
-
-
-def _row_stride(t):
-    """Row stride of a matrix that _matrix has passed (a stride no row uses counts as the row's length)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, bs_stride_nb, bs_stride_kb, ldb=None,
@@ -787,7 +785,7 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
             raise ValueError(f"k = {k} must lie in [1, {MAX_CHOICES}]")
     M = A if rows is None else rows.numel()
     if ldb is None:
-        ldb = _row_stride(b)
+        ldb = b.stride(0) if b.shape[0] > 1 else K
     halves = 2 if swiglu else 1
     if N is None:
         N = b.shape[0] // max(E, 1) // halves
@@ -814,7 +812,7 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
     dev = _current(a, a_s, b, b_s, offsets, rows, c)
     if dev is None:
         _gpu(a=a, a_s=a_s, b=b, b_s=b_s, offsets=offsets, rows=rows, c=c)          # says which one
-    _call("gemm_1x128_128x128_routed", _ptr(a), _row_stride(a), _ptr(a_s), A, _ptr(rows), k, _ptr(b), ldb, b_stride,
-          _ptr(b_s), bs_stride, bs_stride_nb, bs_stride_kb, _ptr(offsets), E, _ptr(c), _row_stride(c), M, N, K,
-          int(bool(swiglu)), _stream(stream, dev))
+    _call("gemm_1x128_128x128_routed", a.data_ptr(), a.stride(0) if A > 1 else K, a_s.data_ptr(), A, _ptr(rows), k,
+          b.data_ptr(), ldb, b_stride, b_s.data_ptr(), bs_stride, bs_stride_nb, bs_stride_kb, offsets.data_ptr(), E,
+          c.data_ptr(), c.stride(0) if M > 1 else N, M, N, K, 1 if swiglu else 0, _stream(stream, dev))
     return c
