@@ -269,8 +269,8 @@ inline int64_t routed_row_tiles(int64_t M, int64_t E, int64_t tm) {
 // the mean over the experts that can have any, and one tile an expert. Measured, 256 CUs (us, registers
 // against LDS): 1 row each of 8 experts of 2048 x 4096, 128 workgroups of the LDS kernel: 13.7
 // against 17.8; 8 rows of 8 experts, gated 2048 x 4096, 256 workgroups: 27.4, 28.2; 2 rows of 56
-// experts of 2048 x 2048, 896: 29.9, 26.8; 16 rows of 64 experts, gated 1024 x 4096, 1024: 109, 99; 60 rows of
-// 8 experts, gated 2048 x 4096, 256: 54, 36.
+// experts of 2048 x 2048, 896: 31, 27; 16 rows of 64 experts, gated 1024 x 4096, 1024: 120, 99; 60 rows of
+// 8 experts, gated 2048 x 4096, 256: 64, 36.
 enum RoutedKernel { kRoutedRegisters16, kRoutedRegisters32, kRoutedLds };
 inline RoutedKernel routed_kernel(int64_t M, int64_t N, int64_t E, bool swiglu, int cus) {
     const int64_t experts = E < M ? E : M, mean = cdiv(M, experts);
