@@ -302,13 +302,14 @@ __device__ __forceinline__ void load_run(const uint16_t* p, bool vec, int left, 
     }
 }
 
-// The largest error of a sigmoid from the hardware's exp2 and reciprocal (each within one unit of the
-// last place; scores are at most 1) and of adding a bias to it.
 enum RouteKey { kKeyLogit, kKeySigmoid, kKeySoftmax };
+// Bounds of a score's error in fp32, from one unit of the last place in each of the hardware's exp2 and
+// reciprocal. Sigmoid: 3 half units for the sum and the reciprocal and 0.8 from the exponential (p (1 -
+// p) |z| is at most 0.23): 3.8 * 2^-24 of 8. Softmax: a sum 21 roundings deep (15 in a lane, 6 across), its
+// terms' errors weighted by themselves, the quotient: 25 * 2^-24 of 32, at a score of 1.
 constexpr float kSigmoidError = 4.8e-7f;  // 2^-21
-// That of a softmax: its sum's error, at most 10 roundings deep, and its own; scores are at most 1.
 constexpr float kSoftmaxError = 2e-6f;    // 2^-19
-constexpr float kKeyRounding = 6e-8f;     // 2^-24, of the key
+constexpr float kKeyRounding = 6e-8f;     // 2^-24, of a key or a sum: the rounding of an addition
 
 // L lanes a token (16, four tokens a wave, up to 256 experts; 64 up to 1024), V consecutive experts a
 // lane. Candidates come from fp32 keys cut to make room for the expert's index in the low bits: then
@@ -455,19 +456,20 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
                     first = fmaxf(first, x);
                 }
         }
-        // Ranks of the groups. With exact keys they are exact; a sum of two scores is off by at most two
-        // keys' errors, a difference of two sums by twice that, and a border inside it is open.
+        // Ranks of the groups. With exact keys they are exact. Else a sum of two keys is off by two scores'
+        // errors, the keys' roundings and its own, a difference of two sums by twice that (each group
+        // with the larger keys of the two sees the pair), and a border inside it is open.
         float tol = 0.0f;
         if (BIAS) {
             const float big = fmaxf(fabsf(first), second == -INFINITY ? 0.0f : fabsf(second));
-            tol = first == -INFINITY ? 0.0f : 4.0f * (key_error + kKeyRounding * big);
+            tol = first == -INFINITY ? 0.0f : 4.0f * key_error + 8.0f * kKeyRounding * big;
             if (second != -INFINITY) first += second;
         }
         wave_lds_fence();
         if (group < a.groups) value[group] = first;
         wave_lds_fence();
         int before = 0, maybe = 0;
-        const float high = first + tol, low = first - tol;
+        const float high = first + tol, low = tol < INFINITY ? first - tol : -INFINITY;
 #pragma unroll 4
         for (int j = 0; j < a.groups; ++j) {
             const float x = value[j];

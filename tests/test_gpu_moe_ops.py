@@ -164,6 +164,34 @@ def test_route_masks_infinities_and_nan(E, score):
                 _check_weights(w, want_w)
 
 
+@pytest.mark.parametrize("E,groups,top", [(64, 8, 2), (256, 8, 4), (96, 8, 3), (512, 16, 3), (64, 1, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_with_biases_of_any_size(E, groups, top, score):
+    """Biases that force experts in (+inf, 1e9), push them back (-1e9) or swamp the scores (+-100 and sums
+    of such that cancel): the order is the one of the 64-bit keys."""
+    g = _g(E + top)
+    z, zh = _logits(g, 24, E, F32)
+    for case in range(5):
+        b = 0.01 * g.standard_normal(E)
+        at = g.permutation(E)
+        if case == 0:
+            b[at[:5]] = np.inf
+        elif case == 1:
+            b[at[:E // 2]] = -1e9
+            b[at[:2]] = 1e9
+        elif case == 2:
+            b += 100.0
+        elif case == 3:
+            b = np.where(g.integers(0, 2, E) == 1, 1e6, -1e6) + b
+        else:
+            b = np.round(g.standard_normal(E) * 2) * 1e4
+        b = b.astype(np.float32)
+        w, ids = bf.moe_route(z, 4, score=score, bias=torch.from_numpy(b).to(DEV), groups=groups, top_groups=top)
+        want_w, want_ids = ref.route(zh, 4, score, b, groups, top)
+        assert np.array_equal(ids.cpu().numpy(), want_ids), case
+        _check_weights(w, want_w)
+
+
 @pytest.mark.parametrize("T,E,k", ROUTES)
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 def test_route_backward(T, E, k, dtype):
@@ -532,3 +560,53 @@ def test_repeated_calls_give_the_same_bits():
     for _ in range(3):
         for a, b in zip(_layer(*args), want):
             assert torch.equal(a, b)
+
+
+def _far_slots(T, k, seed):
+    """A permutation of the rows as slots: rows of a token lie anywhere."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randperm(T * k, generator=g, device=DEV).to(I32).view(T, k)
+
+
+def test_dispatch_and_combine_past_4_gib():
+    """1.12 million rows of 4096 columns: codes of 4.6e9 bytes, copies of 9.2e9, row offsets past 2^32."""
+    T, k, H = 140000, 8, 4096
+    x = torch.randn(T, H, device=DEV, dtype=BF)
+    slots = _far_slots(T, k, 1)
+    q, a_s, copy = bf.moe_dispatch(x, slots, want_copy=True)
+    pick = torch.tensor([0, 1, 524287, 524288, 1048575, 1048576, 1048577, T * k - 1], device=DEV)
+    owner = torch.empty(T * k, dtype=torch.int64, device=DEV)
+    owner[slots.flatten().long()] = torch.arange(T * k, device=DEV) // k
+    want_q, want_s = bf.quantize_lhs(x[owner[pick]])
+    assert torch.equal(q[pick], want_q) and torch.equal(a_s[:, pick], want_s) and torch.equal(copy[pick], x[owner[pick]])
+    del q, a_s
+    w = torch.rand(T, k, device=DEV) + 0.5
+    y = bf.moe_combine(copy, slots, w)                     # every row is its own token's: y = x * sum of the weights
+    t = torch.tensor([0, 1, T // 2, T - 1], device=DEV)
+    want = x[t].double() * w[t].double().sum(1, keepdim=True)
+    assert torch.all((y[t].double() - want).abs() <= (2.0 ** -8 + 10 * E24) * want.abs() + 2.0 ** -133)
+    drows, dw = bf.moe_combine_backward(x, copy, slots, w)
+    r = slots[t].long()
+    want = w[t].double()[:, :, None] * x[t].double()[:, None, :]
+    assert torch.all((drows[r.flatten()].view(4, k, H).double() - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -10) * want.abs() + 2.0 ** -133)
+    norm = (x[t].double() ** 2).sum(1, keepdim=True)       # <dy, row> with dy = x
+    assert torch.all((dw[t].double() - norm).abs() <= (H / 64 + 32) * E24 * norm)
+
+
+@pytest.mark.parametrize("per", [1, 20], ids=["few rows", "tiles"])
+def test_routed_product_of_weights_past_4_gib(per):
+    """300 experts of 4096 x 4096 codes (5.0e9 bytes); the first and the last ones have rows."""
+    E, N, K = 300, 4096, 4096
+    b = torch.full((E * N, K), 0x38, dtype=torch.uint8, device=DEV)          # 1.0
+    b[(E - 1) * N:] = 0xC0                                                   # -2.0
+    b[255 * N:257 * N] = 0x30                                                # 0.5, around 2^32 bytes
+    counts = torch.zeros(E, dtype=torch.int64)
+    counts[[0, 255, 256, E - 1]] = per
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)]).to(DEV)
+    M = 4 * per
+    a = torch.full((M, K), 0x38, dtype=torch.uint8, device=DEV)
+    a_s = torch.full((K // 128, M), 2.0 ** -6, device=DEV)
+    b_s = torch.ones(E * (N // 128) * (K // 128), device=DEV)
+    c = bf.gemm_1x128_128x128_routed(a, a_s, b, b_s, off, E, N * K, (N // 128) * (K // 128), K // 128, 1)
+    want = torch.tensor([64.0, 32.0, 32.0, -128.0], device=DEV).repeat_interleave(per)
+    assert torch.equal(c.float(), want[:, None].expand(M, N))                # exact: powers of two
