@@ -393,8 +393,8 @@ hipError_t launch(RoutedArgs a, bool once, hipStream_t stream) {
 
 hipError_t launch_gemm_routed(RoutedArgs a, bool swiglu, hipStream_t stream) {
     a.c_vec = (reinterpret_cast<uintptr_t>(a.c) % 8 == 0) && a.ldc % 4 == 0;
-    const bool once = sched::routed_reads_once(a.M, a.E);
-    switch (sched::routed_kernel(a.M, a.N, a.E, swiglu, device_cus())) {
+    const bool once = sched::routed_reads_once(a.M, a.N, a.E, swiglu);
+    switch (sched::routed_kernel(a.M, a.N, a.K, a.E, swiglu)) {
         case sched::kRoutedRegisters16: return swiglu ? launch<1, 2, 4, 3, true>(a, stream) : launch<1, 2, 4, 3, false>(a, stream);
         case sched::kRoutedRegisters32: return swiglu ? launch<2, 2, 4, 3, true>(a, stream) : launch<2, 2, 4, 3, false>(a, stream);
         default: return swiglu ? tiled::launch<3, true>(a, once, stream) : tiled::launch<3, false>(a, once, stream);

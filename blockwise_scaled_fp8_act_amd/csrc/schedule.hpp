@@ -263,26 +263,34 @@ inline int64_t routed_row_tiles(int64_t M, int64_t E, int64_t tm) {
     return (M - n) / tm + n;
 }
 
-// Kernel of the routed product. Where workgroups are many or rows are, 64-row tiles through LDS; where
-// neither is, so that a workgroup's own latency counts, 16- or 32-row tiles straight into registers,
-// with narrower columns and the waves splitting K. Rows are known to the device only: the rule takes
-// the mean over the experts that can have any, and one tile an expert. Measured, 256 CUs (us, registers
-// against LDS): 1 row each of 8 experts of 2048 x 4096, 128 workgroups of the LDS kernel: 13.7
-// against 17.8; 8 rows of 8 experts, gated 2048 x 4096, 256 workgroups: 27.4, 28.2; 2 rows of 56
-// experts of 2048 x 2048, 896: 31, 27; 16 rows of 64 experts, gated 1024 x 4096, 1024: 120, 99; 60 rows of
-// 8 experts, gated 2048 x 4096, 256: 64, 36.
+// Kernel of the routed product. 64-row tiles through LDS where rows are many, or workgroups are many for
+// the length of K (a workgroup of it walks all of K); else 16- or 32-row tiles straight into registers,
+// with narrower columns and the waves splitting K, where a workgroup's own latency counts. Rows are
+// known to the device only: the rule takes the mean over the experts that can have any, and one tile
+// an expert. Measured on 256 CUs (us, registers against LDS; wg: workgroups of the LDS kernel): 1 row of 8
+// experts of 2048 x 4096, wg 128: 13.7, 17.8; 2 rows of 16, gated 2048 x 4096, wg 512: 38, 43-47; 1-4 rows of 40
+// of 1280 x 1280, wg 270: 8.1, 8.1; 2 rows of 8 of 4096 x 512, wg 256: 7.9, 6.0; 2 rows of 56 of 2048 x 2048,
+// wg 896: 31, 26; 5 rows of 40 of 1000 x 1280, wg 320: 17, 13; 10 rows of 8, gated 1408 x 1280, wg 176: 12.3, 9.9;
+// 8 rows of 8, gated 2048 x 4096, wg 256: 27.4, 28.2; 3 rows of 36, gated 1408 x 4096, wg 792: 69, 77; 16 rows of
+// 64, gated 1024 x 4096, wg 1024: 120, 99; 48 rows of 8, gated 1024 x 2048, wg 128: 24, 13.
+inline int64_t routed_lds_workgroups(int64_t M, int64_t N, int64_t E, bool swiglu) {
+    return (E < M ? E : M) * cdiv(N, swiglu ? 64 : 128);
+}
 enum RoutedKernel { kRoutedRegisters16, kRoutedRegisters32, kRoutedLds };
-inline RoutedKernel routed_kernel(int64_t M, int64_t N, int64_t E, bool swiglu, int cus) {
-    const int64_t experts = E < M ? E : M, mean = cdiv(M, experts);
-    if (mean > 16 || experts * cdiv(N, swiglu ? 64 : 128) >= 2 * static_cast<int64_t>(cus)) return kRoutedLds;
+inline RoutedKernel routed_kernel(int64_t M, int64_t N, int64_t K, int64_t E, bool swiglu) {
+    const int64_t mean = cdiv(M, E < M ? E : M), Kb = cdiv(K, geom::kBlockK);
+    if (mean > 16 || routed_lds_workgroups(M, N, E, swiglu) >= (mean > 4 ? 10 : 28) * Kb) return kRoutedLds;
     return mean <= 4 ? kRoutedRegisters16 : kRoutedRegisters32;
 }
 
-// Whether the LDS kernel reads the weights past the caches: up to 32 rows an expert on average most
-// experts have one 64-row tile. Measured (us, cached against past the caches): 16 rows of 64 experts, gated
-// 1024 x 4096: 101, 95; 4 rows of 64, gated 1408 x 2048: 44, 38; 32 rows of 64, gated 1024 x 4096: 107, 107;
-// 60 rows of 64 experts of 5120 x 1280, some with two or three tiles: 107, 115.
-inline bool routed_reads_once(int64_t M, int64_t E) { return cdiv(M, E < M ? E : M) <= 32; }
+// Whether the LDS kernel reads the weights past the caches: where there are workgroups enough to keep
+// HBM busy without them and, up to 32 rows an expert on average, most experts have one 64-row tile.
+// Measured (us, cached against past the caches): 16 rows of 64 experts, gated 1024 x 4096, 1024 workgroups:
+// 101, 95; 4 rows of 64, gated 1408 x 2048, 1408: 44, 38; 8 rows of 40 of 1280 x 512, 400: 8.3, 7.7; 8 rows of 40 of
+// 512 x 4096, 160: 17.6, 22.5; 60 rows of 64 experts of 5120 x 1280, some with two or three tiles: 107, 115.
+inline bool routed_reads_once(int64_t M, int64_t N, int64_t E, bool swiglu) {
+    return cdiv(M, E < M ? E : M) <= 32 && routed_lds_workgroups(M, N, E, swiglu) >= 400;
+}
 
 }  // namespace sched
 }  // namespace bsfp8
