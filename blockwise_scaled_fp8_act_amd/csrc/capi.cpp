@@ -332,6 +332,7 @@ int gemm_128x1_impl(const void* a, int64_t lda, const float* a_s, const void* b,
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxChoices = 64;
 constexpr int64_t kMaxPairs = 0x7FFFFFFF;
+constexpr int64_t kMaxWaves = (int64_t{1} << 26) - 64;  // a launch's lanes are counted in 32 bits; whole workgroups
 
 // The pairs of T tokens with k choices each are numbered in 32 bits.
 bool pairs_ok(int64_t T, int64_t k) { return T >= 0 && k >= 1 && k <= kMaxChoices && T <= kMaxPairs / k; }
@@ -340,7 +341,7 @@ int validate_route(int dtype, int64_t T, int64_t E, int64_t ld, int score, int64
     if (!pairs_ok(T, k) || E < 1 || E > kMaxExperts || k > E) return BSFP8_EINVAL;
     if ((dtype != BSFP8_BF16 && dtype != BSFP8_F32) || (score != BSFP8_SOFTMAX && score != BSFP8_SIGMOID))
         return BSFP8_EINVAL;
-    if (ld < E || !std::isfinite(scale)) return BSFP8_EINVAL;
+    if (ld < E || !std::isfinite(scale) || T > kMaxWaves) return BSFP8_EINVAL;
     return BSFP8_OK;
 }
 
@@ -570,7 +571,7 @@ int moe_dispatch(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t
     if (T == 0 || H == 0) return BSFP8_OK;
     if (x == nullptr || slots == nullptr || q == nullptr || a_s == nullptr) return BSFP8_EINVAL;
     if (ldx < H || ldq < H || (copy != nullptr && ldcopy < H)) return BSFP8_EINVAL;
-    if (cdiv(H, 1024) > 0x7FFFFFFFLL / T) return BSFP8_EINVAL;
+    if (cdiv(H, 1024) > kMaxWaves / T) return BSFP8_EINVAL;
     if (int rc = check_device()) return rc;
     return finish(bsfp8::launch_dispatch(static_cast<const uint16_t*>(x), T, H, ldx, slots, static_cast<int>(k),
                                          static_cast<uint8_t*>(q), ldq, a_s, static_cast<uint16_t*>(copy), ldcopy,
@@ -582,7 +583,7 @@ int moe_combine(const void* rows, int64_t R, int64_t ldr, const int32_t* slots, 
     if (!pairs_ok(T, k) || H < 0 || R < 0) return BSFP8_EINVAL;
     if (T == 0 || H == 0) return BSFP8_OK;
     if ((rows == nullptr && R > 0) || slots == nullptr || y == nullptr) return BSFP8_EINVAL;
-    if (ldr < H || ldy < H || cdiv(H, 512) > 0x7FFFFFFFLL / T) return BSFP8_EINVAL;
+    if (ldr < H || ldy < H || cdiv(H, 512) > kMaxWaves / T) return BSFP8_EINVAL;
     if (int rc = check_device()) return rc;
     return finish(bsfp8::launch_combine(static_cast<const uint16_t*>(rows), R, ldr, slots, weights, T,
                                         static_cast<int>(k), H, static_cast<uint16_t*>(y), ldy,
@@ -596,7 +597,7 @@ int moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t
     if (T == 0) return BSFP8_OK;
     if (slots == nullptr || weights == nullptr || dweights == nullptr) return BSFP8_EINVAL;
     if (H > 0 && (dy == nullptr || rows == nullptr || drows == nullptr)) return BSFP8_EINVAL;
-    if (lddy < H || ldr < H || lddr < H) return BSFP8_EINVAL;
+    if (lddy < H || ldr < H || lddr < H || T > kMaxWaves / 4) return BSFP8_EINVAL;
     if (int rc = check_device()) return rc;
     return finish(bsfp8::launch_combine_backward(
         static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(rows), ldr, slots, weights, T,
@@ -615,6 +616,7 @@ int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int6
         return BSFP8_EINVAL;
     if (E > kMaxExperts || M > kMaxPairs || a_rows < 1 || k < 1 || k > kMaxChoices) return BSFP8_EINVAL;
     if (rows == nullptr && a_rows < M) return BSFP8_EINVAL;
+    if (!bsfp8::sched::routed_fits(M, N, K, E, swiglu != 0)) return BSFP8_EINVAL;
     if (lda < K || ldb < K || ldc < N || b_stride < 0 || bs_stride < 0 || bs_stride_nb < 0 || bs_stride_kb < 0)
         return BSFP8_EINVAL;
     if (!aligned16(a) || !aligned16(b) || lda % 16 != 0 || ldb % 16 != 0 || b_stride % 16 != 0) return BSFP8_EALIGN;

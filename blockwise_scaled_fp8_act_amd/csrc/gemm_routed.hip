@@ -223,7 +223,6 @@ hipError_t launch(RoutedArgs a, hipStream_t stream) {
     constexpr int64_t kOut = 16 * (SWIGLU ? NS / 2 : NS);
     a.col_tiles = (a.N + kOut - 1) / kOut;
     const int64_t blocks = sched::routed_row_tiles(a.M, a.E, 16 * MS) * a.col_tiles;
-    if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     routed_kernel<MS, NS, WK, D, SWIGLU><<<dim3(static_cast<unsigned>(blocks)), 64 * WK, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -378,7 +377,6 @@ hipError_t launch(RoutedArgs a, bool once, hipStream_t stream) {
     constexpr int64_t kOut = SWIGLU ? kTN / 2 : kTN;
     a.col_tiles = (a.N + kOut - 1) / kOut;
     const int64_t blocks = sched::routed_row_tiles(a.M, a.E, kTM) * a.col_tiles;
-    if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
     if (once)
         routed_kernel<S, SWIGLU, true><<<grid, 64 * kWaves, 0, stream>>>(a);

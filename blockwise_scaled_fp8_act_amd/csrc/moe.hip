@@ -1201,7 +1201,6 @@ hipError_t launch_plan(const int32_t* ids, int64_t P, int E, int64_t* offsets, i
 hipError_t launch_dispatch(const uint16_t* x, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int k, uint8_t* q,
                            int64_t ldq, float* a_s, uint16_t* copy, int64_t ldcopy, hipStream_t stream) {
     const int64_t chunks = (H + 1023) / 1024, blocks = (T * chunks + 8 * kWaves - 1) / (8 * kWaves) * 8;
-    if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     const bool vec = H % 8 == 0 && rows16(x, 2 * ldx) && reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0 &&
                      (copy == nullptr || rows16(copy, 2 * ldcopy));
     const dim3 grid(static_cast<unsigned>(blocks));
@@ -1215,7 +1214,6 @@ hipError_t launch_dispatch(const uint16_t* x, int64_t T, int64_t H, int64_t ldx,
 hipError_t launch_combine(const uint16_t* rows, int64_t R, int64_t ldr, const int32_t* slots, const float* weights,
                           int64_t T, int k, int64_t H, uint16_t* y, int64_t ldy, hipStream_t stream) {
     const int64_t chunks = (H + 511) / 512, blocks = (T * chunks + kWaves - 1) / kWaves;
-    if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     const bool vec = H % 8 == 0 && rows16(rows, 2 * ldr) && rows16(y, 2 * ldy);
     const dim3 grid(static_cast<unsigned>(blocks));
     if (vec)

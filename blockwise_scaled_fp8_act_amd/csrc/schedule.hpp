@@ -283,6 +283,15 @@ inline RoutedKernel routed_kernel(int64_t M, int64_t N, int64_t K, int64_t E, bo
     return mean <= 4 ? kRoutedRegisters16 : kRoutedRegisters32;
 }
 
+// Whether the kernel's launch stays below 2^32 lanes, which are counted in 32 bits: tiles of 64 rows and
+// 128 columns (64 with swiglu) of 512 lanes, or of 16 or 32 rows and 32 (16) of 256.
+inline bool routed_fits(int64_t M, int64_t N, int64_t K, int64_t E, bool swiglu) {
+    const RoutedKernel kernel = routed_kernel(M, N, K, E, swiglu);
+    const bool lds = kernel == kRoutedLds;
+    const int64_t row_tiles = routed_row_tiles(M, E, lds ? 64 : kernel == kRoutedRegisters16 ? 16 : 32);
+    return cdiv(N, (lds ? 128 : 32) / (swiglu ? 2 : 1)) <= 0xFFFFFFFFLL / (lds ? 512 : 256) / row_tiles;
+}
+
 // Whether the LDS kernel reads the weights past the caches: where there are workgroups enough to keep
 // HBM busy without them and, up to 32 rows an expert on average, most experts have one 64-row tile.
 // Measured (us, cached against past the caches): 16 rows of 64 experts, gated 1024 x 4096, 1024 workgroups:

@@ -379,7 +379,7 @@ enum { BSFP8_SOFTMAX = 0, BSFP8_SIGMOID = 1 }; /* score of an expert */
  * whose logit is -inf, or whose bias is -inf or NaN, is never chosen; a choice that finds no expert has
  * id -1 and weight 0. A row with a NaN logit (softmax: or +inf) has ids -1 and weights NaN.
  * Requirements (else BSFP8_EINVAL): E a multiple of groups, 1 <= top_groups <= groups,
- * k <= top_groups * E / groups, scale finite.
+ * k <= top_groups * E / groups, scale finite, T <= 2^26 - 64 (moe_route_backward too).
  */
 int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int score,
               int64_t k, int64_t groups, int64_t top_groups, int renormalize, float scale,
@@ -420,7 +420,7 @@ int moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t* offse
  *         scales and copy), so every row is written.
  *   copy  NULL, or [T k, H] bf16, row stride ldcopy >= H: the tokens themselves in row order (what
  *         quantize_rhs_grouped takes for the weight gradient).
- * Slots that name no row in [0, T k) are skipped. The gradient with respect to x is moe_combine of the
+ * Slots that name no row in [0, T k) are skipped. T ceil(H/1024) at most 2^26 - 64. The gradient with respect to x is moe_combine of the
  * copy's gradient without weights.
  */
 int moe_dispatch(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t* slots, int64_t k,
@@ -432,7 +432,7 @@ int moe_dispatch(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t
  *   rows [R, H] bf16, row stride ldr >= H;  slots [T, k];  weights [T, k] fp32 or NULL (all 1);
  *   y [T, H] bf16, row stride ldy >= H.
  * A slot outside [0, R) contributes its weight times 0 (so the NaN weights of a row that could not be
- * routed show in its output).
+ * routed show in its output). T ceil(H/512) at most 2^26 - 64.
  */
 int moe_combine(const void* rows, int64_t R, int64_t ldr, const int32_t* slots, const float* weights,
                 int64_t T, int64_t k, int64_t H, void* y, int64_t ldy, void* stream);
@@ -442,7 +442,7 @@ int moe_combine(const void* rows, int64_t R, int64_t ldr, const int32_t* slots, 
  * product of dy[t] and rows[slots[t, j]] (fp32).
  *   dy [T, H], rows [T k, H], drows [T k, H] bf16 with their row strides; slots, weights, dweights [T, k].
  * A dropped pair's padding row of drows is zero and its dweights 0, so with a moe_plan's slots every
- * row is written.
+ * row is written. T at most 2^24 - 16.
  */
 int moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t ldr, const int32_t* slots,
                          const float* weights, int64_t T, int64_t k, int64_t H, void* drows, int64_t lddr,
@@ -462,7 +462,8 @@ int moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t
  *   c, ldc        C [M, N] bf16; swiglu: C = silu(gate) * up, formed in fp32 and rounded once. Rows
  *                 outside every expert's range are not written.
  * Requirements (else BSFP8_EINVAL): K a positive multiple of 128, N a multiple of 128 with swiglu,
- * a_rows >= M without rows, M < 2^31; alignment as gemm_1x128_128x128 (b_stride too). The K range is
+ * a_rows >= M without rows, M < 2^31 and fewer than 2^23 tiles of 64 rows and 128 columns (64 with
+ * swiglu; for up to 16 rows an expert 2^24 of 16 or 32 rows and 32 or 16 columns); alignment as gemm_1x128_128x128 (b_stride too). The K range is
  * summed in parts in a fixed order, so results can differ from the grouped GEMM's in the last bits
  * and are the same on every call. Any row counts are computed; the grouped GEMM is as fast from about
  * 256 rows an expert (8 experts of 4096 x 4096: 64 rows each 36 us against 58, 128 rows 39 against

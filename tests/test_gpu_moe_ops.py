@@ -610,3 +610,26 @@ def test_routed_product_of_weights_past_4_gib(per):
     c = bf.gemm_1x128_128x128_routed(a, a_s, b, b_s, off, E, N * K, (N // 128) * (K // 128), K // 128, 1)
     want = torch.tensor([64.0, 32.0, 32.0, -128.0], device=DEV).repeat_interleave(per)
     assert torch.equal(c.float(), want[:, None].expand(M, N))                # exact: powers of two
+
+
+def test_routed_product_of_the_most_rows():
+    """537 million rows, one output column, 64 choices a token: the most tiles of 64 rows that one launch holds.
+    Row r is its token's, up to the last one; one row more is refused."""
+    k, K = 64, 128
+    M = 64 * (2 ** 23 - 3) + 65
+    T = (M + k - 1) // k
+    a = torch.full((T, K), 0x38, dtype=torch.uint8, device=DEV)                        # 1.0
+    a_s = (2.0 ** (torch.arange(T, device=DEV) % 5 - 9).float()).view(1, T).contiguous()
+    rows = torch.arange(M + 1, dtype=torch.int32, device=DEV)
+    b = torch.full((2, K), 0x38, dtype=torch.uint8, device=DEV)
+    b[1] = 0xC0                                                                        # -2.0
+    b_s = torch.ones(2, device=DEV)
+    c = torch.full((M, 1), float("nan"), dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, 1, 2 ** 28 - 1, 2 ** 28, 2 ** 28 + 1, M - 66, M - 65, M - 64, M - 2, M - 1], device=DEV)
+    off = torch.tensor([0, 2 ** 28, M], device=DEV)
+    bf.gemm_1x128_128x128_routed(a, a_s, b, b_s, off, 2, K, 1, 1, 1, rows=rows[:M], k=k, c=c, N=1)
+    want = 2.0 ** ((at // k) % 5 - 2).float() * torch.where(at < 2 ** 28, 1.0, -2.0)
+    assert torch.equal(c[at, 0].float(), want)
+    assert not any(bool(c[i:i + 2 ** 26].isnan().any()) for i in range(0, M, 2 ** 26))
+    with pytest.raises(bf.Bsfp8Error):
+        bf.gemm_1x128_128x128_routed(a, a_s, b, b_s, off, 2, K, 1, 1, 1, rows=rows, k=k, N=1)

@@ -113,6 +113,40 @@ def test_routed_product_entry_rejects_bad_arguments(L):
         assert f(**bad) == 2, bad
 
 
+def test_entries_reject_launches_of_2_32_lanes(L):
+    """A launch's lanes are counted in 32 bits: a wave a token (or for so many of its columns), four for the
+    gradient of the return, a workgroup a tile of the routed product."""
+    most = 2 ** 26 - 64
+
+    def route(T):
+        return L.moe_route(P, 1, T, 8, 8, None, 0, 2, 1, 1, 1, 1.0, P, P, None)
+
+    def route_backward(T):
+        return L.moe_route_backward(P, 1, T, 8, 8, 0, 2, 1, 1.0, P, P, P, 8, None)
+    for f in (route, route_backward):
+        assert _passed(f(most)) and f(most + 1) == 1
+
+    def dispatch(T, H):
+        return L.moe_dispatch(P, T, H, H, P, 2, P, H, P, None, 0, None)
+    assert _passed(dispatch(most, 1024)) and _passed(dispatch(most // 2, 1025))
+    assert dispatch(most + 1, 1024) == 1 and dispatch(most, 1025) == 1
+
+    def combine(T, H):
+        return L.moe_combine(P, 8, H, P, P, T, 2, H, P, H, None)
+    assert _passed(combine(most, 512)) and combine(most + 1, 512) == 1 and combine(most, 513) == 1
+
+    def combine_backward(T):
+        return L.moe_combine_backward(P, 8, P, 8, P, P, T, 2, 8, P, 8, P, None)
+    assert _passed(combine_backward(most // 4)) and combine_backward(most // 4 + 1) == 1
+
+    def product(M, N, E=2, sw=0):
+        return L.gemm_1x128_128x128_routed(P, 128, P, M, P, 1, P, 128, 128, P, 1, 1, 1, P, E, P, N, M, N, 128, sw, None)
+    rows = 64 * (2 ** 23 - 3) + 65                        # E = 2: (M - 2) / 64 + 2 tiles, at most 2^23 - 1
+    assert _passed(product(rows, 1)) and product(rows + 1, 1) == 1 and product(rows, 129) == 1
+    assert _passed(product(2, 128 * (2 ** 22 - 1))) and product(2, 128 * 2 ** 22) == 1
+    assert _passed(product(2, 64 * (2 ** 22 - 2), sw=1)) and product(2, 64 * 2 ** 22, sw=1) == 1
+
+
 def test_binding_rejects_malformed_tensors():
     z = torch.zeros(4, 16)
     for bad, kind in ((dict(logits=z.half()), TypeError), (dict(logits=z[0]), ValueError), (dict(logits=z.t()), ValueError),
