@@ -154,7 +154,9 @@ class BlockwiseFp8MoE(torch.nn.Module):
         self.register_buffer("bias", torch.zeros(experts, dtype=torch.float32, device=device) if balance_bias else None)
 
     def route(self, x: torch.Tensor):
-        logits = torch.nn.functional.linear(x, self.router).float()
+        # the product's sums are in fp32, its logits rounded to bf16, the parameters' type; a router whose
+        # choice or gradient needs more bits gives fp32 logits of its own to route_experts
+        logits = torch.nn.functional.linear(x, self.router)
         return route_experts(logits, self.k, bias=self.bias, **self.rule)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
