@@ -728,14 +728,17 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* l
 
 // ---------------------------------------------------------------------------------------- plan
 // A stable counting sort of the P = T k pairs into E + 1 bins (bin E: no expert here). A workgroup
-// takes its pairs in rounds; in a round each wave has kPlanSteps steps of 64 pairs, loaded together. A
-// pair's rank among the equal bins of its 64 comes from one ballot per bit of the bin number, and one
-// lane per distinct bin advances the wave's own counter, so no atomics decide an order. With more
-// than one workgroup a first kernel counts each workgroup's bins, and every workgroup sums the
-// counts it needs. Latency-bound: 512 pairs 3.5 us, 4096 7.2 us, 65536 pairs of 64 experts 9.7 us with
-// the counting launch (19.4 with the counts summed one workgroup after the other).
-using sched::kPlanSteps;
-constexpr int kCountThreads = 512;
+// takes its pairs in rounds; in a round each wave has S steps of 64 pairs, loaded together. A pair's
+// rank among the equal bins of its 64 comes from one ballot per bit of the bin number, and one lane
+// per distinct bin advances the wave's own counter, step after step, so no atomics decide an order.
+// Up to 8192 pairs are one round of one workgroup, which gathers the rows in LDS and stores them in
+// order. With more (MANY) a first kernel counts each workgroup's bins, and every workgroup sums the
+// counts it needs. Latency-bound, in a graph: 512 pairs 3.0 us, 4096 6.2, 8192 8.7 (10.8 with the rows
+// scattered to memory), 65536 pairs of 64 experts 9.0 with the counting launch (19 with the counts
+// summed one workgroup after the other).
+constexpr int kCountThreads = 512, kCountSteps = 4;
+constexpr int kBinBits = 11;  // bins 0 to 1024
+typedef uint32_t u32_pair __attribute__((may_alias));  // two 16-bit counters
 
 struct PlanArgs {
     const int32_t* ids;
@@ -756,55 +759,46 @@ __global__ __launch_bounds__(kCountThreads) void plan_count_kernel(PlanArgs a) {
     for (int b = tid; b < bins; b += kCountThreads) hist[b] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * a.seg, hi = min(lo + a.seg, a.P);
-    for (int64_t p0 = lo; p0 < hi; p0 += kPlanSteps * kCountThreads) {
-        int32_t id[kPlanSteps];
+    for (int64_t p0 = lo; p0 < hi; p0 += kCountSteps * kCountThreads) {
+        int32_t id[kCountSteps];
 #pragma unroll
-        for (int s = 0; s < kPlanSteps; ++s) id[s] = p0 + s * kCountThreads + tid < hi ? a.ids[p0 + s * kCountThreads + tid] : 0;
+        for (int s = 0; s < kCountSteps; ++s) id[s] = p0 + s * kCountThreads + tid < hi ? a.ids[p0 + s * kCountThreads + tid] : 0;
 #pragma unroll
-        for (int s = 0; s < kPlanSteps; ++s)
+        for (int s = 0; s < kCountSteps; ++s)
             if (p0 + s * kCountThreads + tid < hi) atomicAdd(&hist[plan_bin(id[s], a.E)], 1);
     }
     __syncthreads();
     for (int b = tid; b < bins; b += kCountThreads) a.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = hist[b];
 }
 
-// Lanes of this wave whose bin equals this lane's, among the lanes of `active`.
-__device__ __forceinline__ uint64_t same_bin(int bin, int bits, uint64_t active) {
-    uint64_t m = active;
-#pragma unroll 4
-    for (int i = 0; i < bits; ++i) {
-        const uint64_t one = __ballot((bin >> i) & 1);
-        m &= (bin >> i) & 1 ? one : ~one;
-    }
-    return m;
-}
-
-template <int W>
+template <int W, int S, bool MANY>
 __global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
-    constexpr int kThreads = 64 * W, kRound = sched::plan_round(W);
+    constexpr int kThreads = 64 * W, kRound = sched::plan_round(W, S);
     extern __shared__ int32_t bin_lds[];
     static_assert(kRound <= 0xFFFF, "a wave's place in a bin is kept in 16 bits");
     __shared__ int32_t wave_total[W];
+    __shared__ uint16_t row_pair[MANY ? 1 : kRound];  // without MANY: a row's pair, kNoPair for none
+    constexpr uint16_t kNoPair = 0xFFFF;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = a.E + 1;
     const int bits = 32 - __builtin_clz(a.E);  // E itself needs a place
     int32_t* const next = bin_lds;     // [bins]: this workgroup's next row of a bin
     int32_t* const all = next + bins;  // [bins]: pairs of a bin
     // [W][bins]: a wave's pairs of a bin in this round, then those of the waves before it
     uint16_t* const wave_bins = reinterpret_cast<uint16_t*>(all + bins);
+    const int pitch = (bins + 1) & ~1;  // whole words a wave
     const int64_t lo = blockIdx.x * a.seg, hi = min(lo + a.seg, a.P);
-    const bool many = gridDim.x > 1;
-    uint16_t* const own = wave_bins + wave * bins;
-    const uint64_t below = (uint64_t{1} << lane) - 1;
+    u32_pair* const own = reinterpret_cast<u32_pair*>(wave_bins + wave * pitch);
 
-    for (int64_t p0 = lo; p0 == lo || p0 < hi; p0 += kRound) {
+    for (int64_t p0 = lo; p0 == lo || (MANY && p0 < hi); p0 += kRound) {
         // a short round is spread over all waves
         const int steps = static_cast<int>((min(hi - p0, int64_t{kRound}) + kThreads - 1) / kThreads);
         const int64_t mine = p0 + wave * 64 * steps + lane;
-        int32_t id[kPlanSteps], rank[kPlanSteps];
+        const auto in = [&](int s) { return s < steps && mine + 64 * s < hi; };
+        int32_t id[S], rank[S];
 #pragma unroll
-        for (int s = 0; s < kPlanSteps; ++s) id[s] = s < steps && mine + 64 * s < hi ? a.ids[mine + 64 * s] : 0;
-        for (int b = tid; b < bins * W; b += kThreads) wave_bins[b] = 0;
-        if (p0 == lo && many) {
+        for (int s = 0; s < S; ++s) id[s] = lo < hi ? a.ids[in(s) ? mine + 64 * s : lo] : 0;
+        for (int b = tid; b < pitch * W / 2; b += kThreads) reinterpret_cast<u32_pair*>(wave_bins)[b] = 0;
+        if (MANY && p0 == lo) {
             // bins of all workgroups, and of those before this one: parts of the workgroups side by side
             for (int b = tid; b < bins; b += kThreads) next[b] = all[b] = 0;
             __syncthreads();
@@ -823,17 +817,40 @@ __global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
                 }
         }
         __syncthreads();
-        // ranks inside the wave's run
+        // Ranks inside the wave's run: the first lane of a bin adds all of its 64 pairs to the wave's counter.
+        // The wave's LDS operations keep their order, so the steps' counters come back without a wait
+        // between them.
+        uint32_t low[S], high[S], old[S];  // lanes with this lane's bin
 #pragma unroll
-        for (int s = 0; s < kPlanSteps; ++s) {
-            if (s >= steps) continue;
-            const bool in = mine + 64 * s < hi;
+        for (int s = 0; s < S; ++s) {
+            const uint64_t m = __ballot(in(s));
+            low[s] = static_cast<uint32_t>(m);
+            high[s] = static_cast<uint32_t>(m >> 32);
             id[s] = plan_bin(id[s], a.E);
-            const uint64_t m = same_bin(id[s], bits, __ballot(in));
-            rank[s] = own[id[s]] + __popcll(m & below);
-            wave_lds_fence();
-            if (in && (m & below) == 0) own[id[s]] = static_cast<uint16_t>(rank[s] + __popcll(m));
-            wave_lds_fence();
+        }
+#pragma unroll
+        for (int i = 0; i < kBinBits; ++i)
+            if (i < bits) {
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int bit = (id[s] << (31 - i)) >> 31;  // all ones or zeros
+                    const uint64_t ones = __ballot(bit != 0);
+                    low[s] &= ~(static_cast<uint32_t>(ones) ^ bit);
+                    high[s] &= ~(static_cast<uint32_t>(ones >> 32) ^ bit);
+                }
+            }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            rank[s] = __builtin_amdgcn_mbcnt_hi(high[s], __builtin_amdgcn_mbcnt_lo(low[s], 0));
+            old[s] = 0;
+            if (in(s) && rank[s] == 0)
+                old[s] = __hip_atomic_fetch_add(own + (id[s] >> 1), static_cast<uint32_t>(__popc(low[s]) + __popc(high[s])) << 16 * (id[s] & 1),
+                                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int first = low[s] != 0 ? __ffs(low[s]) - 1 : 31 + __ffs(high[s]);
+            rank[s] += __shfl(old[s], first) >> 16 * (id[s] & 1) & 0xFFFF;
         }
         __syncthreads();
         // first round: where each bin starts (bins in runs of the workgroup's threads, carried on)
@@ -843,10 +860,10 @@ __global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
                 const int b = b0 + tid;
                 int32_t n = 0;
                 if (b < bins) {
-                    if (many) n = all[b];
+                    if (MANY) n = all[b];
                     else
 #pragma unroll
-                        for (int w = 0; w < W; ++w) n += wave_bins[w * bins + b];
+                        for (int w = 0; w < W; ++w) n += wave_bins[w * pitch + b];
                 }
                 int32_t sum = n;
                 for (int d = 1; d < 64; d <<= 1) {
@@ -863,7 +880,7 @@ __global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
                 }
                 if (b < bins) {
                     if (blockIdx.x == 0) a.offsets[b] = start;
-                    next[b] = start + (many ? next[b] : 0);
+                    next[b] = start + (MANY ? next[b] : 0);
                 }
                 __syncthreads();
             }
@@ -871,25 +888,30 @@ __global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
         for (int b = tid; b < bins; b += kThreads) {
             uint16_t c[W], before = 0;
 #pragma unroll
-            for (int w = 0; w < W; ++w) c[w] = wave_bins[w * bins + b];
+            for (int w = 0; w < W; ++w) c[w] = wave_bins[w * pitch + b];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                wave_bins[w * bins + b] = before;
+                wave_bins[w * pitch + b] = before;
                 before += c[w];
             }
             all[b] = before;  // of this round
         }
         __syncthreads();
 #pragma unroll
-        for (int s = 0; s < kPlanSteps; ++s) {
+        for (int s = 0; s < S; ++s) {
             const int64_t p = mine + 64 * s;
-            if (s >= steps || p >= hi) continue;
-            const int32_t row = next[id[s]] + own[id[s]] + rank[s];
+            if (!in(s)) continue;
+            const int32_t row = next[id[s]] + wave_bins[wave * pitch + id[s]] + rank[s];
             a.slots[p] = id[s] < a.E ? row : -1 - row;
-            a.rows[row] = id[s] < a.E ? static_cast<int32_t>(p) : -1;
+            if (MANY) a.rows[row] = id[s] < a.E ? static_cast<int32_t>(p) : -1;
+            else row_pair[row] = id[s] < a.E ? static_cast<uint16_t>(p) : kNoPair;
         }
         __syncthreads();
-        for (int b = tid; b < bins; b += kThreads) next[b] += all[b];
+        if (MANY) {
+            for (int b = tid; b < bins; b += kThreads) next[b] += all[b];
+        } else {  // rows in order: stores of whole lines (a CU scatters a word a clock)
+            for (int r = tid; r < static_cast<int>(a.P); r += kThreads) a.rows[r] = row_pair[r] == kNoPair ? -1 : row_pair[r];
+        }
     }
 }
 
@@ -1188,13 +1210,19 @@ hipError_t launch_plan(const int32_t* ids, int64_t P, int E, int64_t* offsets, i
         plan_count_kernel<<<dim3(static_cast<unsigned>(blocks)), kCountThreads, sizeof(int32_t) * (E + 1), stream>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    const int waves = sched::plan_waves(P);
-    const size_t lds = (E + 1) * (2 * sizeof(int32_t) + waves * sizeof(uint16_t));
+    const int waves = sched::plan_waves(P), steps = sched::plan_steps(P);
+    const size_t lds = (E + 1) * 2 * sizeof(int32_t) + (E + 2) / 2 * 2 * waves * sizeof(uint16_t);
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (waves == 16)
-        plan_kernel<16><<<grid, 64 * 16, lds, stream>>>(a);
+    if (blocks > 1)
+        plan_kernel<8, 4, true><<<grid, 64 * 8, lds, stream>>>(a);
+    else if (steps == 8)
+        plan_kernel<16, 8, false><<<grid, 64 * 16, lds, stream>>>(a);
+    else if (waves == 16)
+        plan_kernel<16, 4, false><<<grid, 64 * 16, lds, stream>>>(a);
+    else if (steps == 1)
+        plan_kernel<8, 1, false><<<grid, 64 * 8, lds, stream>>>(a);
     else
-        plan_kernel<8><<<grid, 64 * 8, lds, stream>>>(a);
+        plan_kernel<8, 4, false><<<grid, 64 * 8, lds, stream>>>(a);
     return hipGetLastError();
 }
 

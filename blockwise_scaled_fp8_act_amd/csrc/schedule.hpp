@@ -244,15 +244,18 @@ inline ColumnSplit gemm_column_split(int64_t M, int64_t N, int64_t K, int cus, i
 
 namespace sched {
 
-// The plan's counting sort: rounds of four steps of 64 pairs a wave. One workgroup and no counting pass
-// up to one round of 16 waves (of eight where that is enough: 512 pairs 3.6 us against 4.7), else at
-// most 512 workgroups of eight waves and whole rounds (4096 pairs in two rounds of eight waves: 9.2
-// us, in one of 16: 7.2; counted by two workgroups: 9.1).
-constexpr int kPlanSteps = 4;
-constexpr int plan_round(int waves) { return 64 * kPlanSteps * waves; }
-inline int plan_waves(int64_t P) { return P > plan_round(8) && P <= plan_round(16) ? 16 : 8; }
+// The plan's counting sort: rounds of `steps` steps of 64 pairs a wave. One workgroup and no counting
+// pass up to one round of 16 waves and eight steps, 8192 pairs (of 64 experts: 8.7 us in a graph and 9.4
+// as a call, against 8.2 and 14.3 with the counting launch and its memory; 1024 experts 12.2 and 12.2
+// against 13.5 and 14.4), with fewer waves and steps where that is enough (512 pairs in eight waves 3.0
+// us in one step, 3.5 with four to pass by; in 16 waves 4.7; 4096 in two rounds of eight waves 9.2, in
+// one of 16 6.2). Beyond, at most 512 workgroups of eight waves, four steps and whole rounds.
+constexpr int plan_round(int waves, int steps) { return 64 * steps * waves; }
+constexpr int64_t kPlanOne = plan_round(16, 8);  // pairs of one workgroup without a counting pass
+inline int plan_waves(int64_t P) { return P > plan_round(8, 4) && P <= kPlanOne ? 16 : 8; }
+inline int plan_steps(int64_t P) { return P <= plan_round(8, 1) ? 1 : P > plan_round(16, 4) && P <= kPlanOne ? 8 : 4; }
 inline int64_t plan_segment(int64_t P) {
-    return P <= plan_round(16) ? plan_round(16) : cdiv(cdiv(P, 512), plan_round(8)) * plan_round(8);
+    return P <= kPlanOne ? kPlanOne : cdiv(cdiv(P, 512), plan_round(8, 4)) * plan_round(8, 4);
 }
 inline int64_t plan_blocks(int64_t P) { return P > 0 ? cdiv(P, plan_segment(P)) : 1; }
 

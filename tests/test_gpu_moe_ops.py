@@ -219,7 +219,7 @@ def test_route_backward_rows_without_a_choice():
 
 
 PLANS = [(1, 1, 1), (1, 8, 64), (63, 1, 2), (64, 1, 63), (13, 5, 64), (511, 8, 65), (512, 8, 256), (513, 8, 8), (700, 6, 1024), (4096, 8, 64),
-         (33333, 3, 255), (131072, 8, 128)]
+         (256, 8, 64), (2049, 1, 31), (1024, 4, 64), (4097, 1, 1024), (1365, 6, 100), (8192, 1, 1024), (8193, 1, 7), (33333, 3, 255), (131072, 8, 128)]
 
 
 @pytest.mark.parametrize("T,k,E", PLANS)

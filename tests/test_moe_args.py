@@ -221,10 +221,12 @@ int64_t worst(int64_t M, int64_t E, int64_t tm) {   // most tiles E experts with
     return best;
 }
 int main() {
-    for (int64_t P : {0LL, 1LL, 511LL, 512LL, 513LL, 4096LL, 4097LL, 65536LL, 131072LL, 1048575LL, 1048577LL, 99999999LL, 2147483647LL}) {
+    for (int64_t P : {0LL, 1LL, 511LL, 512LL, 513LL, 2048LL, 2049LL, 4096LL, 4097LL, 8192LL, 8193LL, 65536LL, 131072LL, 1048575LL, 1048577LL, 99999999LL, 2147483647LL}) {
         const int64_t s = plan_segment(P), b = plan_blocks(P);
         if (s % 512 != 0 || b < 1 || b > 512 || b * s < P || (P > 0 && (b - 1) * s >= P)) return std::printf("plan %lld\n", (long long)P), 1;
-        if ((P <= 4096) != (b == 1)) return std::printf("blocks %lld\n", (long long)P), 1;
+        if ((P <= 8192) != (b == 1)) return std::printf("blocks %lld\n", (long long)P), 1;
+        if (b == 1 && plan_round(plan_waves(P), plan_steps(P)) < P) return std::printf("round %lld\n", (long long)P), 1;
+        if (b > 1 && s % plan_round(plan_waves(P), plan_steps(P)) != 0) return std::printf("rounds %lld\n", (long long)P), 1;
     }
     for (int64_t tm : {1, 2, 4})
         for (int64_t M = 1; M <= 14; ++M)
