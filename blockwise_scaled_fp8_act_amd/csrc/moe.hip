@@ -319,9 +319,10 @@ constexpr float kKeyRounding = 6e-8f;     // 2^-24, of a key or a sum: the round
 // keys cannot tell that the k best are among the candidates (three keys nearly equal at the border),
 // the choices are made one by one from 64-bit keys; where fp32 cannot tell which groups are kept,
 // the groups are valued again in 64 bits. KEY: the logits, which are exact, or a score + bias.
-// Bound by vector issue: 923 instructions a wave of four tokens at 256 experts in groups, half of them
-// the sort and the takes; 16384 tokens 16 us (48 with one wave a token and 64-bit shuffles; their
-// bytes alone 3.4), one token 4.2 us.
+// Bound by vector issue, 877 instructions a wave of four tokens at 256 experts in groups, nearly half
+// of them the sort and the takes, and by its slowest waves: 16384 tokens 12.7 us in a graph (15.7 where
+// each lane formed its own exact keys; 48 with one wave a token and 64-bit shuffles; their bytes alone
+// 3.4), with a softmax and no groups 12.4 (16.3), one token 4.2 us.
 template <typename LT, int V, int L, RouteKey KEY>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, RouteArgs a) {
     extern __shared__ double lds[];
@@ -383,25 +384,36 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         for (int v = 0; v < V; ++v) key[v] = z[v];
     }
     // The exact key of an expert: score in 64 bits + bias. The softmax's sum in 64 bits is made where a
-    // key is first asked for (wave-uniform: prepare_exact before exact_key).
+    // key is first asked for (prepare_exact before exact_key, in uniform control flow). What follows is
+    // rare, but the launch waits for the last wave: the whole wave works for a team that asks.
     double total64 = 0.0;
-    const auto prepare_exact = [&]() {
-        if (!SOFTMAX_KEY || total64 != 0.0) return;
-        double sum = 0.0;
+    const auto asks = [&](uint64_t lanes, int x) { return (lanes >> (x * L) & (L == 64 ? ~uint64_t{0} : (uint64_t{1} << L) - 1)) != 0; };
+    constexpr int kSteps = (L * V + 63) / 64;
+    const auto prepare_exact = [&](uint64_t lanes) {
+        if (!SOFTMAX_KEY) return;
+        lanes &= __ballot(total64 == 0.0);
 #pragma unroll 1
-        for (int v = 0; v < V && e0 + v < E; ++v) {
-            const float x = load_logit(row + e0 + v);
-            sum += x == -INFINITY ? 0.0 : exp(static_cast<double>(x) - top);
+        for (int x = 0; x < kTokens; ++x) {
+            if (!asks(lanes, x)) continue;
+            const LT* const other = logits + min(t0 + x, a.T - 1) * a.ld;
+            const float other_top = __shfl(top, x * L);
+            double sum = 0.0;
+#pragma unroll 4
+            for (int v = 0; v < kSteps; ++v) {
+                const int e = v * 64 + lane;
+                const float y = load_logit(other + min(e, E - 1));
+                sum += e >= E || y == -INFINITY ? 0.0 : exp(static_cast<double>(y) - other_top);
+            }
+            sum = wave_sum(sum);
+            if (team == x) total64 = sum;
         }
-#pragma unroll 1
-        for (int x = 1; x < L; x <<= 1) sum += __shfl_xor(sum, x);
-        total64 = sum;
     };
-    const auto exact_key = [&](float x, int e) -> double {
+    const auto exact_key_of = [&](float x, int e, float row_top, double row_total) -> double {
         if (!BIAS) return x + 0.0f;
-        const double y = exp(SOFTMAX_KEY ? static_cast<double>(x) - top : -static_cast<double>(x));
-        return (SOFTMAX_KEY ? y / total64 : 1.0 / (1.0 + y)) + static_cast<double>(a.bias[e]);
+        const double y = exp(SOFTMAX_KEY ? static_cast<double>(x) - row_top : -static_cast<double>(x));
+        return (SOFTMAX_KEY ? y / row_total : 1.0 / (1.0 + y)) + static_cast<double>(a.bias[e]);
     };
+    const auto exact_key = [&](float x, int e) { return exact_key_of(x, e, top, total64); };
 
     // doubles of LDS a token has: its keys, a group's run padded to an odd length, and the groups' values
     const int size = a.size, pitch = size | 1, area = a.groups * (pitch + 1);
@@ -482,25 +494,33 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         }
         bool keep = group < a.groups && before < a.top_groups;
         bool lanes_keep = regular;  // keep is about the lane's own experts
-        if (BIAS && __any(keep && maybe > a.top_groups && !bad)) {
+        const uint64_t doubt = BIAS ? __ballot(keep && maybe > a.top_groups && !bad && live) : 0;
+        if (doubt != 0) {
             wave_lds_fence();
-            prepare_exact();
-            double* const value64 = mine64 + a.groups * pitch;
-            int g = e0 / size, i = e0 - g * size;
+            prepare_exact(doubt);
 #pragma unroll 1
-            for (int v = 0; v < V && e0 + v < E; ++v) {
-                const float x = load_logit(row + e0 + v);
-                const double y = exact_key(x, e0 + v);
-                mine64[g * pitch + i] = x == -INFINITY || y != y ? -INFINITY : y;
-                if (++i == size) {
-                    i = 0;
-                    ++g;
+            for (int x = 0; x < kTokens; ++x) {
+                if (!asks(doubt, x)) continue;
+                const LT* const other = logits + (t0 + x) * a.ld;
+                const float other_top = __shfl(top, x * L);
+                const double other_total = __shfl(total64, x * L);
+                double* const keys = lds + static_cast<int64_t>(wave * kTokens + x) * area;
+#pragma unroll 4
+                for (int v = 0; v < kSteps; ++v) {
+                    const int e = v * 64 + lane;
+                    const float z1 = load_logit(other + min(e, E - 1));
+                    const double y = exact_key_of(z1, min(e, E - 1), other_top, other_total);
+                    const int g = e / size;
+                    if (e < E) keys[g * pitch + e - g * size] = z1 == -INFINITY || y != y ? -INFINITY : y;
                 }
             }
             wave_lds_fence();
+        }
+        if ((doubt & team_lanes) != 0) {
+            double* const value64 = mine64 + a.groups * pitch;
             double one = -INFINITY, two = -INFINITY;
             if (sub < a.groups) {
-#pragma unroll 1
+#pragma unroll 8
                 for (int j = 0; j < size; ++j) {
                     const double x = mine64[sub * pitch + j];
                     two = fmax(two, fmin(one, x));
@@ -512,7 +532,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
             wave_lds_fence();
             int rank = 0;
             if (sub < a.groups)
-#pragma unroll 1
+#pragma unroll 4
                 for (int j = 0; j < a.groups; ++j) rank += value64[j] > one || (value64[j] == one && j < sub) ? 1 : 0;
             keep = sub < a.groups && rank < a.top_groups;
             lanes_keep = false;
@@ -556,7 +576,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         for (int v = 0; v < kDepth; ++v) run[v] = ((v + 1 < V ? run[v + 1 < V ? v + 1 : v] : 0u) & own) | (run[v] & ~own);
     };
     if (m <= 10) {
-        for (int j = 0; j < m; ++j) take(j, std::integral_constant<int, 10>{});
+        const auto takes = [&](auto self, auto at) {
+            constexpr int j = decltype(at)::value;
+            if constexpr (j < 10) {
+                if (j >= m) return;
+                take(j, std::integral_constant<int, 10 - j>{});
+                self(self, std::integral_constant<int, j + 1>{});
+            }
+        };
+        takes(takes, std::integral_constant<int, 0>{});
     } else {
         for (int j = 0; j < m; ++j) take(j, std::integral_constant<int, 16>{});
     }
@@ -576,22 +604,26 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
     int id = have ? static_cast<int>(kIndex - (mine & kIndex)) : 0x7FFFFFFF;
     float zc = have ? load_logit(row + id) : -INFINITY;
     int rank = sub;
-    if (__any(have && sub < k && close(mine, after))) {  // by the exact keys
-        prepare_exact();
+    const uint64_t near = __ballot(have && sub < k && close(mine, after) && live && !bad);
+    if (near != 0) {  // by the exact keys
+        prepare_exact(near);
         double full = -INFINITY;
         if (have) full = exact_key(zc, id);
-        rank = rank_row16(full, id);  // lanes without a candidate: -inf, last
+        const int exact_rank = rank_row16(full, id);  // lanes without a candidate: -inf, last
+        if ((near & team_lanes) != 0) rank = exact_rank;
     }
     bool chosen = have && rank < k;
-    if (__any(open && live && !bad)) {  // choice by choice from 64-bit keys in LDS
+    const uint64_t opens = __ballot(open && live && !bad);
+    if (opens != 0) {  // choice by choice from 64-bit keys in LDS
         double* const key64 = lds + static_cast<int64_t>(wave * kTokens + team) * area;
         wave_lds_fence();
-        prepare_exact();
-#pragma unroll 1
-        for (int v = 0; v < V && e0 + v < E; ++v) {
-            const float x = load_logit(row + e0 + v);
-            const double y = exact_key(x, e0 + v);
-            key64[e0 + v] = x == -INFINITY || y != y || ((dropped >> v) & 1) ? -INFINITY : y;
+        prepare_exact(opens);
+#pragma unroll 4
+        for (int v = 0; v < V; ++v) {
+            const int e = min(e0 + v, E - 1);
+            const float x = load_logit(row + e);
+            const double y = exact_key(x, e);
+            if (e0 + v < E) key64[e0 + v] = x == -INFINITY || y != y || ((dropped >> v) & 1) ? -INFINITY : y;
         }
         int found = -1;
 #pragma unroll 1
@@ -600,11 +632,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
             double best = -INFINITY;
             int at = E;
 #pragma unroll 1
-            for (int e = e0; e < min(e0 + V, E); ++e)
-                if (key64[e] > best) {
-                    best = key64[e];
+            for (int e = e0; e < min(e0 + V, E); ++e) {
+                const double x = key64[e];
+                if (x > best) {
+                    best = x;
                     at = e;
                 }
+            }
 #pragma unroll 1
             for (int x = 1; x < L; x <<= 1) {
                 const double ob = __shfl_xor(best, x);

@@ -130,6 +130,24 @@ def test_route_chooses_between_keys_closer_than_fp32(E, groups, top):
             assert ids.cpu().tolist() == [[0, 1, 2, 3]] * 5
 
 
+@pytest.mark.parametrize("E,groups,top", [(16, 4, 2), (64, 8, 3), (100, 5, 2), (256, 8, 4), (256, 1, 1), (512, 8, 4), (1000, 1, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_of_rows_that_tie_beside_rows_that_do_not(E, groups, top, score):
+    """Rows of a few distinct logits, of plain ones, with NaN, with nothing left and of equal logits in one wave, in
+    every order: what a row needs to be told apart leaves its neighbours as they are."""
+    g, k, T = _g(E + top), 4, 61
+    few = np.round(g.standard_normal((T, E)) * 2) / 4
+    kind = g.integers(0, 5, T)[:, None]
+    zh = np.where(kind == 0, few, 1.5 * g.standard_normal((T, E))).astype(np.float32)
+    zh = np.where((kind == 2) & (np.arange(E) == 3), np.nan, np.where(kind == 3, -np.inf, np.where(kind == 4, 0.25, zh)))
+    z = torch.from_numpy(zh.astype(np.float32)).to(DEV)
+    for bias in (np.zeros(E, np.float32), np.round(g.standard_normal(E) * 2).astype(np.float32) / 64):
+        w, ids = bf.moe_route(z, k, score=score, bias=torch.from_numpy(bias).to(DEV), groups=groups, top_groups=top)
+        want_w, want_ids = ref.route(_np(z), k, score, bias, groups, top)
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        _check_weights(w, want_w)
+
+
 @pytest.mark.parametrize("E", [8, 64, 100, 256, 512])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_masks_infinities_and_nan(E, score):
