@@ -166,6 +166,42 @@ def test_serving_step_replays_from_a_graph():
         assert torch.equal(out, want)
 
 
+def test_training_step_replays_from_a_graph():
+    """Forward and backward of route and experts in one graph, on leaves of its own; every replay, with eager
+    work on other leaves between, equals that eager step bit for bit."""
+    T, E, k, F, H = 70, 8, 2, 128, 256
+    x, _, _, w1, w2 = _case(11, T, E, k, F, H)
+    z, dy = torch.randn(T, E, device=DEV), torch.randn(T, H, device=DEV).to(BF)
+
+    def step(leaves, dy):
+        x, z, w1, w2 = leaves
+        y = bf.blockwise_fp8_moe(x, *bf.route_experts(z, k, score="sigmoid", scale=2.5), w1, w2)
+        return (y.detach(), *torch.autograd.grad(y, leaves, dy))
+
+    leaves = [t.clone().requires_grad_() for t in (x, z, w1, w2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(leaves, dy)
+    for _ in range(4):
+        with torch.no_grad():
+            leaves[0].copy_(torch.randn(T, H, device=DEV))
+            leaves[1].copy_(torch.randn(T, E, device=DEV))
+            leaves[2].mul_(0.9)
+        dy.copy_(torch.randn(T, H, device=DEV))
+        want = step([t.detach().clone().requires_grad_() for t in leaves], dy)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, name in zip(got, want, ("y", "dx", "dlogits", "dw_gate_up", "dw_down")):
+            assert torch.equal(a, b), name
+
+
 def test_layer_rejects_malformed_weights():
     x, weights, ids, w1, w2 = _case(1, 4, 4, 2, 128, 128)
     with pytest.raises(TypeError, match="bf16"):
