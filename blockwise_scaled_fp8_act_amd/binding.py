@@ -1,7 +1,8 @@
 """Thin ctypes binding of libbsfp8.so (the gfx950 HIP library); declarations in include/blockwise_fp8.h.
 
 Argument marshalling only: every step runs in the HIP kernels. torch provides device memory and the
-current stream. There is no CPU fallback: if the library is missing, loading raises.
+current stream. The functions of the mixture-of-experts operators first offer their arguments to
+_calls.so (csrc/calls.c), which makes the usual call without ctypes. There is no CPU fallback: if the library is missing, loading raises.
 
 Tensor conventions (torch, on the GPU):
   bf16 inputs       torch.bfloat16 (or int16/uint16 holding bf16 bits)
@@ -32,6 +33,7 @@ _i32 = ctypes.c_int
 _f32 = ctypes.c_float
 
 _lib = None
+_calls = None       # the C part (csrc/calls.c), where torch has what it is bound to
 
 
 class Bsfp8Error(RuntimeError):
@@ -94,8 +96,28 @@ def lib():
                   "quantize_lhs_and_weight_fnuz", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch",
                   "moe_combine", "moe_combine_backward", "gemm_1x128_128x128_routed"):
             getattr(L, f).restype = ctypes.c_int
+        _bind_calls(L)
         _lib = L
     return _lib
+
+
+def _bind_calls(L):
+    """Load _calls.so: the usual call of the small operators in one step (a function of it returns None
+    where an argument is not as usual, and the checks below say what is wrong)."""
+    global _calls
+    get_device = getattr(torch._C, "_cuda_getDevice", None)
+    if get_device is None or _raw_stream is None:
+        return
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        raise ImportError("_calls.so is missing beside libbsfp8.so: build it with `python -m blockwise_scaled_fp8_act_amd.build`") from e
+    calls.bind(torch.Tensor, Bsfp8Error, get_device, _raw_stream,
+               (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float8_e4m3fn),
+               tuple(ctypes.cast(f, _vp).value for f in (L.moe_route, L.moe_route_backward, L.moe_plan_workspace, L.moe_plan,
+                                                         L.moe_dispatch, L.moe_combine, L.moe_combine_backward,
+                                                         L.gemm_1x128_128x128_routed)))
+    _calls = calls
 
 
 # the current stream's handle without building a torch.cuda.Stream object (0.1 against ~3 us per
@@ -596,6 +618,10 @@ def moe_route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, ren
     ``top_groups`` best of ``groups`` groups of consecutive experts; equal keys go to the lower index.
     Returns (weights [T, k] fp32, ids [T, k] int32), largest key first; a choice that finds no expert
     (logits of -inf) has id -1 and weight 0, a row with NaN has ids -1 and weights NaN."""
+    if stream is None and _calls is not None:
+        done = _calls.moe_route(logits, k, score, bias, groups, top_groups, renormalize, scale, weights, ids)
+        if done is not None:
+            return done
     T, E = _route_args(logits, k, score, scale)
     if groups < 1 or E % groups != 0 or not 1 <= top_groups <= groups or k > top_groups * (E // groups):
         raise ValueError(f"groups = {groups} must divide E = {E}, 1 <= top_groups = {top_groups} <= groups, and the "
@@ -622,6 +648,10 @@ def moe_route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, ren
 def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True, scale=1.0, dlogits=None, stream=None):
     """The gradient of moe_route's weights with respect to the logits, from the ids it chose and the
     weights' gradient [T, k] fp32. Returns dlogits [T, E] in the logits' type."""
+    if stream is None and _calls is not None:
+        done = _calls.moe_route_backward(logits, ids, dweights, score, renormalize, scale, dlogits)
+        if done is not None:
+            return done
     T, k = _choices("ids", ids, torch.int32)
     _, E = _route_args(logits, k, score, scale)
     if logits.shape[0] != T:
@@ -646,6 +676,10 @@ def moe_plan(ids, E, offsets=None, slots=None, rows=None, workspace=None, stream
     GEMMs take; slots [T, k] int32, each pair's row, or -1 - r for a dropped pair with padding row r;
     rows [T k] int32, each row's pair t * k + j, -1 for a padding row). ``workspace``: a uint8 tensor of
     moe_plan_workspace(T, k, E) bytes that calls in a row may share."""
+    if stream is None and _calls is not None:
+        done = _calls.moe_plan(ids, E, offsets, slots, rows, workspace)
+        if done is not None:
+            return done
     T, k = _choices("ids", ids, torch.int32)
     if not 1 <= E <= MAX_EXPERTS:
         raise ValueError(f"E = {E} must lie in [1, {MAX_EXPERTS}]")
@@ -696,6 +730,10 @@ def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=
     """x [T, H] bf16 in the row order of a plan's slots [T, k], quantized in 1x128 groups. Returns
     (q [T k, H] uint8, a_s (ceil(H/128), T k) fp32, copy [T k, H] bf16 or None); rows of dropped pairs
     are zero."""
+    if stream is None and _calls is not None:
+        done = _calls.moe_dispatch(x, slots, q, a_s, copy, want_copy)
+        if done is not None:
+            return done
     T, k = _choices("slots", slots, torch.int32)
     H = _matrix("x", x, _BF16, (T, None)).shape[1]
     R = T * k
@@ -723,6 +761,10 @@ def moe_dispatch(x, slots, q=None, a_s=None, copy=None, want_copy=False, stream=
 def moe_combine(rows, slots, weights=None, y=None, stream=None):
     """y[t] = sum over j of weights[t, j] * rows[slots[t, j]] (rows [R, H] bf16, weights fp32 or None for
     1), in fp32 with one rounding. Returns y [T, H] bf16."""
+    if stream is None and _calls is not None:
+        done = _calls.moe_combine(rows, slots, weights, y)
+        if done is not None:
+            return done
     T, k = _choices("slots", slots, torch.int32)
     R, H = _matrix("rows", rows, _BF16).shape
     if weights is not None:
@@ -742,6 +784,10 @@ def moe_combine(rows, slots, weights=None, y=None, stream=None):
 def moe_combine_backward(dy, rows, slots, weights, drows=None, dweights=None, stream=None):
     """Gradients of moe_combine: returns (drows [T k, H] bf16, weights * dy in row order, zero for
     padding rows; dweights [T, k] fp32)."""
+    if stream is None and _calls is not None:
+        done = _calls.moe_combine_backward(dy, rows, slots, weights, drows, dweights)
+        if done is not None:
+            return done
     T, k = _choices("slots", slots, torch.int32)
     H = _matrix("dy", dy, _BF16, (T, None)).shape[1]
     R = T * k
@@ -770,6 +816,11 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
     r of C multiplies A's row rows[r] // k (its token); None: row r of A. ``swiglu``: B_e holds N gate
     rows, then N up rows, and C = silu(gate) * up. N defaults to the output columns of the experts'
     rows stacked in b ([E * N, K], or [E * 2 N, K] with swiglu). Returns c [M, N] bf16."""
+    if stream is None and _calls is not None:
+        done = _calls.gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, bs_stride_nb, bs_stride_kb, ldb, rows, k,
+                                                swiglu, c, N)
+        if done is not None:
+            return done
     A, K = _matrix("a", a, _CODES["e4m3fn"]).shape
     _matrix("b", b, _CODES["e4m3fn"])
     if E < 0 or E > MAX_EXPERTS:

@@ -1,4 +1,5 @@
-"""Build the gfx950 HIP library libbsfp8.so in-tree with hipcc (cross-compiles without a GPU).
+"""Build the gfx950 HIP library libbsfp8.so in-tree with hipcc (cross-compiles without a GPU), and the
+binding's C part _calls.so with the host's C compiler.
 
     python -m blockwise_scaled_fp8_act_amd.build
 """
@@ -8,6 +9,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,10 +17,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libbsfp8.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["capi.cpp", "quantize.hip", "gemm.hip", "moe.hip", "gemm_routed.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CC = os.environ.get("CC", "gcc")
 ARCH = "gfx950"
 CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
@@ -40,9 +44,20 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_calls() -> None:
+    tmp = CALLS_PATH + ".tmp"
+    cmd = [CC, "-O2", "-std=gnu11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "calls.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CC} failed for calls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libbsfp8.so (always recompiles)."""
+    """Compile every HIP source and link libbsfp8.so, compile _calls.so (always recompiles)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    _build_calls()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB_PATH + ".tmp"
@@ -53,6 +68,7 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB_PATH)
     if verbose:
         print(f"built {LIB_PATH}")
+        print(f"built {CALLS_PATH}")
     return LIB_PATH
 
 

@@ -13,6 +13,8 @@ Tolerances, all relative to a sum of magnitudes so that cancellation is counted:
                   rounded one) plus half a bf16 step; with the gate: through the derivative of
                   silu(g) u, |silu'| <= 1.1.
 Chosen experts, plans and codes have to be equal."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -651,3 +653,92 @@ def test_routed_product_of_the_most_rows():
     assert not any(bool(c[i:i + 2 ** 26].isnan().any()) for i in range(0, M, 2 ** 26))
     with pytest.raises(bf.Bsfp8Error):
         bf.gemm_1x128_128x128_routed(a, a_s, b, b_s, off, 2, K, 1, 1, 1, rows=rows, k=k, N=1)
+
+
+def _both_ways(f, *args, **kw):
+    """A call as users make it and the same with its stream named, which takes the long way of the binding."""
+    a, b = f(*args, **kw), f(*args, **kw, stream=torch.cuda.current_stream())
+    a, b = (a, b) if isinstance(a, tuple) else ((a,), (b,))
+    assert len(a) == len(b)
+    for x, y in zip(a, b):
+        assert (x is None) == (y is None)
+        if x is not None:
+            assert x.dtype == y.dtype and x.shape == y.shape and x.stride() == y.stride() and x.device == y.device
+            assert torch.equal(x, y)
+    return a
+
+
+@pytest.mark.parametrize("T,E,k,H", [(1, 8, 1, 128), (1, 256, 8, 1000), (33, 64, 6, 256), (700, 64, 8, 384), (2, 1, 1, 1)])
+def test_both_ways_of_a_call_agree(T, E, k, H):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    z = torch.randn(T, E + 3, device=DEV, generator=g)[:, :E]
+    bias = torch.randn(E, device=DEV, generator=g)
+    x = torch.randn(T, H, device=DEV, generator=g).to(BF)
+    w, ids = _both_ways(bf.moe_route, z, k, score="sigmoid", bias=bias, scale=2)
+    _both_ways(bf.moe_route, z.to(BF), k, renormalize=False)
+    dw = torch.randn(T, k, device=DEV, generator=g)
+    _both_ways(bf.moe_route_backward, z, ids, dw, score="sigmoid")
+    _both_ways(bf.moe_route_backward, z.to(BF), ids, dw)
+    ids[0, 0] = -1
+    _, slots, _ = _both_ways(bf.moe_plan, ids, E)
+    q, a_s, none = _both_ways(bf.moe_dispatch, x, slots)
+    assert none is None
+    rows = _both_ways(bf.moe_dispatch, x, slots, want_copy=True)[2]
+    _both_ways(bf.moe_combine, rows, slots, w)
+    _both_ways(bf.moe_combine, rows, slots)
+    _both_ways(bf.moe_combine_backward, x, rows, slots, w)
+    if H % 128 == 0:
+        offsets, _, index = bf.moe_plan(ids, E)
+        for swiglu in (False, True):
+            b = torch.randn(E * 256, H, device=DEV, generator=g).to(torch.float8_e4m3fn).view(torch.uint8)
+            b_s = torch.rand(E, 2, H // 128, device=DEV, generator=g)
+            qx, sx = bf.quantize_lhs(x)
+            for rows_given in (dict(rows=index, k=k), {}):
+                lhs = (qx, sx) if rows_given else (q, a_s)
+                full = offsets.clone()
+                full[E] = T * k                             # no row of C left unwritten
+                _both_ways(bf.gemm_1x128_128x128_routed, *lhs, b, b_s, full, E, 256 * H, 2 * (H // 128), H // 128, 1, swiglu=swiglu, **rows_given)
+    out = torch.zeros(T, H + 5, dtype=BF, device=DEV)
+    assert bf.moe_combine(rows, slots, w, y=out[:, :H]).data_ptr() == out.data_ptr()
+    assert torch.equal(out[:, :H], bf.moe_combine(rows, slots, w)) and not out[:, H:].any()
+
+
+def test_one_step_calls_refuse_before_they_launch():
+    """Arguments of the wrong type, shape, stride or place on the GPU: the same errors as the long way, outputs as they
+    were, and no memory kept."""
+    T, E, k, H = 8, 16, 2, 256
+    z, x = torch.randn(T, E, device=DEV), torch.randn(T, H, device=DEV).to(BF)
+    w, ids = bf.moe_route(z, k)
+    _, slots, _ = bf.moe_plan(ids, E)
+    rows = bf.moe_dispatch(x, slots, want_copy=True)[2]
+    held = torch.full((T, k), 7, dtype=I32, device=DEV)
+    wide = torch.empty(T, 2 * k, device=DEV)
+    code, scale, edges = torch.zeros(T, H, dtype=torch.uint8, device=DEV), torch.ones(2, T, device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV)
+    long, long_ids = torch.empty(2 ** 26, 1, dtype=BF, device=DEV), torch.empty(2 ** 26, 1, dtype=I32, device=DEV)       # refused: too many tokens
+    before = torch.cuda.memory_allocated()
+    for kind, f, args, kw in [
+            (ValueError, bf.moe_route, (z, E + 1), {}), (ValueError, bf.moe_route, (z.t(), k), {}), (TypeError, bf.moe_route, (z.double(), k), {}),
+            (ValueError, bf.moe_route, (z.cpu(), k), {}), (ValueError, bf.moe_route, (z, k), dict(bias=torch.zeros(E))),
+            (ValueError, bf.moe_route, (z, k), dict(ids=held, weights=wide[:, :k])), (TypeError, bf.moe_route, (z, k), dict(ids=held, weights=held)),
+            (ValueError, bf.moe_route, (z, k), dict(ids=held, scale=float("inf"))), (ValueError, bf.moe_route, (z, k), dict(ids=held, score="tanh")),
+            (ValueError, bf.moe_route, (z, k), dict(ids=held, groups=3)), (ValueError, bf.moe_route, (z, k), dict(ids=held[:4])),
+            (TypeError, bf.moe_plan, (ids.long(), E), {}), (ValueError, bf.moe_plan, (ids, 0), {}), (ValueError, bf.moe_plan, (ids, E), dict(rows=held)),
+            (ValueError, bf.moe_plan, (ids, E), dict(slots=held.cpu())), (ValueError, bf.moe_dispatch, (x[:4], slots), {}),
+            (ValueError, bf.moe_dispatch, (x, slots), dict(q=torch.empty(T, H, dtype=torch.uint8, device=DEV))),
+            (ValueError, bf.moe_combine, (rows, slots, wide), {}), (ValueError, bf.moe_combine, (rows, slots.cpu(), w), {}),
+            (ValueError, bf.moe_combine_backward, (x, rows[:4], slots, w), {}), (TypeError, bf.moe_combine_backward, (x.float(), rows, slots, w), {}),
+            (ValueError, bf.gemm_1x128_128x128_routed, (code, scale, code, scale, edges, 2, 128 * H, 2, 2, 1), {}),
+            (TypeError, bf.gemm_1x128_128x128_routed, (code, scale, code, scale, edges.int(), 1, 0, 0, 2, 1), {}),
+            (ValueError, bf.gemm_1x128_128x128_routed, (code, scale, code, scale, edges[:1], 1, 0, 0, 2, 1), {}),
+            (ValueError, bf.gemm_1x128_128x128_routed, (code, scale, code, scale, edges, 1, 0, 0, 2, 2 ** 62), {}),
+            (ValueError, bf.gemm_1x128_128x128_routed, (code, scale, code, scale, edges, 1, 0, 0, 2, 1), dict(ldb=2 ** 62)),
+            (bf.Bsfp8Error, bf.moe_route, (long, 1), {}), (bf.Bsfp8Error, bf.moe_route_backward, (long, long_ids, long_ids.float()), {}),
+            (ValueError, bf.moe_route_backward, (z[:4], ids, w), {}), (TypeError, bf.moe_route_backward, (z, ids, held), {})]:
+        for _ in range(3):
+            with pytest.raises(kind):
+                f(*args, **kw)
+    args = kw = None
+    gc.collect()          # what the raised errors' frames held
+    torch.cuda.synchronize()
+    assert torch.all(held == 7)
+    assert torch.cuda.memory_allocated() <= before

@@ -4,6 +4,7 @@ compare with agree with differences of the forward definition."""
 import ctypes
 import os
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -276,3 +277,31 @@ def test_route_reference_by_hand():
     z = np.array([[2.0, -9.0, 1.5, 1.5]])
     assert ref.route(z, 2, "sigmoid", groups=2)[1].tolist() == [[0, 1]]
     assert ref.route(z, 2, "sigmoid", bias=np.zeros(4), groups=2)[1].tolist() == [[2, 3]]
+
+
+def test_one_step_calls_leave_the_unusual_alone():
+    """The C part of the binding answers None, without an exception and without keeping a reference, to whatever is no
+    plain GPU tensor or out of range: the checks of the Python functions then say what is wrong."""
+    from blockwise_scaled_fp8_act_amd import binding
+    binding.lib()
+    calls = binding._calls
+    assert calls is not None
+    z, f, i = torch.randn(4, 64), torch.zeros(4, 2), torch.zeros(4, 2, dtype=torch.int32)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    good = {"moe_route": (z, 2, "softmax", None, 1, 1, True, 1.0, f, i), "moe_route_backward": (z, i, f, "softmax", True, 1.0, None),
+            "moe_plan": (i, 8, None, None, None, None), "moe_dispatch": (x, i, None, None, None, False), "moe_combine": (x, i, f, None),
+            "moe_combine_backward": (x, x, i, f, None, None),
+            "gemm_1x128_128x128_routed": (x, f, x, f, f, 2, 128, 1, 1, 1, None, i, 2, False, None, None)}
+    odd = (None, 3, "x", 2.5, float("nan"), 2 ** 70, -1, [1], torch.nn.Parameter(z), z.t(), z[0], z[:0], z.double(), torch.zeros(2, 2, 2))
+    count = [sys.getrefcount(o) for o in odd + (z, f, i, x)]
+    for name, args in good.items():
+        call = getattr(calls, name)
+        assert call(*args) is None                               # tensors of the CPU
+        assert call() is None and call(*args[:-1]) is None and call(*args, 1) is None
+        for at in range(len(args)):
+            for o in odd:
+                assert call(*args[:at], o, *args[at + 1:]) is None
+    o = args = None
+    good.clear()
+    now = [sys.getrefcount(o) for o in odd + (z, f, i, x)]
+    assert all(abs(a - b) <= 16 for a, b in zip(count, now)), (count, now)
