@@ -98,10 +98,10 @@ static int matrix(PyObject* t, View* v, int type, int64_t a, int64_t b) {
 
 /* A new dense tensor on like's device: b < 0 for one dimension. */
 static int make(const View* like, View* v, int type, int64_t a, int64_t b) {
-    PyObject* shape = b < 0 ? Py_BuildValue("(L)", (long long)a) : Py_BuildValue("(LL)", (long long)a, (long long)b);
+    PyObject* shape = b < 0 ? PyLong_FromLongLong(a) : Py_BuildValue("(LL)", (long long)a, (long long)b);
     if (shape == NULL) return 0;
     PyObject* args[3] = {like->t, shape, types[type]};
-    v->t = PyObject_VectorcallMethod(n_new_empty, args, 2 | PY_VECTORCALL_ARGUMENTS_OFFSET, n_dtype_only);
+    v->t = PyObject_VectorcallMethod(n_new_empty, args, 2, type == like->type ? NULL : n_dtype_only);
     Py_DECREF(shape);
     v->made = v->t != NULL;
     v->type = type;
