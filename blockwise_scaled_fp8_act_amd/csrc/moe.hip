@@ -692,7 +692,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
 //   softmax:               dz = p (dp - sum dp p) on all experts, dp = s dw on the chosen ones;
 //   sigmoid:               dz = dp p (1 - p) on the chosen ones, dp = s (dw - sum dw p / D) / D when
 //                          renormalized (D the sum of the chosen p, a constant where it is floored).
-// Latency only: 8191 rows of 64 experts in bf16, 2.3 MB, take 5.4 us.
+// For more than 16 choices or 256 experts; the rest: route_backward_team_kernel.
 template <typename LT, int V>
 __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* logits, int64_t T, int E, int64_t ld,
                                                                      int softmax, int k, int renormalize, float scale,
@@ -758,6 +758,122 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* l
 #pragma unroll
     for (int v = 0; v < V; ++v)
         if (v * 64 + lane < E) store_logit(dlogits + t * ldd + v * 64 + lane, dz[v]);
+}
+
+template <int V>
+__device__ __forceinline__ void store_run(float* p, bool vec, int left, const float (&z)[V]) {
+    if (V % 4 == 0 && vec) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4)
+            if (v < left) *reinterpret_cast<float4*>(p + v) = float4{z[v], z[v + 1], z[v + 2], z[v + 3]};
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < left) p[v] = z[v];
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_run(uint16_t* p, bool vec, int left, const float (&z)[V]) {
+    if (V % 4 == 0 && vec) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4)
+            if (v < left) *reinterpret_cast<uint2*>(p + v) = uint2{pack_bf16x2(z[v], z[v + 1]), pack_bf16x2(z[v + 2], z[v + 3])};
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < left) p[v] = to_bf16(z[v]);
+    }
+}
+
+// The same for up to 16 choices and 256 experts: 16 lanes a token, sums by DPP; a lane holds four
+// experts of every 64, so that a token's lanes store whole lines, and the choices, which differ, find
+// their experts through LDS. 8191 rows of 64 experts in bf16 2.5 us (with a wave a token and sums by
+// shuffles 4.2), 16384 of 256 with sigmoid scores in fp32 6.4 (10.6; 8.4 with a comparison for every
+// choice and expert), with the plain softmax 9.7 (12.8).
+template <typename LT, int V>
+__global__ __launch_bounds__(64 * kWaves) void route_backward_team_kernel(const LT* logits, int64_t T, int E, int64_t ld,
+                                                                          int softmax, int k, int renormalize, float scale,
+                                                                          const int32_t* ids, const float* dweights,
+                                                                          LT* dlogits, int64_t ldd, int vec, int dvec) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15;
+    constexpr int C = V < 4 ? V : 4;  // consecutive experts
+    const int e0 = sub * C;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * 4;
+    if (t0 >= T) return;
+    const bool live = t0 + (lane >> 4) < T;
+    const int64_t t = live ? t0 + (lane >> 4) : T - 1;
+    const LT* row = logits + t * ld;
+
+    int id = sub < k ? ids[t * k + sub] : -1;
+    float dw = sub < k ? dweights[t * k + sub] : 0.0f;
+    const bool have = id >= 0 && id < E;
+    if (!have) {
+        id = -1;
+        dw = 0.0f;
+    }
+    const float zc = have ? load_logit(row + id) : -INFINITY;
+    float dz[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) dz[v] = 0.0f;
+    __shared__ __attribute__((aligned(16))) float spread[kWaves * 4][16 * V];
+    float* const mine = spread[wave * 4 + (lane >> 4)];
+#pragma unroll
+    for (int c = 0; c < V / C; ++c)
+#pragma unroll
+        for (int i = 0; i < C; ++i) mine[64 * c + e0 + i] = 0.0f;
+    wave_lds_fence();
+    float add = 0.0f;  // what this lane's choice adds to its expert's dz
+    if (softmax && renormalize) {
+        const float ztop = from_ordered(umax_row16(ordered(zc)));
+        const float x = have ? expf(zc - ztop) : 0.0f;
+        const float q = x / sum_row16(x);
+        add = scale * q * (dw - sum_row16(have ? q * dw : 0.0f));
+    } else if (softmax) {
+        float z[V], total = 0.0f;
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < V / C; ++c) {
+            float part[C];
+            load_run<C>(row + 64 * c + e0, vec && E % 4 == 0, E - 64 * c - e0, part);
+#pragma unroll
+            for (int i = 0; i < C; ++i) z[C * c + i] = part[i];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
+        const float top = from_ordered(umax_row16(m));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            z[v] = expf(z[v] - top);
+            total += z[v];
+        }
+        total = sum_row16(total);
+        const float q = have ? expf(zc - top) / total : 0.0f;
+        add = scale * dw * q;
+        const float sum = sum_row16(have ? add : 0.0f);
+        const bool any = sum_row16(have ? 1.0f : 0.0f) != 0.0f;
+        const float f = any ? -(sum / total) : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) dz[v] = any ? z[v] * f : 0.0f;
+    } else {
+        const float q = have ? 1.0f / (1.0f + expf(-zc)) : 0.0f;
+        float dq = scale * dw;
+        if (renormalize) {
+            const float sum = sum_row16(q), D = fmaxf(sum, kSumFloor);
+            const float mean = sum_row16(q * dw) / D;
+            dq = scale * (dw - (sum < kSumFloor ? 0.0f : mean)) / D;
+        }
+        add = dq * q * (1.0f / (1.0f + expf(zc)));
+    }
+    if (have) __hip_atomic_fetch_add(mine + id, add, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+    wave_lds_fence();
+    if (!live) return;
+#pragma unroll
+    for (int c = 0; c < V / C; ++c) {
+        float part[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) part[i] = dz[C * c + i] + mine[64 * c + e0 + i];
+        store_run<C>(dlogits + t * ldd + 64 * c + e0, dvec && E % 4 == 0, E - 64 * c - e0, part);
+    }
 }
 
 // ---------------------------------------------------------------------------------------- plan
@@ -1189,6 +1305,16 @@ static hipError_t route_backward_v(const LT* logits, int64_t T, int E, int64_t l
     return hipGetLastError();
 }
 
+template <typename LT, int V>
+static hipError_t route_backward_team(const LT* logits, int64_t T, int E, int64_t ld, const RouteRule& r, const int32_t* ids,
+                                      const float* dweights, LT* dlogits, int64_t ldd, hipStream_t stream) {
+    const int64_t blocks = (T + 4 * kWaves - 1) / (4 * kWaves);
+    route_backward_team_kernel<LT, V><<<dim3(static_cast<unsigned>(blocks)), 64 * kWaves, 0, stream>>>(
+        logits, T, E, ld, r.softmax, r.k, r.renormalize, r.scale, ids, dweights, dlogits, ldd, rows16(logits, ld * sizeof(LT)),
+        rows16(dlogits, ldd * sizeof(LT)));
+    return hipGetLastError();
+}
+
 // Experts per lane: the smallest of 1, 2, 4, 8, 16 that holds E <= 1024.
 #define BSFP8_BY_EXPERTS(call)                  \
     (E <= 64    ? call(1)                       \
@@ -1217,6 +1343,11 @@ static hipError_t route_t(const LT* logits, const RouteArgs& a, hipStream_t stre
 template <typename LT>
 static hipError_t route_backward_t(const void* logits, int64_t T, int E, int64_t ld, const RouteRule& r, const int32_t* ids,
                                    const float* dweights, void* dlogits, int64_t ldd, hipStream_t stream) {
+    if (r.k <= 16 && E <= 256) {
+#define CALL(V) route_backward_team<LT, V>(static_cast<const LT*>(logits), T, E, ld, r, ids, dweights, static_cast<LT*>(dlogits), ldd, stream)
+        return E <= 16 ? CALL(1) : E <= 64 ? CALL(4) : E <= 128 ? CALL(8) : CALL(16);
+#undef CALL
+    }
 #define CALL(V) route_backward_v<LT, V>(static_cast<const LT*>(logits), T, E, ld, r, ids, dweights, static_cast<LT*>(dlogits), ldd, stream)
     return BSFP8_BY_EXPERTS(CALL);
 #undef CALL
