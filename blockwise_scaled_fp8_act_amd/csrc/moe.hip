@@ -927,7 +927,7 @@ __global__ __launch_bounds__(64 * W) void plan_kernel(PlanArgs a) {
     extern __shared__ int32_t bin_lds[];
     static_assert(kRound <= 0xFFFF, "a wave's place in a bin is kept in 16 bits");
     __shared__ int32_t wave_total[W];
-    __shared__ uint16_t row_pair[MANY ? 1 : kRound];  // without MANY: a row's pair, kNoPair for none
+    __shared__ uint16_t row_pair[MANY ? 2 : kRound];  // without MANY: a row's pair, kNoPair for none
     constexpr uint16_t kNoPair = 0xFFFF;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = a.E + 1;
     const int bits = 32 - __builtin_clz(a.E);  // E itself needs a place
