@@ -48,6 +48,18 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// Below this logit sigmoid scores are formed in 64 bits: 1 / (1 + exp(-z)) in fp32 is 0 from -88.7 on,
+// where exp(-z) overflows, while the score and a floored sum of such still give ordinary weights.
+constexpr float kFarLogit = -80.0f;
+__device__ __forceinline__ double far_score(float z) { return 1.0 / (1.0 + exp(-static_cast<double>(z))); }
+
+// Sum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ double sum_row16(double v) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
 // ------------------------------------------------------------------------------------- routing
 // Scores and keys that decide a choice are compared in 64 bits: the choice is made between values
 // that may lie closer together than fp32 rounding, and its results are whole numbers.
@@ -672,6 +684,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         const float sum = sum_row16(w);
         if (a.renormalize) w /= fmaxf(sum, kSumFloor);
     }
+    w *= a.scale;
+    const uint64_t far = __ballot(!a.softmax && chosen && zc < kFarLogit && live && !bad);
+    if (far != 0) {
+        const double p = chosen ? far_score(zc) : 0.0, sum = sum_row16(p);
+        if ((far & team_lanes) != 0) w = static_cast<float>(a.scale * (a.renormalize ? p / fmax(sum, static_cast<double>(kSumFloor)) : p));
+    }
     if (live && sub < k) {
         if (bad) {  // no probabilities: no expert, NaN weights
             a.weights[t * k + sub] = NAN;
@@ -682,7 +700,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
         }
     }
     if (live && !bad && chosen) {
-        a.weights[t * k + rank] = a.scale * w;
+        a.weights[t * k + rank] = w;
         a.ids[t * k + rank] = id;
     }
 }
