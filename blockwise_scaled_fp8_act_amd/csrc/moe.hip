@@ -708,8 +708,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
 // One wave a token: the gradient of the chosen weights, spread over the row's logits.
 //   softmax, renormalized: dz = s q (dw - sum q dw) on the chosen experts, q = softmax over them;
 //   softmax:               dz = p (dp - sum dp p) on all experts, dp = s dw on the chosen ones;
-//   sigmoid:               dz = dp p (1 - p) on the chosen ones, dp = s (dw - sum dw p / D) / D when
-//                          renormalized (D the sum of the chosen p, a constant where it is floored).
+//   sigmoid:               dz = s q (dw - sum dw q) (1 - p) on the chosen ones, q = p / D, when renormalized
+//                          (D the sum of the chosen p; floored it is a constant, without the sum of
+//                          dw q), else dz = s p dw (1 - p). p is divided first: q is at most 1, while
+//                          dw / D overflows where the scores are small.
 // For more than 16 choices or 256 experts; the rest: route_backward_team_kernel.
 template <typename LT, int V>
 __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* logits, int64_t T, int E, int64_t ld,
@@ -756,14 +758,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* l
             for (int v = 0; v < V; ++v) dz[v] = -(p[v] / total) * sum;
             add = scale * dw * q;
         } else {
-            const float q = id >= 0 ? 1.0f / (1.0f + expf(-zc)) : 0.0f;
-            float dq = scale * dw;
+            float q = id >= 0 ? 1.0f / (1.0f + expf(-zc)) : 0.0f, mean = 0.0f;
             if (renormalize) {
-                const float sum = wave_sum(q), D = fmaxf(sum, kSumFloor);
-                const float mean = wave_sum(q * dw) / D;
-                dq = scale * (dw - (sum < kSumFloor ? 0.0f : mean)) / D;
+                const float sum = wave_sum(q);
+                q /= fmaxf(sum, kSumFloor);
+                mean = sum < kSumFloor ? 0.0f : wave_sum(q * dw);
             }
-            add = id >= 0 ? dq * q * (1.0f / (1.0f + expf(zc))) : 0.0f;
+            add = scale * (q * (dw - mean) * (1.0f / (1.0f + expf(zc))));
         }
         for (int j = 0; j < k; ++j) {
             const int at = __builtin_amdgcn_readlane(id, j);
@@ -873,14 +874,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_team_kernel(const 
 #pragma unroll
         for (int v = 0; v < V; ++v) dz[v] = any ? z[v] * f : 0.0f;
     } else {
-        const float q = have ? 1.0f / (1.0f + expf(-zc)) : 0.0f;
-        float dq = scale * dw;
+        float q = have ? 1.0f / (1.0f + expf(-zc)) : 0.0f, mean = 0.0f;
         if (renormalize) {
-            const float sum = sum_row16(q), D = fmaxf(sum, kSumFloor);
-            const float mean = sum_row16(q * dw) / D;
-            dq = scale * (dw - (sum < kSumFloor ? 0.0f : mean)) / D;
+            const float sum = sum_row16(q);
+            q /= fmaxf(sum, kSumFloor);
+            mean = sum < kSumFloor ? 0.0f : sum_row16(q * dw);
         }
-        add = dq * q * (1.0f / (1.0f + expf(zc)));
+        add = scale * (q * (dw - mean) * (1.0f / (1.0f + expf(zc))));
     }
     if (have) __hip_atomic_fetch_add(mine + id, add, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     wave_lds_fence();

@@ -1,6 +1,7 @@
 """GPU tests of sigmoid routing where the scores leave fp32's ordinary range: logits from -80 on, whose scores
 and their sums reach the smallest normal number (2^-126, the floor of a renormalized sum) and below.
-References and bounds as in test_gpu_moe_ops.py: weights 32 * 2^-24 relative and one subnormal step."""
+References and bounds as in test_gpu_moe_ops.py: weights 32 * 2^-24 relative and one subnormal step; gradients
+64 * 2^-24 of the magnitudes that enter an element, half a step of its type and one bf16 subnormal step."""
 import numpy as np
 import pytest
 import torch
@@ -51,3 +52,36 @@ def test_sigmoid_weights_of_far_logits(E, k, dtype):
                     want, want_ids = ref.route(zh, k, "sigmoid", bias, groups, top, renormalize=renorm, scale=2.5)
                 assert np.array_equal(ids.cpu().numpy(), want_ids), (bias is None, renorm, groups)
                 assert np.all(np.abs(_np(w) - want) <= 32 * E24 * np.abs(want) + 2.0 ** -149), (bias is None, renorm, groups)
+
+
+def _check_gradient(z, zh, ids, dw, renorm, what):
+    dz = bf.moe_route_backward(z, torch.from_numpy(ids).to(DEV), torch.from_numpy(dw).to(DEV), score="sigmoid", renormalize=renorm, scale=2.5)
+    with np.errstate(over="ignore"):
+        want, size = ref.route_backward(zh, ids, dw, "sigmoid", renorm, 2.5)
+    half = 2.0 ** -8 if z.dtype == BF else E24
+    assert np.all(np.abs(_np(dz) - want) <= 64 * E24 * size + half * np.abs(want) + 2.0 ** -133), what
+
+
+def _gradients(seed, T, k):
+    """Weights' gradients of ordinary size, of a loss scaled by 65536, and of 1e30."""
+    g = np.random.Generator(np.random.PCG64(seed))
+    dw = g.standard_normal((T, k))
+    return [(s * dw).astype(np.float32) for s in (1.0, 65536.0, 1e30)] + [np.full((T, k), 2.0, np.float32)]
+
+
+BACK = [(8, 1), (8, 8), (16, 4), (64, 16), (256, 8), (384, 8), (64, 17), (300, 24)]
+
+
+@pytest.mark.parametrize("E,k", BACK)
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_sigmoid_gradient_stays_finite_where_scores_are_small(E, k, dtype):
+    """Scores that sum to 1e-37 (above the floor) or to nothing (below): the gradient is of the weights'
+    gradient's size, however small the sum is that divides."""
+    T = 12
+    g = np.random.Generator(np.random.PCG64(E))
+    zh = np.repeat(np.array([-70.0, -80.0, -85.0, -1e4, -3e38, -60.0])[:, None], 2, 0) + 0.5 * g.standard_normal((T, E))
+    z = torch.from_numpy(zh.astype(np.float32)).to(DEV).to(dtype)
+    ids = ref.choose(g, T, k, E, dropped=0.1)
+    for i, dw in enumerate(_gradients(k, T, k)):
+        for renorm in (True, False):
+            _check_gradient(z, _np(z), ids, dw, renorm, (i, renorm))
