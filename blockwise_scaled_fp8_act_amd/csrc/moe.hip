@@ -705,6 +705,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, Ro
     }
 }
 
+// A choice's part of the sigmoid gradient in 64 bits; p: its score, sum, dot: the sums of p, p dw.
+__device__ __forceinline__ float far_gradient(double p, double sum, double dot, float z, float dw, int renormalize, float scale) {
+    const double D = renormalize ? fmax(sum, static_cast<double>(kSumFloor)) : 1.0;
+    const double mean = renormalize && sum >= kSumFloor ? dot / D : 0.0;
+    return static_cast<float>(scale * (p / D * (dw - mean)) * far_score(-z));
+}
+
 // One wave a token: the gradient of the chosen weights, spread over the row's logits.
 //   softmax, renormalized: dz = s q (dw - sum q dw) on the chosen experts, q = softmax over them;
 //   softmax:               dz = p (dp - sum dp p) on all experts, dp = s dw on the chosen ones;
@@ -765,6 +772,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const LT* l
                 mean = sum < kSumFloor ? 0.0f : wave_sum(q * dw);
             }
             add = scale * (q * (dw - mean) * (1.0f / (1.0f + expf(zc))));
+            if (__any(id >= 0 && zc < kFarLogit)) {
+                const double p = id >= 0 ? far_score(zc) : 0.0;
+                add = far_gradient(p, wave_sum(p), wave_sum(p * dw), zc, dw, renormalize, scale);
+            }
         }
         for (int j = 0; j < k; ++j) {
             const int at = __builtin_amdgcn_readlane(id, j);
@@ -881,6 +892,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_team_kernel(const 
             mean = sum < kSumFloor ? 0.0f : sum_row16(q * dw);
         }
         add = scale * (q * (dw - mean) * (1.0f / (1.0f + expf(zc))));
+        const uint64_t far = __ballot(have && zc < kFarLogit);
+        if (far != 0) {
+            const double p = have ? far_score(zc) : 0.0;
+            const float x = far_gradient(p, sum_row16(p), sum_row16(p * dw), zc, dw, renormalize, scale);
+            if (((far >> (lane & 48)) & 0xFFFF) != 0) add = x;
+        }
     }
     if (have) __hip_atomic_fetch_add(mine + id, add, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     wave_lds_fence();

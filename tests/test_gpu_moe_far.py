@@ -85,3 +85,15 @@ def test_sigmoid_gradient_stays_finite_where_scores_are_small(E, k, dtype):
     for i, dw in enumerate(_gradients(k, T, k)):
         for renorm in (True, False):
             _check_gradient(z, _np(z), ids, dw, renorm, (i, renorm))
+
+
+@pytest.mark.parametrize("E,k", BACK)
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_sigmoid_gradient_of_far_logits(E, k, dtype):
+    z, zh = _far_logits(E + k, E, dtype)
+    T = z.shape[0]
+    ids = ref.choose(np.random.Generator(np.random.PCG64(E)), T, k, E, dropped=0.1)
+    ids = np.where(np.isneginf(np.take_along_axis(zh, ids.clip(0, E - 1).astype(np.int64), 1)), -1, ids).astype(np.int32)
+    for i, dw in enumerate(_gradients(k, T, k)):
+        for renorm in (True, False):
+            _check_gradient(z, zh, ids, dw, renorm, (i, renorm))
