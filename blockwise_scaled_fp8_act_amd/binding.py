@@ -568,7 +568,8 @@ def _empty(like, shape, dtype, stream):
     if stream is None or not like.is_cuda:
         return like.new_empty(shape, dtype=dtype)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        handle = int(stream)        # 0 is the default stream's; ExternalStream(0) would make a new stream
+        stream = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
