@@ -105,14 +105,13 @@ def _bind_calls(L):
     """Load _calls.so: the usual call of the small operators in one step (a function of it returns None
     where an argument is not as usual, and the checks below say what is wrong)."""
     global _calls
-    get_device = getattr(torch._C, "_cuda_getDevice", None)
-    if get_device is None or _raw_stream is None:
+    if _raw_stream is None:
         return
     try:
         from . import _calls as calls
     except ImportError as e:
         raise ImportError("_calls.so is missing beside libbsfp8.so: build it with `python -m blockwise_scaled_fp8_act_amd.build`") from e
-    calls.bind(torch.Tensor, Bsfp8Error, get_device, _raw_stream,
+    calls.bind(torch.Tensor, Bsfp8Error, _get_device, _raw_stream,
                (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float8_e4m3fn),
                tuple(ctypes.cast(f, _vp).value for f in (L.moe_route, L.moe_route_backward, L.moe_plan_workspace, L.moe_plan,
                                                          L.moe_dispatch, L.moe_combine, L.moe_combine_backward,
@@ -123,6 +122,8 @@ def _bind_calls(L):
 # the current stream's handle without building a torch.cuda.Stream object (0.1 against ~3 us per
 # call), where this torch provides it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current GPU's index, once a GPU tensor exists (torch.cuda is initialised then)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream, dev=None):
@@ -246,7 +247,7 @@ def _gpu(**tensors):
             if at < 0:
                 raise ValueError(f"{name} must be a GPU tensor, got one on {t.device}")
             if dev is None:
-                dev = torch._C._cuda_getDevice()    # a GPU tensor exists: torch.cuda is initialised
+                dev = _get_device()
             if at != dev:
                 _on_gpu(name, t, dev)
     return dev
@@ -580,7 +581,7 @@ def _current(first, *rest):
     for t in rest:
         if t is not None and t.get_device() != dev:
             return None
-    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else None
+    return dev if dev >= 0 and dev == _get_device() else None
 
 
 def _choices(name, t, dtype):

@@ -1,11 +1,16 @@
 """CPU checks of the mixture-of-experts binding around its calls: where outputs are allocated, and what the
 package does without the parts that are not everywhere."""
 import contextlib
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from blockwise_scaled_fp8_act_amd import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class _Like:
@@ -39,3 +44,31 @@ def test_outputs_belong_to_the_stream_whose_handle_is_given(monkeypatch, handle,
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
     assert binding._empty(_Like(current), (2, 3), torch.int32, handle) == (want, (2, 3), torch.int32)
     assert binding._empty(_Like(current), 5, torch.uint8, None) == ("current", 5, torch.uint8)
+
+
+def test_checks_work_where_torch_lacks_its_shortcuts():
+    """A torch without the private functions that the binding prefers: every check of a GPU tensor, the older entry
+    points' among them, goes by the public ones."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+torch.cuda.current_device = lambda: 1
+from blockwise_scaled_fp8_act_amd import binding
+class T:
+    device, is_cuda = "cuda", True
+    def __init__(self, at): self.at = at
+    def get_device(self): return self.at
+assert binding._gpu(x=T(1), y=None) == 1 and binding._current(T(1), None, T(1)) == 1 and binding._current(T(0)) is None
+try:
+    binding._gpu(x=T(0))
+except ValueError as e:
+    assert "current device" in str(e)
+else:
+    raise SystemExit("accepted a tensor of another device")
+binding.lib()
+assert binding._calls is None
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
