@@ -1,8 +1,9 @@
 """Thin ctypes binding of libbsfp8.so (the gfx950 HIP library); declarations in include/blockwise_fp8.h.
 
 Argument marshalling only: every step runs in the HIP kernels. torch provides device memory and the
-current stream. The functions of the mixture-of-experts operators first offer their arguments to
-_calls.so (csrc/calls.c), which makes the usual call without ctypes. There is no CPU fallback: if the library is missing, loading raises.
+current stream. The functions of the mixture-of-experts operators first offer their arguments to the
+C part _calls (csrc/calls.c), if it was built, which makes the usual call without ctypes. There is no
+CPU fallback: if the library is missing, loading raises.
 
 Tensor conventions (torch, on the GPU):
   bf16 inputs       torch.bfloat16 (or int16/uint16 holding bf16 bits)
@@ -33,7 +34,7 @@ _i32 = ctypes.c_int
 _f32 = ctypes.c_float
 
 _lib = None
-_calls = None       # the C part (csrc/calls.c), where torch has what it is bound to
+_calls = None       # the C part (csrc/calls.c), where it was built and torch has what it is bound to
 
 
 class Bsfp8Error(RuntimeError):
@@ -102,15 +103,15 @@ def lib():
 
 
 def _bind_calls(L):
-    """Load _calls.so: the usual call of the small operators in one step (a function of it returns None
+    """Load _calls, where it was built: the usual call of the small operators in one step (a function of it returns None
     where an argument is not as usual, and the checks below say what is wrong)."""
     global _calls
     if _raw_stream is None:
         return
     try:
         from . import _calls as calls
-    except ImportError as e:
-        raise ImportError("_calls.so is missing beside libbsfp8.so: build it with `python -m blockwise_scaled_fp8_act_amd.build`") from e
+    except ImportError:         # not built, or for another interpreter: the same kernels, called through ctypes
+        return
     calls.bind(torch.Tensor, Bsfp8Error, _get_device, _raw_stream,
                (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float8_e4m3fn),
                tuple(ctypes.cast(f, _vp).value for f in (L.moe_route, L.moe_route_backward, L.moe_plan_workspace, L.moe_plan,

@@ -4,11 +4,12 @@ import contextlib
 import os
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 import torch
 
-from blockwise_scaled_fp8_act_amd import binding
+from blockwise_scaled_fp8_act_amd import binding, build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -72,3 +73,35 @@ assert binding._calls is None
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_library_works_without_the_c_part(monkeypatch):
+    """_calls not built, or for another interpreter: the library loads, and the long way of a call answers."""
+    import blockwise_scaled_fp8_act_amd as bf
+    monkeypatch.delattr(bf, "_calls", raising=False)
+    monkeypatch.setitem(sys.modules, bf.__name__ + "._calls", None)
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "_calls", None)
+    assert binding.lib().bsfp8_status_string(0) and binding._calls is None
+    with pytest.raises(ValueError, match="k = 17"):
+        bf.moe_route(torch.zeros(4, 16), 17)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        bf.moe_route(torch.zeros(4, 16), 2)
+
+
+def test_c_part_is_built_for_this_interpreter_or_left_out(monkeypatch, tmp_path):
+    """Its name carries the interpreter's tag; without Python's headers or a C compiler the build goes on, and
+    nothing that an earlier build made stays behind."""
+    assert build.CALLS_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    here = str(tmp_path)
+    old = tmp_path / "_calls.so"
+    monkeypatch.setattr(build, "PKG", here)
+    monkeypatch.setattr(build, "CALLS_PATH", os.path.join(here, os.path.basename(build.CALLS_PATH)))
+    old.write_bytes(b"of another interpreter")
+    assert build._build_calls() and os.listdir(here) == [os.path.basename(build.CALLS_PATH)]
+    for name, value in (("CC", "no-such-compiler"), ("sysconfig", type("S", (), {"get_paths": staticmethod(lambda: {"include": here})}))):
+        old.write_bytes(b"of another interpreter")
+        with monkeypatch.context() as m:
+            m.setattr(build, name, value)
+            assert not build._build_calls() and os.listdir(here) == []
+        assert build._build_calls()
