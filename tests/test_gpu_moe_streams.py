@@ -1,5 +1,5 @@
 """GPU tests of the mixture-of-experts calls' memory and streams: outputs belong to the stream that the call
-names, workspaces can be shared by calls in a row, the plan's two launches replay from a graph."""
+names."""
 import pytest
 import torch
 
