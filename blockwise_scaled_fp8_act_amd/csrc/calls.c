@@ -2,8 +2,8 @@
  * current GPU, the current stream, every argument as binding.py's functions want it. A function here
  * looks at its arguments, makes the outputs that are not given, calls the library and returns what
  * binding.py's function of that name returns; where anything is not as usual it returns None and has
- * done nothing, and binding.py goes the long way, whose checks say what is wrong. What is accepted
- * here is a part of what is accepted there. A tensor is read through its Python attributes, so nothing
+ * done nothing, and binding.py goes the long way, whose checks say what is wrong (so too where this part
+ * was not built). What is accepted here is a part of what is accepted there. A tensor is read through its Python attributes, so nothing
  * depends on torch's binary interface.
  *
  * Why: for few tokens these operators' kernels take 3 to 9 us and the launch 3.3. A call here takes 4.6

@@ -328,13 +328,17 @@ constexpr float kKeyRounding = 6e-8f;     // 2^-24, of a key or a sum: the round
 // one unsigned maximum over the lanes (a DPP step each) yields key and index, and the owner drops
 // the head of its sorted run. Where neighbours among the k + 2 (at most 16) best are too close for the
 // cut keys to order them, the candidates are ranked by their exact keys, one a lane. Where the cut
-// keys cannot tell that the k best are among the candidates (three keys nearly equal at the border),
+// keys cannot tell that the k best are among the candidates (the k-th too close to the best key that is
+// none: four nearly equal keys at the border, three for k = 15, two for k = 16),
 // the choices are made one by one from 64-bit keys; where fp32 cannot tell which groups are kept,
 // the groups are valued again in 64 bits. KEY: the logits, which are exact, or a score + bias.
-// Bound by vector issue, 877 instructions a wave of four tokens at 256 experts in groups, nearly half
-// of them the sort and the takes, and by its slowest waves: 16384 tokens 12.7 us in a graph (15.7 where
+// 16384 tokens of 256 experts in groups 10.8 us in a graph, 12.3-12.9 with inputs that change (15.7 where
 // each lane formed its own exact keys; 48 with one wave a token and 64-bit shuffles; their bytes alone
-// 3.4), with a softmax and no groups 12.4 (16.3), one token 4.2 us.
+// 3.4), with a softmax and no groups 10.7 and 12.6 (16.3), one token 4.2 us. Vector issue is about half
+// of that: 880 instructions a wave of four tokens, nearly half of them the sort and the takes, 14
+// thousand of 26 thousand cycles, all waves in one round. The launch ends with its slowest waves, most
+// likely those with exact keys: the cut's tolerance (2^-14 of a key at 256 experts) holds neighbours of
+// 4% of the tokens, so of 15% of the waves, where fp32's own error would hold those of 0.05%.
 template <typename LT, int V, int L, RouteKey KEY>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(const LT* logits, RouteArgs a) {
     extern __shared__ double lds[];
@@ -818,7 +822,7 @@ __device__ __forceinline__ void store_run(uint16_t* p, bool vec, int left, const
 // The same for up to 16 choices and 256 experts: 16 lanes a token, sums by DPP; a lane holds four
 // experts of every 64, so that a token's lanes store whole lines, and the choices, which differ, find
 // their experts through LDS. 8191 rows of 64 experts in bf16 2.5 us (with a wave a token and sums by
-// shuffles 4.2), 16384 of 256 with sigmoid scores in fp32 6.4 (10.6; 8.4 with a comparison for every
+// shuffles 4.2), 16384 of 256 with sigmoid scores in fp32 5.9-6.4 (10.6; 8.4 with a comparison for every
 // choice and expert), with the plain softmax 9.7 (12.8).
 template <typename LT, int V>
 __global__ __launch_bounds__(64 * kWaves) void route_backward_team_kernel(const LT* logits, int64_t T, int E, int64_t ld,

@@ -15,7 +15,9 @@ Training (``blockwise_fp8_moe``) runs the grouped GEMMs of the dense layer's rec
 expert's first token. Serving (``ServingMoE``) keeps the quantized weights and runs the routed
 products, which read the tokens through the plan and join the gate and up halves, so a decode step
 moves the chosen experts' weights and little else. silu(G) * U of the training path is elementwise
-torch code; every other step runs in the library's kernels. All activations and weights are bf16 on
+torch code; every other step runs in the library's kernels. Training holds G and U in bf16, the grouped
+GEMM's output, since the backward takes them; serving joins them in fp32 before the one rounding, so the
+two forms of one layer differ by those roundings (at most 2^-8 of G and of U). All activations and weights are bf16 on
 the GPU, H and F multiples of 128.
 """
 from __future__ import annotations
@@ -166,7 +168,8 @@ class BlockwiseFp8MoE(torch.nn.Module):
 
 
 class ServingMoE:
-    """The layer for inference: the experts' weights quantized once, products for few rows an expert."""
+    """The layer for inference: the experts' weights quantized once, products for few rows an expert. Any
+    number of tokens is computed; from about 256 rows an expert the grouped GEMM is as fast."""
 
     def __init__(self, w_gate_up: torch.Tensor, w_down: torch.Tensor):
         self.E, self.F, self.H = _expert_weights(w_gate_up, w_down)

@@ -374,7 +374,8 @@ enum { BSFP8_SOFTMAX = 0, BSFP8_SIGMOID = 1 }; /* score of an expert */
  *   ids     [T, k] int32: the experts with the largest keys in the kept groups, largest first.
  *   weights [T, k] fp32: scale * p of the chosen experts (without the bias); renormalize != 0: divided
  *           by their sum (for softmax that is the softmax over the chosen logits; for sigmoid a sum
- *           below 2^-126 counts as 2^-126).
+ *           below 2^-126 counts as 2^-126). Sigmoid scores of a token with a chosen logit below -80
+ *           are formed and summed in 64 bits, so far logits have weights too.
  * Keys are formed and compared in 64 bits; equal keys (and groups) go to the lower index. An expert
  * whose logit is -inf, or whose bias is -inf or NaN, is never chosen; a choice that finds no expert has
  * id -1 and weight 0. A row with a NaN logit (softmax: or +inf) has ids -1 and weights NaN.
@@ -390,7 +391,8 @@ int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, c
  * itself has none). ids [T, k] as moe_route gave them (ids outside [0, E) have no gradient),
  * dweights [T, k] fp32, dlogits [T, E] in the logits' type with row stride lddl >= E; every element is
  * written. A row without a chosen expert has zero gradient. score, renormalize and scale as in the
- * forward call. Sums in fp32, one rounding.
+ * forward call. Sums in fp32 (sigmoid: 64 bits where a chosen logit is below -80), one rounding; a
+ * sigmoid score is divided by the sum before dweights comes in, so small sums do not overflow.
  */
 int moe_route_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int score, int64_t k,
                        int renormalize, float scale, const int32_t* ids, const float* dweights,
