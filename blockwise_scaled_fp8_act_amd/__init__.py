@@ -11,6 +11,7 @@ input generators (``inputs``).
 """
 from .binding import (  # noqa: F401
     Bsfp8Error,
+    clip_grads,
     encode_e4m3_f32,
     encode_e4m3fnuz_f32,
     fp8_format,
@@ -20,6 +21,9 @@ from .binding import (  # noqa: F401
     gemm_1x128_128x128_grouped,
     gemm_1x128_128x128_noalloc,
     gemm_1x128_128x128_routed,
+    gemm_i8,
+    grad_norm,
+    grad_workspace,
     moe_combine,
     moe_combine_backward,
     moe_dispatch,
@@ -32,7 +36,16 @@ from .binding import (  # noqa: F401
     quantize_lhs_and_weight,
     quantize_rhs,
     quantize_rhs_grouped,
+    quantize_rows_i8,
     quantize_weight_128x128,
+    rms_norm_backward,
+    rms_norm_backward_workspace,
+    rms_norm_quantize,
+    rms_norm_quantize_rhs,
+    swiglu_backward,
+    swiglu_backward_quantize,
+    swiglu_quantize,
+    swiglu_quantize_lhs_and_rhs,
 )
 from .linear import BlockwiseFp8Linear, blockwise_fp8_linear  # noqa: F401
 from .moe import BlockwiseFp8MoE, ServingMoE, blockwise_fp8_moe, route_experts  # noqa: F401

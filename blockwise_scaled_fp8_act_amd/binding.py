@@ -14,6 +14,7 @@ Tensor conventions (torch, on the GPU):
   RHS scales s      torch.float32 (Kb, N) row-major
   weight scales s   torch.float32 (Nb, Kb) row-major
   GEMM output       torch.bfloat16 [M, N]
+  int8 codes        torch.int8, one fp32 scale a row (M,)
 """
 from __future__ import annotations
 
@@ -82,6 +83,23 @@ def lib():
         L.moe_combine_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]
         L.gemm_1x128_128x128_routed.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
                                                 _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i32, _vp]
+        L.rms_norm_quantize.argtypes = [_vp, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i32, _f32, _vp, _i64, _vp, _i32, _vp, _i64,
+                                        _vp, _vp, _i64, _vp]
+        L.rms_norm_quantize_rhs.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _i64, _vp, _vp]
+        L.rms_norm_backward_workspace.argtypes = [_i64, _i64]
+        L.rms_norm_backward_workspace.restype = _i64
+        L.rms_norm_backward.argtypes = [_vp, _i64, _vp, _i32, _i64, _vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64,
+                                        _vp]
+        L.swiglu_quantize.argtypes = [_vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp]
+        L.swiglu_quantize_lhs_and_rhs.argtypes = [_vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp]
+        L.swiglu_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp]
+        L.swiglu_backward_quantize.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp]
+        L.quantize_rows_i8.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]
+        L.gemm_i8.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp]
+        L.grad_workspace.argtypes = [_vp, _i64]
+        L.grad_workspace.restype = _i64
+        L.grad_norm.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp]
+        L.clip_grads.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _i64, _vp]
         for f in ("quantize_lhs", "quantize_rhs", "quantize_weight_128x128", "gemm_1x128_128x128",
                   "gemm_1x128_128x1", "quantize_lhs_and_rhs", "encode_e4m3_f32",
                   "quantize_lhs_and_weight"):
@@ -95,7 +113,9 @@ def lib():
                   "gemm_1x128_128x128_fnuz", "gemm_1x128_128x1_fnuz", "encode_e4m3fnuz_f32",
                   "quantize_lhs_and_rhs_fnuz", "quantize_lhs_and_weight",
                   "quantize_lhs_and_weight_fnuz", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch",
-                  "moe_combine", "moe_combine_backward", "gemm_1x128_128x128_routed"):
+                  "moe_combine", "moe_combine_backward", "gemm_1x128_128x128_routed", "rms_norm_quantize",
+                  "rms_norm_quantize_rhs", "rms_norm_backward", "swiglu_quantize", "swiglu_quantize_lhs_and_rhs",
+                  "swiglu_backward", "swiglu_backward_quantize", "quantize_rows_i8", "gemm_i8", "grad_norm", "clip_grads"):
             getattr(L, f).restype = ctypes.c_int
         _bind_calls(L)
         _lib = L
@@ -870,3 +890,392 @@ def gemm_1x128_128x128_routed(a, a_s, b, b_s, offsets, E, b_stride, bs_stride, b
           b.data_ptr(), ldb, b_stride, b_s.data_ptr(), bs_stride, bs_stride_nb, bs_stride_kb, offsets.data_ptr(), E,
           c.data_ptr(), c.stride(0) if M > 1 else N, M, N, K, 1 if swiglu else 0, _stream(stream, dev))
     return c
+
+
+# ---------------------------------------------------------------- between the 8-bit products
+# The codes that an operator writes its rows in: the FP8 formats (1x128 groups), "int8" (one scale a row), None (no codes).
+_CODE_KINDS = {None: 0, "e4m3fn": 1, "e4m3fnuz": 2, "int8": 3}
+_TYPE_IDS = {torch.bfloat16: 0, torch.float32: 1}
+_BF16_F32 = (torch.bfloat16, torch.float32)
+MAX_ROWS = 2 ** 24 - 16
+MAX_I8_K = 131071
+
+
+def _code_kind(fmt):
+    if fmt is None or fmt == "int8":
+        return fmt
+    return fp8_format(fmt)
+
+
+def _stride(t, rows):
+    """Row stride to pass for a matrix that passed _matrix (whatever a single row's stride says)."""
+    return t.stride(0) if rows > 1 else t.shape[1]
+
+
+def _row_outputs(like, T, H, kind, q, s, y, want_y, stream):
+    """Checked or new outputs q, s, y of rows [T, H] in the codes ``kind``."""
+    if T > MAX_ROWS:
+        raise ValueError(f"{T} rows, at most {MAX_ROWS} are taken")
+    if kind is None:
+        if q is not None or s is not None:
+            raise ValueError("q and s are not written without codes (fmt=None)")
+        want_y = True
+    else:
+        shape = (T,) if kind == "int8" else (cdiv(H, BLOCK), T)
+        types = (torch.int8,) if kind == "int8" else _CODES[kind]
+        if q is None:
+            q = _empty(like, (T, H), types[0], stream)
+        else:
+            _matrix("q", q, types, (T, H))
+        if s is None:
+            s = _empty(like, shape, torch.float32, stream)
+        else:
+            _dense("s", s, torch.float32, shape)
+    if y is not None:
+        _matrix("y", y, _BF16, (T, H))
+    elif want_y:
+        y = _empty(like, (T, H), torch.bfloat16, stream)
+    return q, s, y
+
+
+def _tile_outputs(like, T, C, q, a_s, qT, s, stream, fmt):
+    """Checked or new outputs of both groupings of [T, C], named as quantize_lhs_and_rhs names them."""
+    if q is None:
+        q = _empty(like, (T, C), torch.uint8, stream)
+    else:
+        _codes("q", q, fmt, (T, C))
+    if a_s is None:
+        a_s = _empty(like, (cdiv(C, BLOCK), T), torch.float32, stream)
+    else:
+        _dense("a_s", a_s, torch.float32, (cdiv(C, BLOCK), T))
+    if qT is None:
+        qT = _empty(like, (C, T), torch.uint8, stream)
+    else:
+        _codes("qT", qT, fmt, (C, T))
+    if s is None:
+        s = _empty(like, (cdiv(T, BLOCK), C), torch.float32, stream)
+    else:
+        _dense("s", s, torch.float32, (cdiv(T, BLOCK), C))
+    return q, a_s, qT, s
+
+
+def _weight_of(weight, H):
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in _BF16_F32:
+        raise TypeError(f"weight must be a bfloat16 or float32 tensor, got {getattr(weight, 'dtype', type(weight).__name__)}")
+    return _dense("weight", weight, weight.dtype, (H,))
+
+
+def rms_norm_quantize(x, weight, residual=None, eps=1e-6, fmt="e4m3fn", q=None, s=None, h=None, y=None, rstd=None, want_y=False,
+                      want_rstd=False, stream=None):
+    """Root-mean-square norm of x [T, H] (bf16), with the residual's addition, as 8-bit codes. h = x +
+    residual in the residual's type (bf16 or fp32; h may be the residual itself), rstd = 1 / sqrt(mean(h^2)
+    + eps), v = h * rstd * weight (weight [H] bf16 or fp32). ``fmt``: "e4m3fn" or "e4m3fnuz" (q [T, H]
+    uint8, s (Hb, T) fp32, as quantize_lhs), "int8" (q int8, s (T,)), or None (y only). Returns (q, s, h, y,
+    rstd): h None without a residual (it is x), y [T, H] bf16 and rstd (T,) fp32 where given or wanted."""
+    kind = _code_kind(fmt)
+    T, H = _matrix("x", x, _BF16).shape
+    _weight_of(weight, H)
+    if not (eps > 0 and math.isfinite(eps)) or ctypes.c_float(eps).value in (0.0, math.inf):
+        raise ValueError(f"eps must be positive and finite, got {eps}")
+    res_type = 0
+    if residual is not None:
+        _matrix("residual", residual, _BF16_F32, (T, H))
+        res_type = _TYPE_IDS[residual.dtype]
+        if h is None:
+            h = _empty(residual, (T, H), residual.dtype, stream)
+        else:
+            _matrix("h", h, (residual.dtype,), (T, H))
+    elif h is not None:
+        raise ValueError("h is not written without a residual (it is x)")
+    q, s, y = _row_outputs(x, T, H, kind, q, s, y, want_y, stream)
+    if rstd is not None:
+        _dense("rstd", rstd, torch.float32, (T,))
+    elif want_rstd:
+        rstd = _empty(x, (T,), torch.float32, stream)
+    dev = _current(x, weight, residual, h, q, s, y, rstd)
+    if dev is None:
+        _gpu(x=x, weight=weight, residual=residual, h=h, q=q, s=s, y=y, rstd=rstd)
+    _call("rms_norm_quantize", _ptr(x), T, H, _stride(x, T), _ptr(residual), res_type, 0 if residual is None else _stride(residual, T),
+          _ptr(weight), _TYPE_IDS[weight.dtype], eps, _ptr(h), 0 if h is None else _stride(h, T), _ptr(rstd), _CODE_KINDS[kind], _ptr(q),
+          0 if q is None else _stride(q, T), _ptr(s), _ptr(y), 0 if y is None else _stride(y, T), _stream(stream, dev))
+    return q, s, h, y, rstd
+
+
+def rms_norm_quantize_rhs(h, weight, rstd, qT=None, s=None, stream=None, fmt="e4m3fn"):
+    """The normed rows h * rstd * weight in 128x1 groups, transposed (quantize_rhs of their fp32 values), from h
+    [T, H] (bf16 or fp32), weight [H] and rstd (T,) as rms_norm_quantize gave them. Returns (qT [H, T] uint8,
+    s (Tb, H) fp32)."""
+    kind = fp8_format(fmt)
+    T, H = _matrix("h", h, _BF16_F32).shape
+    _weight_of(weight, H)
+    _dense("rstd", rstd, torch.float32, (T,))
+    if qT is None:
+        qT = _empty(h, (H, T), torch.uint8, stream)
+    else:
+        _codes("qT", qT, kind, (H, T))
+    if s is None:
+        s = _empty(h, (cdiv(T, BLOCK), H), torch.float32, stream)
+    else:
+        _dense("s", s, torch.float32, (cdiv(T, BLOCK), H))
+    dev = _current(h, weight, rstd, qT, s)
+    if dev is None:
+        _gpu(h=h, weight=weight, rstd=rstd, qT=qT, s=s)
+    _call("rms_norm_quantize_rhs", _ptr(h), _TYPE_IDS[h.dtype], T, H, _stride(h, T), _ptr(weight), _TYPE_IDS[weight.dtype], _ptr(rstd),
+          _CODE_KINDS[kind], _ptr(qT), _stride(qT, H), _ptr(s), _stream(stream, dev))
+    return qT, s
+
+
+@functools.lru_cache(maxsize=1024)      # sizes alone decide it
+def _norm_backward_bytes(T, H):
+    return lib().rms_norm_backward_workspace(T, H)
+
+
+def rms_norm_backward_workspace(T, H):
+    """Bytes of device memory rms_norm_backward needs for T rows of H columns."""
+    need = _norm_backward_bytes(T, H)
+    if need < 0:
+        raise ValueError(f"no norm of {T} rows of {H} columns")
+    return need
+
+
+def _workspace(like, workspace, need, stream, align):
+    """The checked workspace, or a new one; None where none is needed."""
+    if workspace is None:
+        return _empty(like, need, torch.uint8, stream) if need > 0 else None
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes, the call needs {need}")
+    if workspace.data_ptr() % align:
+        raise ValueError(f"workspace must be {align}-byte aligned")
+    return workspace
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of the norm's value from dy [T, H] (bf16): dx [T, H], of h's type, is that of h, and so of x
+    and of the residual (``dh``, of h's type, is added: the gradient that reaches h by another way; dx may be
+    dh itself); dweight [H], of the weight's type. ``workspace``: a uint8 tensor of
+    rms_norm_backward_workspace(T, H) bytes that calls in a row may share. Returns (dx, dweight)."""
+    T, H = _matrix("dy", dy, _BF16).shape
+    _matrix("h", h, _BF16_F32, (T, H))
+    _weight_of(weight, H)
+    _dense("rstd", rstd, torch.float32, (T,))
+    if dh is not None:
+        _matrix("dh", dh, (h.dtype,), (T, H))
+    if dx is None:
+        dx = _empty(h, (T, H), h.dtype, stream)
+    else:
+        _matrix("dx", dx, (h.dtype,), (T, H))
+    if dweight is None:
+        dweight = _empty(weight, (H,), weight.dtype, stream)
+    else:
+        _dense("dweight", dweight, weight.dtype, (H,))
+    workspace = _workspace(dy, workspace, rms_norm_backward_workspace(T, H), stream, 16)
+    dev = _current(dy, h, weight, rstd, dh, dx, dweight, workspace)
+    if dev is None:
+        _gpu(dy=dy, h=h, weight=weight, rstd=rstd, dh=dh, dx=dx, dweight=dweight, workspace=workspace)
+    _call("rms_norm_backward", _ptr(dy), _stride(dy, T), _ptr(h), _TYPE_IDS[h.dtype], _stride(h, T), _ptr(weight), _TYPE_IDS[weight.dtype],
+          _ptr(rstd), _ptr(dh), 0 if dh is None else _stride(dh, T), T, H, _ptr(dx), _stride(dx, T), _ptr(dweight), _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _stream(stream, dev))
+    return dx, dweight
+
+
+def _gate_up(gu):
+    T, C = _matrix("gu", gu, _BF16).shape
+    if C % 2:
+        raise ValueError(f"gu must hold gate and up halves, got {C} columns")
+    return T, C // 2
+
+
+def swiglu_quantize(gu, fmt="e4m3fn", q=None, s=None, y=None, want_y=False, stream=None):
+    """silu(gate) * up of gu [T, 2 F] (bf16, gate columns first) as 8-bit codes; ``fmt`` and the outputs as in
+    rms_norm_quantize. Returns (q, s, y)."""
+    kind = _code_kind(fmt)
+    T, F = _gate_up(gu)
+    q, s, y = _row_outputs(gu, T, F, kind, q, s, y, want_y, stream)
+    dev = _current(gu, q, s, y)
+    if dev is None:
+        _gpu(gu=gu, q=q, s=s, y=y)
+    _call("swiglu_quantize", _ptr(gu), T, F, _stride(gu, T), _CODE_KINDS[kind], _ptr(q), 0 if q is None else _stride(q, T), _ptr(s), _ptr(y),
+          0 if y is None else _stride(y, T), _stream(stream, dev))
+    return q, s, y
+
+
+def swiglu_quantize_lhs_and_rhs(gu, q=None, a_s=None, qT=None, s=None, stream=None, fmt="e4m3fn"):
+    """silu(gate) * up of gu [T, 2 F] in both groupings: (q [T, F], a_s (Fb, T), qT [F, T], s (Tb, F)), as
+    quantize_lhs_and_rhs of its fp32 values."""
+    kind = fp8_format(fmt)
+    T, F = _gate_up(gu)
+    q, a_s, qT, s = _tile_outputs(gu, T, F, q, a_s, qT, s, stream, kind)
+    dev = _current(gu, q, a_s, qT, s)
+    if dev is None:
+        _gpu(gu=gu, q=q, a_s=a_s, qT=qT, s=s)
+    _call("swiglu_quantize_lhs_and_rhs", _ptr(gu), T, F, _stride(gu, T), _CODE_KINDS[kind], _ptr(q), _stride(q, T), _ptr(a_s), _ptr(qT),
+          _stride(qT, F), _ptr(s), _stream(stream, dev))
+    return q, a_s, qT, s
+
+
+def swiglu_backward(dy, gu, dgu=None, stream=None):
+    """The gradient [T, 2 F] (bf16) of silu(gate) * up with respect to gu, from dy [T, F] (bf16)."""
+    T, F = _gate_up(gu)
+    _matrix("dy", dy, _BF16, (T, F))
+    if dgu is None:
+        dgu = _empty(gu, (T, 2 * F), torch.bfloat16, stream)
+    else:
+        _matrix("dgu", dgu, _BF16, (T, 2 * F))
+    dev = _current(dy, gu, dgu)
+    if dev is None:
+        _gpu(dy=dy, gu=gu, dgu=dgu)
+    _call("swiglu_backward", _ptr(dy), _stride(dy, T), _ptr(gu), _stride(gu, T), T, F, _ptr(dgu), _stride(dgu, T), _stream(stream, dev))
+    return dgu
+
+
+def swiglu_backward_quantize(dy, gu, q=None, a_s=None, qT=None, s=None, stream=None, fmt="e4m3fn"):
+    """swiglu_backward in both groupings: (q [T, 2 F], a_s (2Fb, T), qT [2 F, T], s (Tb, 2 F)), as
+    quantize_lhs_and_rhs of its fp32 values."""
+    kind = fp8_format(fmt)
+    T, F = _gate_up(gu)
+    _matrix("dy", dy, _BF16, (T, F))
+    q, a_s, qT, s = _tile_outputs(gu, T, 2 * F, q, a_s, qT, s, stream, kind)
+    dev = _current(dy, gu, q, a_s, qT, s)
+    if dev is None:
+        _gpu(dy=dy, gu=gu, q=q, a_s=a_s, qT=qT, s=s)
+    _call("swiglu_backward_quantize", _ptr(dy), _stride(dy, T), _ptr(gu), _stride(gu, T), T, F, _CODE_KINDS[kind], _ptr(q), _stride(q, T),
+          _ptr(a_s), _ptr(qT), _stride(qT, 2 * F), _ptr(s), _stream(stream, dev))
+    return q, a_s, qT, s
+
+
+# ---------------------------------------------------------------- int8
+def quantize_rows_i8(x, q=None, s=None, stream=None):
+    """int8 codes of x [M, K] (bf16) with one scale a row: a token's activations, or the output channels of a
+    weight [out, in]. Returns (q [M, K] int8, s (M,) fp32)."""
+    M, K = _matrix("x", x, _BF16).shape
+    q, s, _ = _row_outputs(x, M, K, "int8", q, s, None, False, stream)
+    dev = _current(x, q, s)
+    if dev is None:
+        _gpu(x=x, q=q, s=s)
+    _call("quantize_rows_i8", _ptr(x), M, K, _stride(x, M), _ptr(q), _stride(q, M), _ptr(s), _stream(stream, dev))
+    return q, s
+
+
+def gemm_i8(a, a_s, b, b_s, c=None, K=None, stream=None):
+    """C = (A B^T) * a_s * b_s: A [M, K] int8 with a scale a row a_s (M,), B [N, K] int8 with a scale an output
+    column b_s (N,); the sum exact in int32. Returns c [M, N] bf16. Rows are 16-byte aligned."""
+    _matrix("a", a, (torch.int8,))
+    _matrix("b", b, (torch.int8,))
+    M, N = a.shape[0], b.shape[0]
+    most = min(a.shape[1], b.shape[1])
+    K = a.shape[1] if K is None else int(K)
+    if not 0 <= K <= most:
+        raise ValueError(f"K = {K} must lie in [0, min(a.shape[1], b.shape[1])] = [0, {most}]")
+    if K > MAX_I8_K:
+        raise ValueError(f"K = {K} products may pass int32, at most {MAX_I8_K} are summed")
+    _dense("a_s", a_s, torch.float32, (M,))
+    _dense("b_s", b_s, torch.float32, (N,))
+    if c is None:
+        c = _empty(a, (M, N), torch.bfloat16, stream)
+    else:
+        _matrix("c", c, (torch.bfloat16,), (M, N))
+    dev = _current(a, a_s, b, b_s, c)
+    if dev is None:
+        _gpu(a=a, a_s=a_s, b=b, b_s=b_s, c=c)
+    _call("gemm_i8", _ptr(a), _i8_stride(a, M), _ptr(a_s), _ptr(b), _i8_stride(b, N), _ptr(b_s), _ptr(c), _stride(c, M), M, N, K,
+          _stream(stream, dev))
+    return c
+
+
+def _i8_stride(t, rows):
+    """Row stride of an operand; a single row's counts as the next multiple of 16."""
+    return t.stride(0) if rows > 1 else cdiv(t.shape[1], 16) * 16
+
+
+# ---------------------------------------------------------------- gradients of many tensors
+def _flat_stride(t):
+    """Whether the tensor's values lie side by side, in whatever order of the dimensions."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size != 1:
+            if stride != want:
+                return False
+            want *= size
+    return True
+
+
+def _grad_list(name, tensors):
+    tensors = list(tensors)
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}] must be a torch.Tensor, got {type(t).__name__}")
+        if t.dtype not in _BF16_F32:
+            raise TypeError(f"{name}[{i}] has dtype {t.dtype}, expected bfloat16 or float32")
+        if t.layout != torch.strided or not _flat_stride(t):
+            raise ValueError(f"{name}[{i}] must be dense (shape {tuple(t.shape)})")
+    return tensors
+
+
+def _grad_arrays(tensors):
+    n = len(tensors)
+    return ((_vp * n)(*[t.data_ptr() for t in tensors]), (_i64 * n)(*[t.numel() for t in tensors]),
+            (_i32 * n)(*[_TYPE_IDS[t.dtype] for t in tensors]))
+
+
+def _grad_call(grads, norm, workspace, stream, outs=()):
+    """What both calls need: device, arrays, norm, workspace."""
+    first = grads[0] if grads else norm
+    if first is None:
+        raise ValueError("no gradients: give norm, or at least one tensor")
+    dev = _current(first, norm, *grads, *outs)
+    if dev is None:
+        _gpu(norm=norm, **{f"grads[{i}]": t for i, t in enumerate(grads)}, **{f"out[{i}]": t for i, t in enumerate(outs)})
+    addresses, sizes, types = _grad_arrays(grads)
+    if norm is None:
+        norm = _empty(first, (1,), torch.float32, stream)
+    else:
+        _dense("norm", norm, torch.float32, (1,))
+    workspace = _workspace(first, workspace, lib().grad_workspace(sizes, len(grads)), stream, 8)
+    if workspace is not None and workspace.get_device() != dev:
+        _gpu(workspace=workspace)
+    return dev, addresses, sizes, types, norm, workspace
+
+
+def grad_workspace(grads):
+    """Bytes of device memory grad_norm and clip_grads need for these tensors."""
+    sizes = [t.numel() for t in grads]
+    return lib().grad_workspace((_i64 * len(sizes))(*sizes), len(sizes))
+
+
+def grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The 2-norm of all values of the tensors (bf16 or fp32, dense, on one GPU): returns norm (1,) fp32 on the
+    device; the host is not synchronised. ``workspace``: a uint8 tensor of grad_workspace(grads) bytes that
+    calls in a row may share."""
+    grads = _grad_list("grads", grads)
+    dev, addresses, sizes, types, norm, workspace = _grad_call(grads, norm, workspace, stream)
+    _call("grad_norm", addresses, sizes, types, len(grads), _ptr(norm), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+          _stream(stream, dev))
+    return norm
+
+
+def clip_grads(grads, max_norm, out=None, norm=None, eps=1e-6, workspace=None, stream=None):
+    """Scales the gradients by min(1, max_norm / (norm + eps)), norm being grad_norm(grads); in place, or into
+    the tensors of ``out`` (of the gradients' shapes and layouts, bf16 or fp32). Where the norm is not finite the
+    gradients are left (copied) as they are. Returns norm (1,) fp32 on the device; the host is not synchronised."""
+    grads = _grad_list("grads", grads)
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm must be >= 0, got {max_norm}")
+    if not (eps >= 0 and math.isfinite(eps)):
+        raise ValueError(f"eps must be >= 0 and finite, got {eps}")
+    outs = grads
+    if out is not None:
+        outs = _grad_list("out", out)
+        if len(outs) != len(grads):
+            raise ValueError(f"out holds {len(outs)} tensors, grads {len(grads)}")
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if o.shape != g.shape or any(n > 1 and a != b for n, a, b in zip(g.shape, g.stride(), o.stride())):
+                raise ValueError(f"out[{i}] has shape {tuple(o.shape)} and strides {o.stride()}, expected {tuple(g.shape)} and {g.stride()}")
+    dev, addresses, sizes, types, norm, workspace = _grad_call(grads, norm, workspace, stream, () if out is None else outs)
+    to, _, out_types = (addresses, sizes, types) if out is None else _grad_arrays(outs)
+    _call("clip_grads", addresses, to, sizes, types, out_types, len(grads), max_norm, eps, _ptr(norm), _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _stream(stream, dev))
+    return norm

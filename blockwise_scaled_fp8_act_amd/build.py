@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG, "libbsfp8.so")
 # named for this interpreter, whose full C interface it uses: another one does not load it
 CALLS_PATH = os.path.join(PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
-SOURCES = ["capi.cpp", "quantize.hip", "gemm.hip", "moe.hip", "gemm_routed.hip"]
+SOURCES = ["capi.cpp", "quantize.hip", "gemm.hip", "moe.hip", "gemm_routed.hip", "norm.hip", "swiglu.hip", "quantize_i8.hip", "gemm_i8.hip",
+           "grads.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CC = os.environ.get("CC", "gcc")

@@ -4,11 +4,14 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "launch.hpp"
 
@@ -345,6 +348,122 @@ int validate_route(int dtype, int64_t T, int64_t E, int64_t ld, int score, int64
     return BSFP8_OK;
 }
 
+// Limits of the operators that take rows of tokens: a workgroup of four waves a row.
+constexpr int64_t kMaxRows = (int64_t{1} << 24) - 16;
+constexpr int64_t kMaxI8K = 131071;  // 2^14 K < 2^31
+
+bool dtype_ok(int d) { return d == BSFP8_BF16 || d == BSFP8_F32; }
+bool fp8_codes(int codes) { return codes == BSFP8_CODES_E4M3FN || codes == BSFP8_CODES_E4M3FNUZ; }
+
+// Outputs of an operator that writes rows as codes.
+int validate_codes(int64_t T, int64_t H, int codes, const void* q, int64_t ldq, const float* s, const void* y, int64_t ldy) {
+    if (T < 0 || H < 0 || T > kMaxRows || H > 0x7FFFFFFF) return BSFP8_EINVAL;
+    if (codes != BSFP8_CODES_NONE && codes != BSFP8_CODES_INT8 && !fp8_codes(codes)) return BSFP8_EINVAL;
+    if (T == 0 || H == 0) return BSFP8_OK;
+    if ((codes == BSFP8_CODES_NONE) != (q == nullptr) || (q == nullptr) != (s == nullptr)) return BSFP8_EINVAL;
+    if (q == nullptr && y == nullptr) return BSFP8_EINVAL;
+    if ((q != nullptr && ldq < H) || (y != nullptr && ldy < H)) return BSFP8_EINVAL;
+    return BSFP8_OK;
+}
+
+// Outputs in both groupings of a [T, C] tensor.
+int validate_tiles(int64_t T, int64_t C, int codes, const void* q, int64_t ldq, const float* a_s, const void* qT, int64_t ldqT,
+                   const float* s) {
+    if (T < 0 || C < 0 || C > 0x7FFFFFFF || cdiv(T, kGroupEdge) > kMaxGridY || !fp8_codes(codes)) return BSFP8_EINVAL;
+    if (T == 0 || C == 0) return BSFP8_OK;
+    if (q == nullptr || a_s == nullptr || qT == nullptr || s == nullptr || ldq < C || ldqT < T) return BSFP8_EINVAL;
+    return BSFP8_OK;
+}
+
+// The tensors of grad_norm and clip_grads; the number of their launches' workgroups, or -1.
+int64_t grad_partials(const int64_t* sizes, int64_t count) {
+    if (count < 0 || count > 0xFFFFFF || (count > 0 && sizes == nullptr)) return -1;
+    int64_t partials = 0, units = 0, in_launch = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] < 0 || sizes[i] > (int64_t{1} << 48)) return -1;
+        if (sizes[i] == 0) continue;
+        units += cdiv(sizes[i], bsfp8::sched::kGradUnit);
+        if (++in_launch == bsfp8::kGradTensors) {
+            partials += bsfp8::sched::grad_blocks(units);
+            units = in_launch = 0;
+        }
+    }
+    return partials + (in_launch > 0 ? bsfp8::sched::grad_blocks(units) : 0);
+}
+
+// No output shares memory with another tensor of the call, but with its own gradient as a whole.
+bool outputs_apart(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, const int* out_dtypes,
+                   int64_t count) {
+    struct Range {
+        uintptr_t from, to;
+        int64_t i;
+    };
+    const auto bytes = [&](int64_t i, int d) { return static_cast<uintptr_t>(sizes[i]) * (d == BSFP8_F32 ? 4 : 2); };
+    std::vector<Range> out;
+    out.reserve(static_cast<size_t>(count));
+    for (int64_t i = 0; i < count; ++i)
+        if (sizes[i] > 0) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(outs[i]);
+            out.push_back({p, p + bytes(i, out_dtypes[i]), i});
+        }
+    const auto before = [](const Range& a, const Range& b) { return a.from < b.from; };
+    if (!std::is_sorted(out.begin(), out.end(), before)) std::sort(out.begin(), out.end(), before);
+    for (size_t k = 1; k < out.size(); ++k)
+        if (out[k].from < out[k - 1].to) return false;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(grads[i]), to = from + bytes(i, dtypes[i]);
+        if (grads[i] == outs[i] && dtypes[i] == out_dtypes[i]) continue;  // the outputs are apart, so this one meets no other
+        // the outputs end in order, too: the first that ends behind `from`
+        const auto at = std::upper_bound(out.begin(), out.end(), from, [](uintptr_t v, const Range& r) { return v < r.to; });
+        if (at != out.end() && at->from < to) return false;
+    }
+    return true;
+}
+
+// Calls f(table, workgroups before) for each launch of the tensors that hold values.
+template <typename F>
+hipError_t for_grad_tables(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes,
+                           const int* out_dtypes, int64_t count, F f) {
+    bsfp8::GradTable t;
+    t.count = 0;
+    t.first[0] = 0;
+    int64_t before = 0;
+    const auto flush = [&]() {
+        if (t.count == 0) return hipSuccess;
+        const hipError_t e = f(t, before);
+        before += bsfp8::sched::grad_blocks(t.first[t.count]);
+        t.count = 0;
+        return e;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const int k = t.count++;
+        t.in[k] = grads[i];
+        t.out[k] = outs != nullptr ? outs[i] : nullptr;
+        t.n[k] = sizes[i];
+        t.first[k + 1] = t.first[k] + cdiv(sizes[i], bsfp8::sched::kGradUnit);
+        t.in_f32[k] = dtypes[i] == BSFP8_F32;
+        t.out_f32[k] = outs != nullptr && out_dtypes[i] == BSFP8_F32;
+        if (t.count == bsfp8::kGradTensors)
+            if (const hipError_t e = flush()) return e;
+    }
+    return flush();
+}
+
+int validate_grads(const void* const* grads, const int64_t* sizes, const int* dtypes, int64_t count, const float* norm,
+                   const void* workspace, int64_t workspace_bytes) {
+    const int64_t partials = grad_partials(sizes, count);
+    if (partials < 0 || norm == nullptr || (count > 0 && (grads == nullptr || dtypes == nullptr))) return BSFP8_EINVAL;
+    if (partials > 0 && (workspace == nullptr || workspace_bytes < 8 * partials)) return BSFP8_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 7) != 0) return BSFP8_EINVAL;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!dtype_ok(dtypes[i]) || (sizes[i] > 0 && grads[i] == nullptr)) return BSFP8_EINVAL;
+        if (sizes[i] > 0 && reinterpret_cast<uintptr_t>(grads[i]) % (dtypes[i] == BSFP8_F32 ? 4 : 2) != 0) return BSFP8_EINVAL;
+    }
+    return BSFP8_OK;
+}
+
 int encode_impl(const float* x, void* q, int64_t n, bool fnuz, void* stream) {
     if (n < 0) return BSFP8_EINVAL;
     if (n == 0) return BSFP8_OK;
@@ -625,6 +744,174 @@ int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int6
                                  static_cast<const uint8_t*>(b), ldb, b_stride, b_s, bs_stride, bs_stride_nb,
                                  bs_stride_kb, offsets, E, static_cast<uint16_t*>(c), ldc, M, N, K, 0, 0};
     return finish(bsfp8::launch_gemm_routed(args, swiglu != 0, static_cast<hipStream_t>(stream)));
+}
+
+int rms_norm_quantize(const void* x, int64_t T, int64_t H, int64_t ldx, const void* residual, int res_dtype, int64_t ldr,
+                      const void* weight, int w_dtype, float eps, void* h, int64_t ldh, float* rstd, int codes, void* q,
+                      int64_t ldq, float* s, void* y, int64_t ldy, void* stream) {
+    if (int rc = validate_codes(T, H, codes, q, ldq, s, y, ldy)) return rc;
+    if (!dtype_ok(res_dtype) || !dtype_ok(w_dtype) || !(eps > 0.0f) || !std::isfinite(eps)) return BSFP8_EINVAL;
+    if (T == 0 || H == 0) return BSFP8_OK;
+    if (x == nullptr || weight == nullptr || ldx < H || (residual == nullptr) != (h == nullptr)) return BSFP8_EINVAL;
+    if (residual != nullptr && (ldr < H || ldh < H)) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::NormArgs a{static_cast<const uint16_t*>(x), ldx, residual, ldr, res_dtype == BSFP8_F32, weight,
+                            w_dtype == BSFP8_F32, eps, h, ldh, rstd, T, H, 0};
+    const bsfp8::RowCodes out{codes, static_cast<uint8_t*>(q), ldq, s, static_cast<uint16_t*>(y), ldy};
+    return finish(bsfp8::launch_rms_norm(a, out, static_cast<hipStream_t>(stream)));
+}
+
+int rms_norm_quantize_rhs(const void* h, int h_dtype, int64_t T, int64_t H, int64_t ldh, const void* weight, int w_dtype,
+                          const float* rstd, int codes, void* qT, int64_t ldqT, float* s, void* stream) {
+    if (T < 0 || H < 0 || H > 0x7FFFFFFF || cdiv(T, kGroupEdge) > kMaxGridY || !fp8_codes(codes)) return BSFP8_EINVAL;
+    if (!dtype_ok(h_dtype) || !dtype_ok(w_dtype)) return BSFP8_EINVAL;
+    if (T == 0 || H == 0) return BSFP8_OK;
+    if (h == nullptr || weight == nullptr || rstd == nullptr || qT == nullptr || s == nullptr || ldh < H || ldqT < T)
+        return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_rms_norm_rhs(h, h_dtype == BSFP8_F32, ldh, weight, w_dtype == BSFP8_F32, rstd, T, H,
+                                             static_cast<uint8_t*>(qT), ldqT, s, codes == BSFP8_CODES_E4M3FNUZ,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int64_t rms_norm_backward_workspace(int64_t T, int64_t H) {
+    if (T < 0 || H < 0 || T > kMaxRows || H > 0x7FFFFFFF) return -1;
+    return bsfp8::sched::norm_backward_blocks(T) * H * static_cast<int64_t>(sizeof(float));
+}
+
+int rms_norm_backward(const void* dy, int64_t lddy, const void* h, int h_dtype, int64_t ldh, const void* weight, int w_dtype,
+                      const float* rstd, const void* dh, int64_t lddh, int64_t T, int64_t H, void* dx, int64_t lddx,
+                      void* dweight, void* workspace, int64_t workspace_bytes, void* stream) {
+    const int64_t need = rms_norm_backward_workspace(T, H);
+    if (need < 0 || !dtype_ok(h_dtype) || !dtype_ok(w_dtype)) return BSFP8_EINVAL;
+    if (H == 0) return BSFP8_OK;
+    if (weight == nullptr || dweight == nullptr) return BSFP8_EINVAL;
+    if (T > 0) {
+        if (dy == nullptr || h == nullptr || rstd == nullptr || dx == nullptr) return BSFP8_EINVAL;
+        if (lddy < H || ldh < H || lddx < H || (dh != nullptr && lddh < H)) return BSFP8_EINVAL;
+        if (workspace == nullptr || workspace_bytes < need) return BSFP8_EINVAL;
+    }
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15) != 0) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::NormBackwardArgs a{static_cast<const uint16_t*>(dy), lddy, h, ldh, weight, w_dtype == BSFP8_F32, rstd, dh,
+                                    lddh, dx, lddx, dweight, static_cast<float*>(workspace), T, H};
+    return finish(bsfp8::launch_rms_norm_backward(a, h_dtype == BSFP8_F32, static_cast<hipStream_t>(stream)));
+}
+
+int swiglu_quantize(const void* gu, int64_t T, int64_t F, int64_t ldgu, int codes, void* q, int64_t ldq, float* s, void* y,
+                    int64_t ldy, void* stream) {
+    if (int rc = validate_codes(T, F, codes, q, ldq, s, y, ldy)) return rc;
+    if (T == 0 || F == 0) return BSFP8_OK;
+    if (gu == nullptr || ldgu < 2 * F) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::RowCodes out{codes, static_cast<uint8_t*>(q), ldq, s, static_cast<uint16_t*>(y), ldy};
+    return finish(bsfp8::launch_swiglu(static_cast<const uint16_t*>(gu), ldgu, T, F, out, static_cast<hipStream_t>(stream)));
+}
+
+int swiglu_quantize_lhs_and_rhs(const void* gu, int64_t T, int64_t F, int64_t ldgu, int codes, void* q, int64_t ldq, float* a_s,
+                                void* qT, int64_t ldqT, float* s, void* stream) {
+    if (int rc = validate_tiles(T, F, codes, q, ldq, a_s, qT, ldqT, s)) return rc;
+    if (T == 0 || F == 0) return BSFP8_OK;
+    if (gu == nullptr || ldgu < 2 * F) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::TileCodes out{static_cast<uint8_t*>(q), ldq, a_s, static_cast<uint8_t*>(qT), ldqT, s};
+    return finish(bsfp8::launch_swiglu_dual(static_cast<const uint16_t*>(gu), ldgu, T, F, out, codes == BSFP8_CODES_E4M3FNUZ,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int swiglu_backward(const void* dy, int64_t lddy, const void* gu, int64_t ldgu, int64_t T, int64_t F, void* dgu, int64_t lddgu,
+                    void* stream) {
+    if (T < 0 || F < 0 || F > 0x3FFFFFFF) return BSFP8_EINVAL;
+    if (T == 0 || F == 0) return BSFP8_OK;
+    if (dy == nullptr || gu == nullptr || dgu == nullptr || lddy < F || ldgu < 2 * F || lddgu < 2 * F) return BSFP8_EINVAL;
+    if (cdiv(F, 512) > kMaxWaves / T) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_swiglu_backward(static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(gu), ldgu, T,
+                                                F, static_cast<uint16_t*>(dgu), lddgu, static_cast<hipStream_t>(stream)));
+}
+
+int swiglu_backward_quantize(const void* dy, int64_t lddy, const void* gu, int64_t ldgu, int64_t T, int64_t F, int codes, void* q,
+                             int64_t ldq, float* a_s, void* qT, int64_t ldqT, float* s, void* stream) {
+    if (F < 0 || F > 0x3FFFFFFF) return BSFP8_EINVAL;
+    if (int rc = validate_tiles(T, 2 * F, codes, q, ldq, a_s, qT, ldqT, s)) return rc;
+    if (T == 0 || F == 0) return BSFP8_OK;
+    if (dy == nullptr || gu == nullptr || lddy < F || ldgu < 2 * F) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    const bsfp8::TileCodes out{static_cast<uint8_t*>(q), ldq, a_s, static_cast<uint8_t*>(qT), ldqT, s};
+    return finish(bsfp8::launch_swiglu_backward_dual(static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(gu), ldgu, T,
+                                                     F, out, codes == BSFP8_CODES_E4M3FNUZ, static_cast<hipStream_t>(stream)));
+}
+
+int quantize_rows_i8(const void* x, int64_t M, int64_t K, int64_t ldx, void* q, int64_t ldq, float* s, void* stream) {
+    if (M < 0 || K < 0 || M > kMaxRows || K > 0x7FFFFFFF) return BSFP8_EINVAL;
+    if (M == 0 || K == 0) return BSFP8_OK;
+    if (x == nullptr || q == nullptr || s == nullptr || ldx < K || ldq < K) return BSFP8_EINVAL;
+    if (int rc = check_device()) return rc;
+    return finish(bsfp8::launch_quantize_rows_i8(static_cast<const uint16_t*>(x), ldx, M, K, static_cast<uint8_t*>(q), ldq, s,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+int gemm_i8(const void* a, int64_t lda, const float* a_s, const void* b, int64_t ldb, const float* b_s, void* c, int64_t ldc,
+            int64_t M, int64_t N, int64_t K, void* stream) {
+    if (M < 0 || N < 0 || K < 0 || K > kMaxI8K) return BSFP8_EINVAL;
+    if (M == 0 || N == 0) return BSFP8_OK;
+    if (c == nullptr || ldc < N || cdiv(M, 64) > ((int64_t{1} << 22) - 1) / cdiv(N, 64)) return BSFP8_EINVAL;
+    if (K > 0) {
+        if (a == nullptr || a_s == nullptr || b == nullptr || b_s == nullptr || lda < K || ldb < K) return BSFP8_EINVAL;
+        if (lda > kMaxOperandLd || ldb > kMaxOperandLd) return BSFP8_EINVAL;
+        if (!aligned16(a) || !aligned16(b) || lda % 16 != 0 || ldb % 16 != 0) return BSFP8_EALIGN;
+    }
+    if (int rc = check_device()) return rc;
+    const bsfp8::I8Args args{static_cast<const uint8_t*>(a), lda, a_s, static_cast<const uint8_t*>(b), ldb, b_s,
+                             static_cast<uint16_t*>(c), ldc, M, N, K};
+    return finish(bsfp8::launch_gemm_i8(args, bsfp8::device_cus(), static_cast<hipStream_t>(stream)));
+}
+
+int64_t grad_workspace(const int64_t* sizes, int64_t count) {
+    const int64_t partials = grad_partials(sizes, count);
+    return partials < 0 ? -1 : 8 * partials;
+}
+
+int grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int64_t count, float* norm, void* workspace,
+              int64_t workspace_bytes, void* stream) {
+    if (int rc = validate_grads(grads, sizes, dtypes, count, norm, workspace, workspace_bytes)) return rc;
+    if (int rc = check_device()) return rc;
+    double* partial = static_cast<double*>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const hipError_t e = for_grad_tables(grads, nullptr, sizes, dtypes, nullptr, count, [&](const bsfp8::GradTable& t, int64_t before) {
+        return bsfp8::launch_grad_squares(t, partial + before, st);
+    });
+    if (e != hipSuccess) return BSFP8_EHIP;
+    return finish(bsfp8::launch_grad_norm(partial, grad_partials(sizes, count), norm, st));
+}
+
+int clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, const int* out_dtypes,
+               int64_t count, float max_norm, float eps, float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (int rc = validate_grads(grads, sizes, dtypes, count, norm, workspace, workspace_bytes)) return rc;
+    if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || !std::isfinite(eps)) return BSFP8_EINVAL;
+    if (count > 0 && (outs == nullptr || out_dtypes == nullptr)) return BSFP8_EINVAL;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!dtype_ok(out_dtypes[i]) || (sizes[i] > 0 && outs[i] == nullptr)) return BSFP8_EINVAL;
+        if (sizes[i] > 0 && reinterpret_cast<uintptr_t>(outs[i]) % (out_dtypes[i] == BSFP8_F32 ? 4 : 2) != 0) return BSFP8_EINVAL;
+    }
+    try {
+        if (!outputs_apart(grads, outs, sizes, dtypes, out_dtypes, count)) return BSFP8_EINVAL;
+    } catch (const std::bad_alloc&) {
+        return BSFP8_EHIP;
+    }
+    if (int rc = check_device()) return rc;
+    double* partial = static_cast<double*>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t partials = grad_partials(sizes, count);
+    if (partials == 0) return finish(bsfp8::launch_grad_norm(partial, 0, norm, st));
+    hipError_t e = for_grad_tables(grads, outs, sizes, dtypes, out_dtypes, count, [&](const bsfp8::GradTable& t, int64_t before) {
+        return bsfp8::launch_grad_squares(t, partial + before, st);
+    });
+    if (e != hipSuccess) return BSFP8_EHIP;
+    // the first launch of the clipped copies writes the norm
+    return finish(for_grad_tables(grads, outs, sizes, dtypes, out_dtypes, count, [&](const bsfp8::GradTable& t, int64_t before) {
+        return bsfp8::launch_grad_clip(t, partial, partials, max_norm, eps, before == 0 ? norm : nullptr, st);
+    }));
 }
 
 }  // extern "C"

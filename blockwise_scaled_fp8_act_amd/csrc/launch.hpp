@@ -116,4 +116,101 @@ struct RoutedArgs {
 };
 hipError_t launch_gemm_routed(RoutedArgs a, bool swiglu, hipStream_t stream);
 
+// Codes that an operator writes its rows in (BSFP8_CODES_*).
+constexpr int kCodesNone = 0, kCodesE4m3Fn = 1, kCodesE4m3Fnuz = 2, kCodesI8 = 3;
+struct RowCodes {
+    int codes;
+    uint8_t* q;  // [T, H], row stride ldq
+    int64_t ldq;
+    float* s;    // e4m3: column-major [T, ceil(H/128)], ld T; int8: [T]
+    uint16_t* y; // nullptr, or the values in bf16, row stride ldy
+    int64_t ldy;
+};
+
+// RMS norm (norm.hip). residual and h: both nullptr, or both set and of one type.
+struct NormArgs {
+    const uint16_t* x;
+    int64_t ldx;
+    const void* residual;
+    int64_t ldr;
+    bool res_f32;
+    const void* weight;
+    bool w_f32;
+    float eps;
+    void* h;
+    int64_t ldh;
+    float* rstd;  // nullptr: not written
+    int64_t T, H;
+    int64_t per_xcd;  // set by the launcher
+};
+hipError_t launch_rms_norm(NormArgs a, const RowCodes& out, hipStream_t stream);
+hipError_t launch_rms_norm_rhs(const void* h, bool h_f32, int64_t ldh, const void* weight, bool w_f32, const float* rstd, int64_t T,
+                               int64_t H, uint8_t* qT, int64_t ldqT, float* s, bool fnuz, hipStream_t stream);
+struct NormBackwardArgs {
+    const uint16_t* dy;
+    int64_t lddy;
+    const void* h;
+    int64_t ldh;
+    const void* weight;
+    bool w_f32;
+    const float* rstd;
+    const void* dh;  // nullptr, or of h's type
+    int64_t lddh;
+    void* dx;  // of h's type
+    int64_t lddx;
+    void* dweight;  // of the weight's type
+    float* partial; // sched::norm_backward_blocks(T) rows of H sums
+    int64_t T, H;
+};
+hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, bool h_f32, hipStream_t stream);
+
+// SwiGLU (swiglu.hip): gu [T, 2 F], gate then up.
+hipError_t launch_swiglu(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, const RowCodes& out, hipStream_t stream);
+struct TileCodes {
+    uint8_t* q;
+    int64_t ldq;
+    float* a_s;
+    uint8_t* qT;
+    int64_t ldqT;
+    float* s;
+};
+hipError_t launch_swiglu_dual(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, const TileCodes& out, bool fnuz,
+                              hipStream_t stream);
+hipError_t launch_swiglu_backward(const uint16_t* dy, int64_t lddy, const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F,
+                                  uint16_t* dgu, int64_t lddgu, hipStream_t stream);
+hipError_t launch_swiglu_backward_dual(const uint16_t* dy, int64_t lddy, const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F,
+                                       const TileCodes& out, bool fnuz, hipStream_t stream);
+
+// int8 rows (quantize_i8.hip) and products (gemm_i8.hip).
+hipError_t launch_quantize_rows_i8(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, uint8_t* q, int64_t ldq, float* s,
+                                   hipStream_t stream);
+struct I8Args {
+    const uint8_t* a;
+    int64_t lda;
+    const float* a_s;
+    const uint8_t* b;
+    int64_t ldb;
+    const float* b_s;
+    uint16_t* c;
+    int64_t ldc, M, N, K;
+};
+hipError_t launch_gemm_i8(const I8Args& a, int cus, hipStream_t stream);
+
+// Gradients of many tensors (grads.hip): the tensors of one launch, in units of sched::kGradUnit values.
+constexpr int kGradTensors = 96;
+struct GradTable {
+    const void* in[kGradTensors];
+    void* out[kGradTensors];  // clip only
+    int64_t n[kGradTensors];
+    int64_t first[kGradTensors + 1];  // units before tensor i; the last one: all
+    uint8_t in_f32[kGradTensors], out_f32[kGradTensors];
+    int count;
+};
+static_assert(sizeof(GradTable) <= 3800, "kernel arguments fit 4 KB");
+hipError_t launch_grad_squares(const GradTable& t, double* partial, hipStream_t stream);
+hipError_t launch_grad_norm(const double* partial, int64_t count, float* norm, hipStream_t stream);
+// norm: nullptr where another launch of the call writes it
+hipError_t launch_grad_clip(const GradTable& t, const double* partial, int64_t count, float max_norm, float eps, float* norm,
+                            hipStream_t stream);
+
 }  // namespace bsfp8

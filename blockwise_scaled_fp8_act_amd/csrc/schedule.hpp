@@ -304,5 +304,17 @@ inline bool routed_reads_once(int64_t M, int64_t N, int64_t E, bool swiglu) {
     return cdiv(M, E < M ? E : M) <= 32 && routed_lds_workgroups(M, N, E, swiglu) >= 400;
 }
 
+// Operators that hold a row in registers (norm.hip, swiglu.hip, quantize_i8.hip): rows of up to kRowWaveMax
+// columns take a wave, up to kRowMax a workgroup of four; longer ones are read again for each pass.
+constexpr int64_t kRowWaveMax = 1024, kRowMax = 16384;
+
+// Workgroups of the norm's gradient, each with its own part of the weight's gradient.
+inline int64_t norm_backward_blocks(int64_t T) { return T < 512 ? T : 512; }
+
+// Gradients of many tensors: units of kGradUnit values, dealt in consecutive runs to at most kGradBlocks
+// workgroups of a launch.
+constexpr int64_t kGradUnit = 8192, kGradBlocks = 512;
+inline int64_t grad_blocks(int64_t units) { return units < kGradBlocks ? units : kGradBlocks; }
+
 }  // namespace sched
 }  // namespace bsfp8

@@ -1,0 +1,98 @@
+// Device helper of the operators that write their values in both groupings of a training step: the codes
+// of a tile of 128 rows and 128 columns held in registers, row-wise in 1x128 groups and, transposed,
+// column-wise in 128x1 groups. A tile holds exactly one group of every row and of every column.
+#pragma once
+
+#include "row_codes.hpp"
+
+namespace bsfp8 {
+
+constexpr int kTileThreads = 512;
+constexpr int kTileRows = 4;  // a thread's consecutive rows, of 8 columns: 16 lanes make a row of the tile
+
+// The transposed code tile and, before it, the column maxima of the 32 row groups.
+struct TileLds {
+    uint4 tile[kGroup * 8];  // [column][8 chunks of 16 rows], the chunk swizzled by the column's eights
+    uint32_t red[32][kGroup + 1];
+    float mult[kGroup];
+};
+
+// v[i][j]: row r0 + 4 (t / 16) + i, column c0 + 8 (t % 16) + j; zero outside the [T, C] tensor. VEC_Q: code
+// rows 8-byte aligned and C a multiple of 8; VEC_T: rows of qT 16-byte aligned and T a multiple of 16.
+// Every thread of the workgroup calls it; it may be called again at once.
+template <bool FNUZ, bool ROWS, bool VEC_Q, bool VEC_T>
+__device__ __forceinline__ void emit_tile(const TileCodes& out, int64_t r0, int64_t c0, int64_t T, int64_t C, const float (&v)[kTileRows][8],
+                                          TileLds& lds) {
+    const int t = threadIdx.x, cg = t & 15, rg = t >> 4;
+    const int64_t c = c0 + cg * 8;
+    const auto encode = [](float a, float b, float d, float e) { return encode4_in_range<FNUZ>(a, b, d, e); };
+
+    // column maxima of this thread's rows, then of all in LDS
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) am = max(am, abs_bits(v[i][j]));
+        lds.red[rg][cg * 8 + j] = am;
+    }
+    if (ROWS) {
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) {
+            const GroupScale g = fp8_scale<FNUZ>(umax_row16(amax8(v[i])));
+            const int64_t r = r0 + rg * kTileRows + i;
+            if (r >= T) continue;
+            const uint32_t w0 = encode(v[i][0] * g.m, v[i][1] * g.m, v[i][2] * g.m, v[i][3] * g.m);
+            const uint32_t w1 = encode(v[i][4] * g.m, v[i][5] * g.m, v[i][6] * g.m, v[i][7] * g.m);
+            uint8_t* q = out.q + r * out.ldq + c;
+            if (VEC_Q) {
+                if (c < C) *reinterpret_cast<uint2*>(q) = make_uint2(w0, w1);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < C) q[j] = static_cast<uint8_t>((j < 4 ? w0 : w1) >> (8 * (j & 3)));
+            }
+            if (cg == 0) out.a_s[c0 / kGroup * T + r] = g.s;
+        }
+    }
+    __syncthreads();
+    if (t < kGroup) {
+        uint32_t am = 0;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) am = max(am, lds.red[r][t]);
+        const GroupScale g = fp8_scale<FNUZ>(am);
+        lds.mult[t] = g.m;
+        if (c0 + t < C) out.s[r0 / kGroup * C + c0 + t] = g.s;
+    }
+    __syncthreads();
+    // column j of my eight: the codes of my four rows are a dword of the transposed tile
+    uint32_t* tw = reinterpret_cast<uint32_t*>(lds.tile);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int cl = cg * 8 + j;
+        const float m = lds.mult[cl];
+        tw[cl * 32 + (((rg >> 2) ^ (cg & 7)) * 4) + (rg & 3)] = encode(v[0][j] * m, v[1][j] * m, v[2][j] * m, v[3][j] * m);
+    }
+    __syncthreads();
+    // eight consecutive lanes write a column's 128 codes: whole lines of qT
+    const int chunk = t & 7;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int cl = p * 64 + (t >> 3);
+        const int64_t col = c0 + cl, r = r0 + chunk * 16;
+        if (col >= C) continue;
+        const uint4 w = lds.tile[cl * 8 + (chunk ^ ((cl >> 3) & 7))];
+        uint8_t* q = out.qT + col * out.ldqT + r;
+        if (VEC_T) {
+            if (r < T) *reinterpret_cast<uint4*>(q) = w;
+        } else {
+            const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (r + j < T) q[j] = static_cast<uint8_t>(d[j >> 2] >> (8 * (j & 3)));
+        }
+    }
+    // the next call's maxima go into lds.red, which every thread has read before the last barrier; its
+    // multipliers and codes come behind a barrier that follows the reads above
+}
+
+}  // namespace bsfp8

@@ -478,6 +478,119 @@ int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int6
                               const int64_t* offsets, int64_t E,
                               void* c, int64_t ldc, int64_t M, int64_t N, int64_t K, int swiglu, void* stream);
 
+/*
+ * Operators between the 8-bit products of a gated feed-forward layer, the int8 product, and the global
+ * gradient norm. Each of T rows is a token; all are deterministic, allocate nothing and may be captured
+ * into a graph. T at most 2^24 - 16. Codes (the `codes` argument):
+ *   E4M3FN, E4M3FNUZ  q [T, H] fp8 in 1x128 groups, s column-major [T, ceil(H/128)] with ld T, by the
+ *                     quantizers' arithmetic on the fp32 value (which is not rounded to bf16 before);
+ *   INT8              q [T, H] int8, s [T]: one scale a row, s = max(amax, 1e-12f) / 127,
+ *                     q = rint(fl32(v * fl32(127 / max(amax, 1e-12f)))), ties to even;
+ *   NONE              neither (q and s are NULL): the bf16 output alone.
+ * A group (a row, for INT8) that holds a NaN has scale NaN, one that holds an infinity scale infinity; its
+ * codes are of no use then, and a product with such a row is NaN. Any alignment and row length are
+ * accepted; rows 16-byte aligned (codes 8-byte) of a multiple of 8 columns are read in whole pieces.
+ */
+enum { BSFP8_CODES_NONE = 0, BSFP8_CODES_E4M3FN = 1, BSFP8_CODES_E4M3FNUZ = 2, BSFP8_CODES_INT8 = 3 };
+
+/*
+ * rms_norm_quantize: h = x + residual, v = (h * rstd) * weight with rstd = 1 / sqrt(mean(h^2) + eps).
+ *   x         [T, H] bf16, row stride ldx >= H.
+ *   residual  NULL, or [T, H] bf16 or fp32 (res_dtype: BSFP8_BF16, BSFP8_F32), row stride ldr >= H.
+ *   h         with a residual: [T, H] of the residual's type, row stride ldh >= H; the sum rounded to
+ *             that type, and what the norm is taken of. It may be the residual itself (same address and
+ *             stride). NULL without a residual (h is x).
+ *   weight    [H] bf16 or fp32 (w_dtype), contiguous.
+ *   eps       positive and finite.  The sum of squares is in 64 bits; rstd is rounded to fp32.
+ *   rstd      NULL, or [T] fp32: what the gradient takes.
+ *   codes, q, ldq >= H, s   the codes of v.   y  NULL, or [T, H] bf16, row stride ldy >= H: v rounded.
+ */
+int rms_norm_quantize(const void* x, int64_t T, int64_t H, int64_t ldx, const void* residual, int res_dtype, int64_t ldr,
+                      const void* weight, int w_dtype, float eps, void* h, int64_t ldh, float* rstd,
+                      int codes, void* q, int64_t ldq, float* s, void* y, int64_t ldy, void* stream);
+
+/*
+ * rms_norm_quantize_rhs: the normed rows in 128x1 groups, transposed (the operand of the weight gradient),
+ * formed again from h [T, H] (bf16 or fp32, h_dtype), weight and rstd as rms_norm_quantize gave them.
+ *   qT [H, T] fp8, row stride ldqT >= T; s [ceil(T/128), H]: as quantize_rhs of the fp32 values. codes:
+ *   E4M3FN or E4M3FNUZ. ceil(T/128) at most 65535.
+ */
+int rms_norm_quantize_rhs(const void* h, int h_dtype, int64_t T, int64_t H, int64_t ldh, const void* weight, int w_dtype,
+                          const float* rstd, int codes, void* qT, int64_t ldqT, float* s, void* stream);
+
+/*
+ * rms_norm_backward: gradients of the norm's value. With n = h * rstd and g = dy * weight:
+ *   dx [T, H]    = dh + rstd * (g - n * mean(g * n)), of h's type (h_dtype): the gradient of h, and so of x
+ *                  and of the residual.
+ *   dweight [H]  = the sum over the rows of dy * n, of the weight's type, added in fp32 in a fixed order.
+ *   dy [T, H] bf16;  dh NULL (zero) or [T, H] of h's type: the gradient that reaches h by another way.
+ *   dx may be dh itself (same address and stride).
+ *   workspace  device memory of rms_norm_backward_workspace(T, H) bytes (-1: invalid sizes), 16-byte
+ *              aligned, not in use by another call.
+ * T == 0 writes dweight = 0.
+ */
+int64_t rms_norm_backward_workspace(int64_t T, int64_t H);
+int rms_norm_backward(const void* dy, int64_t lddy, const void* h, int h_dtype, int64_t ldh, const void* weight, int w_dtype,
+                      const float* rstd, const void* dh, int64_t lddh, int64_t T, int64_t H, void* dx, int64_t lddx,
+                      void* dweight, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * swiglu_quantize: of gu [T, 2 F] bf16 (gate in the first F columns, up behind), row stride ldgu >= 2 F,
+ * v = silu(gate) * up in fp32; codes, q [T, F], s and y [T, F] as in rms_norm_quantize. Gates below -80
+ * are formed so that a small silu(gate) times a large up keeps its value.
+ * swiglu_quantize_lhs_and_rhs: v in both groupings, as quantize_lhs_and_rhs: q [T, F], a_s column-major
+ * [T, ceil(F/128)], qT [F, T], s [ceil(T/128), F]. codes: E4M3FN or E4M3FNUZ.
+ * swiglu_backward: dgu [T, 2 F] bf16 of dy [T, F] bf16: dgate = dy up sig (1 + gate (1 - sig)),
+ * dup = dy gate sig, with sig = sigmoid(gate).
+ * swiglu_backward_quantize: the same gradient in both groupings, as quantize_lhs_and_rhs of its fp32
+ * values: q [T, 2 F], a_s, qT [2 F, T], s.
+ * ceil(T/128) at most 65535 for the forms with both groupings.
+ */
+int swiglu_quantize(const void* gu, int64_t T, int64_t F, int64_t ldgu, int codes, void* q, int64_t ldq, float* s,
+                    void* y, int64_t ldy, void* stream);
+int swiglu_quantize_lhs_and_rhs(const void* gu, int64_t T, int64_t F, int64_t ldgu, int codes, void* q, int64_t ldq, float* a_s,
+                                void* qT, int64_t ldqT, float* s, void* stream);
+int swiglu_backward(const void* dy, int64_t lddy, const void* gu, int64_t ldgu, int64_t T, int64_t F,
+                    void* dgu, int64_t lddgu, void* stream);
+int swiglu_backward_quantize(const void* dy, int64_t lddy, const void* gu, int64_t ldgu, int64_t T, int64_t F, int codes,
+                             void* q, int64_t ldq, float* a_s, void* qT, int64_t ldqT, float* s, void* stream);
+
+/*
+ * quantize_rows_i8: x [M, K] bf16, row stride ldx >= K, as INT8 codes: q [M, K] int8 (ldq >= K), s [M].
+ * For activations a scale a token, for a weight [out, in] a scale an output channel.
+ */
+int quantize_rows_i8(const void* x, int64_t M, int64_t K, int64_t ldx, void* q, int64_t ldq, float* s, void* stream);
+
+/*
+ * gemm_i8: C[m, n] = (float(sum_k A[m, k] B[n, k]) * a_s[m]) * b_s[n], the sum exact in int32, bf16 out.
+ *   a [M, K] int8, row stride lda;  a_s [M];  b [N, K] int8, row stride ldb;  b_s [N];
+ *   c [M, N] bf16, row stride ldc >= N.  K == 0 writes C = 0.
+ * Alignment (else BSFP8_EALIGN): a and b 16-byte aligned, lda and ldb multiples of 16. Rows may be read
+ * to the 16 bytes that hold their last code. Limits (else BSFP8_EINVAL): K at most 131071 (the sum of
+ * products of -128 fits int32), lda and ldb at most 2^23, fewer than 2^22 tiles of 64 x 64.
+ */
+int gemm_i8(const void* a, int64_t lda, const float* a_s, const void* b, int64_t ldb, const float* b_s,
+            void* c, int64_t ldc, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * grad_norm: norm[0] = sqrt(the sum of the squares of all values of `count` tensors), fp32; squares and sum
+ * in 64 bits, in an order that depends on the sizes alone. No tensor: 0.
+ *   grads, sizes, dtypes   host arrays of `count` device addresses, numbers of values (each tensor dense)
+ *                          and types (BSFP8_BF16, BSFP8_F32), read before the call returns.
+ *   workspace  device memory of grad_workspace(sizes, count) bytes (-1: invalid sizes), 8-byte aligned, not in use
+ *              by another call.
+ * clip_grads: the same norm, and outs[i] = grads[i] * c in fp32, rounded to out_dtypes[i], with
+ * c = min(1, max_norm / (norm + eps)); c = 1 where the norm is not finite, so that the gradients stay as
+ * they are and norm[0] says so. outs[i] may be grads[i] itself (of one type); any other overlap of an
+ * output with a gradient or an output is BSFP8_EINVAL. max_norm >= 0, eps >= 0 and finite.
+ * The host is not synchronised; gradients are read in 16-byte pieces where they are so aligned.
+ */
+int64_t grad_workspace(const int64_t* sizes, int64_t count);
+int grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int64_t count, float* norm,
+              void* workspace, int64_t workspace_bytes, void* stream);
+int clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, const int* out_dtypes,
+               int64_t count, float max_norm, float eps, float* norm, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
