@@ -5,9 +5,17 @@
 //   * operands go from memory straight to LDS by buffer loads whose resources end with the tensor: rows past
 //     an end read as zero. Of a partial last K-block the bytes at and past K are zeroed in A's fragments
 //     alone, which makes every product with them zero.
+// Three kernels; sched::i8_kernel has the rule between them and the tiles' measured costs:
+//   * rows of B straight to the lanes (a few rows of A): bound by reading B once;
+//   * tiles with several K-blocks in LDS: problems whose 256 x 256 tiles would leave compute units idle;
+//   * 256 x 256 tiles, bound by the card's power: the matrix cores are busy for 60% of the cycles, at a clock
+//     that has come down from 2.4 to 1.9 GHz.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "geometry.hpp"
 #include "launch.hpp"
+#include "schedule.hpp"
 
 namespace bsfp8 {
 namespace {
@@ -26,17 +34,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, static_cast<int>(bytes), 0x00020000);
 }
 
-// 16 bytes a lane from the resource to LDS address lds + 16 * lane.
+// 16 bytes a lane from the resource to LDS address lds + 16 * lane; PAST: not kept in the caches.
+template <bool PAST = false>
 __device__ __forceinline__ void dma16(uint32_t lds, __amdgpu_buffer_rsrc_t r, uint32_t voff) {
     uint32_t saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(r)
-        : "memory");
+    if (PAST)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen nt lds\n\ts_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(r)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(r)
+                     : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -53,102 +64,332 @@ __device__ __forceinline__ int64_t tile_bytes(int64_t rows, int64_t ld, int64_t 
     return rows > 0 ? (rows - 1) * ld + ((K + 15) & ~int64_t{15}) : 0;
 }
 
-// BM x BN tiles of C in waves of WM x WN. LDS stage: A rows, then B rows, 128 bytes of K each, the 16-byte
-// chunks of a row swizzled by (row / 2) % 8 (geom::lds_swizzle), so that a fragment's reads hit all banks.
-template <int BM, int BN, int WM, int WN>
-struct Tile {
-    static constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kThreads = 64 * kWaves;
-    static constexpr int kMS = WM / 16, kNS = WN / 16;
-    static constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 8 rows each
-    static constexpr int kStage = (BM + BN) * 8;           // 16-byte units
-    static_assert((BM + BN) % (8 * kWaves) == 0, "whole loads a wave");
-};
+// The offset of a K-block past the last: beyond every resource (their sizes and the lanes' offsets are below
+// 2^31), so its loads write zeros to LDS and the count of loads under way stays the same.
+constexpr uint32_t kPastEnd = 0x80000000u;
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((Tile<BM, BN, WM, WN>::kThreads), 1) void gemm_i8_kernel(I8Args g, int mt, int nt, int c_vec) {
-    using C = Tile<BM, BN, WM, WN>;
-    __shared__ u32x4 smem[2 * C::kStage];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % C::kWavesM, wn = wave / C::kWavesM, l16 = lane & 15, lg = lane >> 4;
+// Zeroes the bytes of a lane's 16 that lie at or past `left`.
+__device__ __forceinline__ void keep_bytes(i32x4& v, int left) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int l = left - 4 * d;
+        v[d] &= l >= 4 ? -1 : l <= 0 ? 0 : (1 << (8 * l)) - 1;
+    }
+}
+
+// The output columns n .. n + 3: their scales, zero past the end or without a sum (K == 0).
+__device__ __forceinline__ void column_scales(const I8Args& g, int64_t n, float (&s)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = g.K > 0 && n + e < g.N ? g.b_s[n + e] : 0.0f;
+}
+__device__ __forceinline__ uint2 scaled4(const i32x4& sum, float as, const float (&bs)[4]) {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (static_cast<float>(sum[e]) * as) * bs[e];
+    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void store4(const I8Args& g, int64_t m, int64_t n, uint2 w, int c_vec) {
+    uint16_t* c = g.c + m * g.ldc + n;
+    if (c_vec && n + 4 <= g.N) {
+        *reinterpret_cast<uint2*>(c) = w;
+    } else {
+        const uint16_t h[4] = {static_cast<uint16_t>(w.x), static_cast<uint16_t>(w.x >> 16), static_cast<uint16_t>(w.y),
+                               static_cast<uint16_t>(w.y >> 16)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < g.N) c[e] = h[e];
+    }
+}
+
+// ---- Tiles of BM x BN in waves of WM x WN, STAGES blocks of KS bytes of K in LDS, loads STAGES - 1 blocks
+// ahead of the products. A row of a stage has its 16-byte chunks swizzled by the row, so that the 16 rows of a
+// fragment's read fall on all banks: chunk c at c ^ swizzle(row). One barrier a block. With few workgroups a
+// block's time is one wait, barrier and chain of reads and products, so blocks are long (256 bytes) for the
+// small tiles; with two workgroups on a CU each hides the other's waits. PAST: B is read past the caches,
+// for weights that are read once and by so many workgroups that HBM is the bound (14336 x 4096, 16 rows: 14.4
+// us through the caches, 12.7 past them).
+template <int BM, int BN, int WM, int WN, int STAGES, int KS, bool PAST>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args g, int mt, int nt, int c_vec) {
+    constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kMS = WM / 16, kNS = WN / 16;
+    constexpr int kChunks = KS / 16, kRows = 64 / kChunks;  // of a row; rows of one load
+    constexpr int kStage = (BM + BN) * kChunks, kLoads = (BM + BN) / kRows / kWaves;
+    static_assert((BM + BN) % (kRows * kWaves) == 0 && BM % kRows == 0, "whole loads a wave");
+    static_assert((STAGES - 2) * kLoads <= 63, "loads under way that can be counted");
+    static_assert(KS == 128 || KS == 256, "swizzles of these");
+    __shared__ u32x4 smem[STAGES * kStage];
+    const auto swizzle = [](int row) { return KS == 128 ? geom::lds_swizzle(row) : row & 15; };
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % kWavesM, wn = wave / kWavesM, l16 = lane & 15, lg = lane >> 4;
     int tm, tn;
     geom::tile_of(blockIdx.x, mt, nt, tm, tn);
     const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a + m0 * g.lda, tile_bytes(min(g.M - m0, int64_t{BM}), g.lda, g.K));
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b + n0 * g.ldb, tile_bytes(min(g.N - n0, int64_t{BN}), g.ldb, g.K));
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)));
-    const int Kb = static_cast<int>((g.K + kGroup - 1) / kGroup);
+    const int Kb = static_cast<int>((g.K + KS - 1) / KS);
 
-    // load p of a wave: rows 8 r .. of A (r < BM / 8) or of B
-    auto issue = [&](int kb, int stage) {
+    // load p of a wave: kRows rows of A, or of B behind them
+    uint32_t off[kLoads];
 #pragma unroll
-        for (int p = 0; p < C::kLoads; ++p) {
-            const int r = wave * C::kLoads + p;
-            const bool is_a = r < BM / 8;
-            const int q = is_a ? r : r - BM / 8;
-            const uint32_t off = static_cast<uint32_t>((8 * q + (lane >> 3)) * (is_a ? g.lda : g.ldb)) + 16 * geom::fast_operand_chunk(q, lane);
-            dma16(lds0 + static_cast<uint32_t>(stage * C::kStage + 64 * r) * 16, is_a ? ra : rb, off + static_cast<uint32_t>(kb * kGroup));
+    for (int p = 0; p < kLoads; ++p) {
+        const int r = wave * kLoads + p;
+        const bool is_a = r < BM / kRows;
+        const int row = kRows * (is_a ? r : r - BM / kRows) + lane / kChunks;
+        off[p] = static_cast<uint32_t>(row * (is_a ? g.lda : g.ldb)) + 16 * ((lane % kChunks) ^ swizzle(row));
+    }
+    const auto issue = [&](int kb, int stage) {
+        const uint32_t k = kb < Kb ? static_cast<uint32_t>(kb * KS) : kPastEnd;
+#pragma unroll
+        for (int p = 0; p < kLoads; ++p) {
+            const int r = wave * kLoads + p;
+            const uint32_t to = lds0 + static_cast<uint32_t>(stage * kStage + 64 * r) * 16;
+            if (r < BM / kRows) dma16(to, ra, off[p] + k);
+            else dma16<PAST>(to, rb, off[p] + k);
         }
     };
 
-    i32x4 acc[C::kMS][C::kNS];
+    i32x4 acc[kMS][kNS];
 #pragma unroll
-    for (int i = 0; i < C::kMS; ++i)
+    for (int i = 0; i < kMS; ++i)
 #pragma unroll
-        for (int j = 0; j < C::kNS; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-
-    const int sw = geom::lds_swizzle(l16);
-    if (Kb > 0) issue(0, 0);
+        for (int j = 0; j < kNS; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    if (Kb > 0) {
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t) issue(t, t);
+    }
+    const int sw = swizzle(l16);
+    int stage = 0;
     for (int kb = 0; kb < Kb; ++kb) {
-        wait_loads<0>();
-        lds_barrier();  // block kb is there, and no wave reads the other stage any more
-        if (kb + 1 < Kb) issue(kb + 1, (kb + 1) & 1);
-        const u32x4* st = smem + (kb & 1) * C::kStage;
-        const int keep = static_cast<int>(min(g.K - static_cast<int64_t>(kb) * kGroup, int64_t{kGroup}));
+        wait_loads<(STAGES - 2) * kLoads>();
+        lds_barrier();  // block kb is there, and no wave reads the stage before it any more
+        issue(kb + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+        const u32x4* st = smem + stage * kStage;
+        i32x4 a[KS / 64][kMS], b[KS / 64][kNS];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < KS / 64; ++h) {
             const int pos = (lg + 4 * h) ^ sw;
-            i32x4 a[C::kMS], b[C::kNS];
 #pragma unroll
-            for (int i = 0; i < C::kMS; ++i) {
-                a[i] = __builtin_bit_cast(i32x4, st[(WM * wm + 16 * i + l16) * 8 + pos]);
-                if (keep < kGroup)
+            for (int i = 0; i < kMS; ++i) a[h][i] = __builtin_bit_cast(i32x4, st[(WM * wm + 16 * i + l16) * kChunks + pos]);
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const int left = keep - 16 * (lg + 4 * h) - 4 * d;
-                        a[i][d] &= left >= 4 ? -1 : left <= 0 ? 0 : (1 << (8 * left)) - 1;
-                    }
-            }
+            for (int j = 0; j < kNS; ++j) b[h][j] = __builtin_bit_cast(i32x4, st[(BM + WN * wn + 16 * j + l16) * kChunks + pos]);
+        }
+        const int64_t keep = g.K - static_cast<int64_t>(kb) * KS;
+        if (keep < KS) {
 #pragma unroll
-            for (int j = 0; j < C::kNS; ++j) b[j] = __builtin_bit_cast(i32x4, st[BM * 8 + (WN * wn + 16 * j + l16) * 8 + pos]);
+            for (int h = 0; h < KS / 64; ++h)
 #pragma unroll
-            for (int i = 0; i < C::kMS; ++i)
+                for (int i = 0; i < kMS; ++i) keep_bytes(a[h][i], static_cast<int>(keep) - 16 * (lg + 4 * h));
+        }
 #pragma unroll
-                for (int j = 0; j < C::kNS; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+        for (int h = 0; h < KS / 64; ++h)
+#pragma unroll
+            for (int i = 0; i < kMS; ++i)
+#pragma unroll
+                for (int j = 0; j < kNS; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[h][j], a[h][i], acc[i][j], 0, 0, 0);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    wait_loads<0>();  // the last blocks' empty loads: none may land after the workgroup's LDS is given away
+
+#pragma unroll
+    for (int j = 0; j < kNS; ++j) {
+        const int64_t n = n0 + WN * wn + 16 * j + 4 * lg;
+        float bs[4];
+        column_scales(g, n, bs);
+#pragma unroll
+        for (int i = 0; i < kMS; ++i) {
+            const int64_t m = m0 + WM * wm + 16 * i + l16;
+            if (m < g.M) store4(g, m, n, scaled4(acc[i][j], g.K > 0 ? g.a_s[m] : 0.0f, bs), c_vec);
         }
     }
+}
 
+// ---- 256 x 256 tiles, eight waves of 64 x 128 (two a SIMD), two stages of 128 bytes of K. A wave reads the
+// fragments of half a block (64 bytes) while it multiplies the half before, and the one barrier a block comes
+// after its first half: by then every wave has read the whole stage, so the loads of the block after next go
+// there, a block's time before they are needed. 16384 x 5120 x 5120 383 us, 2.24 Pop/s (400 us with reads and
+// products of a block in turn); 8192^3 437 us, 2.51. Bound by power: the same loop over zeros takes 402. Not
+// better: 32 x 32 x 32 instructions (488), a ring of five half blocks (473, in 6% fewer cycles at a lower
+// clock), four waves of 128 x 128 (550).
+constexpr int kBig = 256;
+__global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, int c_vec) {
+    constexpr int WM = 64, WN = 128, kMS = WM / 16, kNS = WN / 16, kHalf = kBig * 8, kStage = 2 * kHalf;  // 16-byte units
+    __shared__ u32x4 smem[2 * kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 3, wn = wave >> 2, l16 = lane & 15, lg = lane >> 4;
+    int tm, tn;
+    geom::tile_of(blockIdx.x, mt, nt, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * kBig, n0 = static_cast<int64_t>(tn) * kBig;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a + m0 * g.lda, tile_bytes(min(g.M - m0, int64_t{kBig}), g.lda, g.K));
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b + n0 * g.ldb, tile_bytes(min(g.N - n0, int64_t{kBig}), g.ldb, g.K));
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)));
+    const int Kb = static_cast<int>((g.K + kGroup - 1) / kGroup);
+
+    // a wave loads 32 rows of A and 32 of B a block, 8 a load; the chunk differs between even and odd loads
+    uint32_t offa[2], offb[2];
 #pragma unroll
-    for (int i = 0; i < C::kMS; ++i) {
-        const int64_t m = m0 + WM * wm + 16 * i + l16;
-        if (m >= g.M) continue;
-        const float as = Kb > 0 ? g.a_s[m] : 0.0f;
+    for (int q = 0; q < 2; ++q) {
+        offa[q] = static_cast<uint32_t>((32 * wave + 8 * q + (lane >> 3)) * g.lda) + 16 * geom::fast_operand_chunk(q, lane);
+        offb[q] = static_cast<uint32_t>((32 * wave + 8 * q + (lane >> 3)) * g.ldb) + 16 * geom::fast_operand_chunk(q, lane);
+    }
+    const uint32_t stepa = static_cast<uint32_t>(16 * g.lda), stepb = static_cast<uint32_t>(16 * g.ldb);
+    const auto issue = [&](int kb, int stage) {
+        const uint32_t k = static_cast<uint32_t>(kb * kGroup), to = lds0 + static_cast<uint32_t>(stage * kStage + 256 * wave) * 16;
 #pragma unroll
-        for (int j = 0; j < C::kNS; ++j) {
-            const int64_t n = n0 + WN * wn + 16 * j + 4 * lg;
-            float v[4];
+        for (int p = 0; p < 4; ++p) dma16(to + p * 1024, ra, offa[p & 1] + (p >> 1) * stepa + k);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (static_cast<float>(acc[i][j][e]) * as) * (Kb > 0 && n + e < g.N ? g.b_s[n + e] : 0.0f);
-            const uint32_t w0 = pack_bf16x2(v[0], v[1]), w1 = pack_bf16x2(v[2], v[3]);
-            uint16_t* c = g.c + m * g.ldc + n;
-            if (c_vec && n + 4 <= g.N) {
-                *reinterpret_cast<uint2*>(c) = make_uint2(w0, w1);
-            } else {
-                const uint16_t h[4] = {static_cast<uint16_t>(w0), static_cast<uint16_t>(w0 >> 16), static_cast<uint16_t>(w1),
-                                       static_cast<uint16_t>(w1 >> 16)};
+        for (int p = 0; p < 4; ++p) dma16(to + kHalf * 16 + p * 1024, rb, offb[p & 1] + (p >> 1) * stepb + k);
+    };
+
+    i32x4 acc[kMS][kNS];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < g.N) c[e] = h[e];
+    for (int i = 0; i < kMS; ++i)
+#pragma unroll
+        for (int j = 0; j < kNS; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+    if (Kb > 0) {
+        const int sw = geom::lds_swizzle(l16);
+        const u32x4* la = smem + (WM * wm + l16) * 8;
+        const u32x4* lb = smem + kHalf + (WN * wn + l16) * 8;
+        i32x4 a[2][kMS], b[2][kNS];
+        const auto read = [&](int half, int stage) {
+            const int at = stage * kStage + ((lg + 4 * half) ^ sw);
+#pragma unroll
+            for (int i = 0; i < kMS; ++i) a[half][i] = __builtin_bit_cast(i32x4, la[at + 128 * i]);
+#pragma unroll
+            for (int j = 0; j < kNS; ++j) b[half][j] = __builtin_bit_cast(i32x4, lb[at + 128 * j]);
+        };
+        const auto multiply = [&](int half) {
+#pragma unroll
+            for (int j = 0; j < kNS; ++j)
+#pragma unroll
+                for (int i = 0; i < kMS; ++i) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[half][j], a[half][i], acc[i][j], 0, 0, 0);
+        };
+        // twelve reads spread over the 32 products
+        const auto spread = [&]() {
+#pragma unroll
+            for (int r = 0; r < kMS + kNS; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             }
+            __builtin_amdgcn_sched_group_barrier(0x008, kMS * kNS - kMS - kNS, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        issue(0, 0);
+        wait_loads<0>();
+        lds_barrier();
+        if (Kb > 1) issue(1, 1);
+        read(0, 0);
+        const int left = static_cast<int>(g.K - static_cast<int64_t>(Kb - 1) * kGroup);  // bytes of the last block
+        for (int kb = 0; kb < Kb - 1; ++kb) {
+            const int s = kb & 1;
+            __builtin_amdgcn_sched_barrier(0);
+            read(1, s);
+            multiply(0);
+            spread();
+            wait_loads<0>();
+            lds_barrier();  // block kb + 1 is there, and no wave reads stage s any more
+            if (kb + 2 < Kb) issue(kb + 2, s);
+            __builtin_amdgcn_sched_barrier(0);
+            read(0, s ^ 1);
+            multiply(1);
+            spread();
+        }
+        // the last block, of whose bytes `left` count
+        read(1, (Kb - 1) & 1);
+#pragma unroll
+        for (int i = 0; i < kMS; ++i) {
+            keep_bytes(a[0][i], left - 16 * lg);
+            keep_bytes(a[1][i], left - 16 * (lg + 4));
+        }
+        multiply(0);
+        multiply(1);
+    }
+
+    // each wave's 64 x 128 block goes through LDS, 16-byte chunk c of row r at c ^ (r % 16), so that a store
+    // writes whole lines; they are not read again here and go past the caches
+    lds_barrier();
+    uint8_t* block = reinterpret_cast<uint8_t*>(smem) + wave * (WM * WN * 2);
+#pragma unroll
+    for (int j = 0; j < kNS; ++j) {
+        float bs[4];
+        column_scales(g, n0 + WN * wn + 16 * j + 4 * lg, bs);
+#pragma unroll
+        for (int i = 0; i < kMS; ++i) {
+            const int r = 16 * i + l16;
+            const int64_t m = m0 + WM * wm + r;
+            const float as = g.K > 0 && m < g.M ? g.a_s[m] : 0.0f;
+            *reinterpret_cast<uint2*>(block + r * 256 + (((2 * j + (lg >> 1)) ^ (r & 15)) * 16) + 8 * (lg & 1)) = scaled4(acc[i][j], as, bs);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < WM / 4; ++p) {
+        const int r = 4 * p + lg;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(block + r * 256 + ((l16 ^ (r & 15)) * 16));
+        const int64_t m = m0 + WM * wm + r, n = n0 + WN * wn + 8 * l16;
+        if (m >= g.M) continue;
+        uint16_t* c = g.c + m * g.ldc + n;
+        if (c_vec && n + 8 <= g.N) {
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(c));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < g.N) c[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+// ---- One to four rows of A: four columns a workgroup, whose waves take a KB of each in turn, 16 bytes a lane,
+// and add products of four bytes. B is read once, past the caches, in pieces of a KB: one row, 14336 x 4096
+// 10.5 us, 5.6 TB/s (14.2 in 16-row tiles whose loads read 256 bytes of a row).
+constexpr int kCols = 4, kPiece = 1024;
+template <int ROWS>
+__global__ __launch_bounds__(256) void rows_kernel(I8Args g) {
+    __shared__ int part[4][kCols][ROWS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols;
+    const uint8_t* pb[kCols];
+#pragma unroll
+    for (int r = 0; r < kCols; ++r) pb[r] = g.b + min(n0 + r, g.N - 1) * g.ldb;
+    int acc[kCols][ROWS] = {};
+    const int K = static_cast<int>(g.K);
+    for (int k0 = wave * kPiece; k0 < K; k0 += 4 * kPiece) {
+        const int k = k0 + 16 * lane, at = k < K ? k : 0;
+        i32x4 a[ROWS], b[kCols];
+#pragma unroll
+        for (int r = 0; r < kCols; ++r) b[r] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[r] + at));
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) {
+            a[m] = *reinterpret_cast<const i32x4*>(g.a + m * g.lda + at);
+            keep_bytes(a[m], K - k);
+        }
+#pragma unroll
+        for (int r = 0; r < kCols; ++r)
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) acc[r][m] = __builtin_amdgcn_sdot4(a[m][d], b[r][d], acc[r][m], false);
+    }
+#pragma unroll
+    for (int r = 0; r < kCols; ++r)
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) {
+            int v = acc[r][m];
+            v += __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);   // the pair's other lane
+            v += __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false);   // the other pair of four
+            v += __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false);  // the other four of eight
+            v += __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, false);  // the other eight of sixteen
+            v += __shfl_xor(v, 16);
+            v += __shfl_xor(v, 32);
+            if (lane == 0) part[wave][r][m] = v;
+        }
+    __syncthreads();
+    if (threadIdx.x < kCols * ROWS) {
+        const int r = threadIdx.x % kCols, m = threadIdx.x / kCols;
+        const int64_t n = n0 + r;
+        if (n < g.N) {
+            const int sum = part[0][r][m] + part[1][r][m] + part[2][r][m] + part[3][r][m];
+            const float v = K > 0 ? (static_cast<float>(sum) * g.a_s[m]) * g.b_s[n] : 0.0f;
+            g.c[m * g.ldc + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f));
         }
     }
 }
@@ -156,15 +397,38 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN>::kThreads), 1) void gemm_i8_k
 }  // namespace
 
 hipError_t launch_gemm_i8(const I8Args& g, int cus, hipStream_t stream) {
-    const int c_vec = reinterpret_cast<uintptr_t>(g.c) % 8 == 0 && g.ldc % 4 == 0;
-    const auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-#define BSFP8_I8(BM, BN, WM, WN)                                                                                         \
-    gemm_i8_kernel<BM, BN, WM, WN><<<static_cast<unsigned>(tiles(BM, BN)), Tile<BM, BN, WM, WN>::kThreads, 0, stream>>>( \
-        g, static_cast<int>((g.M + BM - 1) / BM), static_cast<int>((g.N + BN - 1) / BN), c_vec)
-    if (tiles(256, 256) >= cus / 2) BSFP8_I8(256, 256, 64, 128);
-    else if (tiles(128, 128) >= cus / 2) BSFP8_I8(128, 128, 64, 64);
-    else BSFP8_I8(64, 64, 32, 32);
-#undef BSFP8_I8
+    const sched::I8Kernel kernel = sched::i8_kernel(g.M, g.N, g.K, cus);
+    const sched::I8Tile tile = sched::kI8Tiles[kernel];
+    const int mt = static_cast<int>(sched::cdiv(g.M, tile.bm)), nt = static_cast<int>(sched::cdiv(g.N, tile.bn));
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(mt) * nt);
+    const int64_t piece = kernel == sched::kI8Big ? 16 : 8;
+    const int c_vec = reinterpret_cast<uintptr_t>(g.c) % piece == 0 && 2 * g.ldc % piece == 0;
+    const bool past = sched::i8_reads_once(g.M, g.N, kernel, cus);
+#define BSFP8_TILE(BM, BN, WM, WN, STAGES, KS)                                                                      \
+    do {                                                                                                            \
+        constexpr int kThreads = 64 * (BM / WM) * (BN / WN);                                                        \
+        if (past) tile_kernel<BM, BN, WM, WN, STAGES, KS, true><<<grid, kThreads, 0, stream>>>(g, mt, nt, c_vec);   \
+        else tile_kernel<BM, BN, WM, WN, STAGES, KS, false><<<grid, kThreads, 0, stream>>>(g, mt, nt, c_vec);       \
+    } while (0)
+    switch (kernel) {
+        case sched::kI8Rows:
+            switch (g.M) {
+                case 1: rows_kernel<1><<<grid, 256, 0, stream>>>(g); break;
+                case 2: rows_kernel<2><<<grid, 256, 0, stream>>>(g); break;
+                case 3: rows_kernel<3><<<grid, 256, 0, stream>>>(g); break;
+                default: rows_kernel<4><<<grid, 256, 0, stream>>>(g); break;
+            }
+            break;
+        case sched::kI8Tile32x32: BSFP8_TILE(32, 32, 16, 16, 4, 256); break;
+        case sched::kI8Tile32x64: BSFP8_TILE(32, 64, 32, 16, 3, 256); break;
+        case sched::kI8Tile64x64: BSFP8_TILE(64, 64, 16, 32, 4, 256); break;
+        case sched::kI8Tile64x128: tile_kernel<64, 128, 32, 32, 3, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
+        case sched::kI8Tile128x128: tile_kernel<128, 128, 32, 64, 4, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
+        case sched::kI8Tile128x128Two: tile_kernel<128, 128, 32, 64, 2, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
+        case sched::kI8Tile128x256: tile_kernel<128, 256, 32, 128, 3, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
+        default: big_kernel<<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
+    }
+#undef BSFP8_TILE
     return hipGetLastError();
 }
 

@@ -316,5 +316,50 @@ inline int64_t norm_backward_blocks(int64_t T) { return T < 512 ? T : 512; }
 constexpr int64_t kGradUnit = 8192, kGradBlocks = 512;
 inline int64_t grad_blocks(int64_t units) { return units < kGradBlocks ? units : kGradBlocks; }
 
+// gemm_i8: the kernel of M x N x K. A tile kernel's time goes by rounds: its tiles over the compute units, one or
+// two workgroups on each (those whose LDS lets two in), every round as long as K's blocks of 128 plus what a
+// tile does before and after them. The costs are microseconds a block of a round of up to `cus` tiles, and of
+// up to twice as many, fitted on MI355X to 119 problems of 4 to 8192 rows by 512 to 14336 columns (weights not
+// in the last-level cache); the tiles chosen by them are within 1% of the best ones on average, 11% at most.
+// Times measured (us; 32x32, 64x64, 128x128 with four stages, 256x256): 64 x 4096 x 4096 8.0, 11.9, 19.5, 49;
+// 512 x 5120 x 5120 53, 41, 32, 82 (64x128: 40); 2048 x 4096 x 4096 113, 81, 49, 62 (128x128 twice a CU: 41);
+// 8192 x 5120 x 5120 624, 445, 288, 235. Up to four rows go to the kernel without tiles (1 x 14336 x 4096
+// 10.5, in 32x64 tiles 14.1; 2 x 4096 x 14336 11.9, 17.2).
+enum I8Kernel {
+    kI8Rows, kI8Tile32x32, kI8Tile32x64, kI8Tile64x64, kI8Tile64x128, kI8Tile128x128, kI8Tile128x128Two, kI8Tile128x256, kI8Big
+};
+struct I8Tile {
+    int bm, bn;
+    double one, two;  // two == 0: one workgroup a compute unit
+    int more;         // blocks that a tile's beginning and end count as
+};
+constexpr I8Tile kI8Tiles[] = {
+    {4, 4, 0, 0, 0},           {32, 32, 0.16, 0.27, 3},  {32, 64, 0.25, 0.43, 3},   {64, 64, 0.30, 0, 3},  {64, 128, 0.48, 0.85, 3},
+    {128, 128, 0.65, 0, 5},    {128, 128, 0.90, 1.15, 4}, {128, 256, 1.05, 0, 7},    {256, 256, 1.65, 0, 9},
+};
+constexpr int64_t kI8RowsColumns = int64_t{1} << 24;  // 2^32 lanes and more beyond
+
+inline double i8_cost(const I8Tile& t, int64_t M, int64_t N, int64_t K, int cus) {
+    const int64_t tiles = cdiv(M, t.bm) * cdiv(N, t.bn), round = t.two > 0 ? 2 * static_cast<int64_t>(cus) : cus;
+    const int64_t rest = tiles % round;
+    const double whole = static_cast<double>(tiles / round) * (t.two > 0 ? t.two : t.one);
+    const double last = rest == 0 ? 0.0 : rest <= cus ? t.one : t.two;
+    return (whole + last) * static_cast<double>(cdiv(K, geom::kBlockK) + t.more);
+}
+inline I8Kernel i8_kernel(int64_t M, int64_t N, int64_t K, int cus) {
+    if (M <= 4 && N <= kI8RowsColumns) return kI8Rows;
+    int best = kI8Tile32x32;
+    for (int k = kI8Tile32x64; k <= kI8Big; ++k)
+        if (i8_cost(kI8Tiles[k], M, N, K, cus) < i8_cost(kI8Tiles[best], M, N, K, cus)) best = k;
+    return static_cast<I8Kernel>(best);
+}
+
+// Whether a small tile kernel reads B past the caches: one row of tiles, more of them than compute units. Us
+// through the caches and past them: 16 x 14336 x 4096 in 32x64 14.4, 13.0; 64 x 14336 x 4096 in 64x64 17.2, 15.4; with
+// fewer, 16 x 4096 x 14336 in 32x32 18.4, 19.3, and 64 x 5120 x 5120 in 64x64 16.7, 16.3.
+inline bool i8_reads_once(int64_t M, int64_t N, I8Kernel kernel, int cus) {
+    return kernel != kI8Rows && kernel <= kI8Tile64x64 && M <= kI8Tiles[kernel].bm && cdiv(N, kI8Tiles[kernel].bn) > cus * 3 / 4;
+}
+
 }  // namespace sched
 }  // namespace bsfp8
