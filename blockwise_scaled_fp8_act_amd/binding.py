@@ -1,7 +1,7 @@
 """Thin ctypes binding of libbsfp8.so (the gfx950 HIP library); declarations in include/blockwise_fp8.h.
 
 Argument marshalling only: every step runs in the HIP kernels. torch provides device memory and the
-current stream. The functions of the mixture-of-experts operators first offer their arguments to the
+current stream. The functions whose kernels take a few microseconds first offer their arguments to the
 C part _calls (csrc/calls.c), if it was built, which makes the usual call without ctypes. There is no
 CPU fallback: if the library is missing, loading raises.
 
@@ -133,10 +133,12 @@ def _bind_calls(L):
     except ImportError:         # not built, or for another interpreter: the same kernels, called through ctypes
         return
     calls.bind(torch.Tensor, Bsfp8Error, _get_device, _raw_stream,
-               (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float8_e4m3fn),
-               tuple(ctypes.cast(f, _vp).value for f in (L.moe_route, L.moe_route_backward, L.moe_plan_workspace, L.moe_plan,
-                                                         L.moe_dispatch, L.moe_combine, L.moe_combine_backward,
-                                                         L.gemm_1x128_128x128_routed)))
+               (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float8_e4m3fn, torch.int8),
+               tuple(ctypes.cast(f, _vp).value for f in (
+                   L.moe_route, L.moe_route_backward, L.moe_plan_workspace, L.moe_plan, L.moe_dispatch, L.moe_combine, L.moe_combine_backward,
+                   L.gemm_1x128_128x128_routed, L.rms_norm_quantize, L.rms_norm_quantize_rhs, L.rms_norm_backward_workspace,
+                   L.rms_norm_backward, L.swiglu_quantize, L.swiglu_quantize_lhs_and_rhs, L.swiglu_backward, L.swiglu_backward_quantize,
+                   L.quantize_rows_i8, L.gemm_i8, L.grad_workspace, L.grad_norm, L.clip_grads)))
     _calls = calls
 
 
@@ -972,6 +974,10 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, fmt="e4m3fn", q=None, 
     + eps), v = h * rstd * weight (weight [H] bf16 or fp32). ``fmt``: "e4m3fn" or "e4m3fnuz" (q [T, H]
     uint8, s (Hb, T) fp32, as quantize_lhs), "int8" (q int8, s (T,)), or None (y only). Returns (q, s, h, y,
     rstd): h None without a residual (it is x), y [T, H] bf16 and rstd (T,) fp32 where given or wanted."""
+    if stream is None and _calls is not None:
+        done = _calls.rms_norm_quantize(x, weight, residual, eps, fmt, q, s, h, y, rstd, want_y, want_rstd)
+        if done is not None:
+            return done
     kind = _code_kind(fmt)
     T, H = _matrix("x", x, _BF16).shape
     _weight_of(weight, H)
@@ -1005,6 +1011,10 @@ def rms_norm_quantize_rhs(h, weight, rstd, qT=None, s=None, stream=None, fmt="e4
     """The normed rows h * rstd * weight in 128x1 groups, transposed (quantize_rhs of their fp32 values), from h
     [T, H] (bf16 or fp32), weight [H] and rstd (T,) as rms_norm_quantize gave them. Returns (qT [H, T] uint8,
     s (Tb, H) fp32)."""
+    if stream is None and _calls is not None:
+        done = _calls.rms_norm_quantize_rhs(h, weight, rstd, qT, s, fmt)
+        if done is not None:
+            return done
     kind = fp8_format(fmt)
     T, H = _matrix("h", h, _BF16_F32).shape
     _weight_of(weight, H)
@@ -1056,6 +1066,10 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None, works
     and of the residual (``dh``, of h's type, is added: the gradient that reaches h by another way; dx may be
     dh itself); dweight [H], of the weight's type. ``workspace``: a uint8 tensor of
     rms_norm_backward_workspace(T, H) bytes that calls in a row may share. Returns (dx, dweight)."""
+    if stream is None and _calls is not None:
+        done = _calls.rms_norm_backward(dy, h, weight, rstd, dh, dx, dweight, workspace)
+        if done is not None:
+            return done
     T, H = _matrix("dy", dy, _BF16).shape
     _matrix("h", h, _BF16_F32, (T, H))
     _weight_of(weight, H)
@@ -1090,6 +1104,10 @@ def _gate_up(gu):
 def swiglu_quantize(gu, fmt="e4m3fn", q=None, s=None, y=None, want_y=False, stream=None):
     """silu(gate) * up of gu [T, 2 F] (bf16, gate columns first) as 8-bit codes; ``fmt`` and the outputs as in
     rms_norm_quantize. Returns (q, s, y)."""
+    if stream is None and _calls is not None:
+        done = _calls.swiglu_quantize(gu, fmt, q, s, y, want_y)
+        if done is not None:
+            return done
     kind = _code_kind(fmt)
     T, F = _gate_up(gu)
     q, s, y = _row_outputs(gu, T, F, kind, q, s, y, want_y, stream)
@@ -1104,6 +1122,10 @@ def swiglu_quantize(gu, fmt="e4m3fn", q=None, s=None, y=None, want_y=False, stre
 def swiglu_quantize_lhs_and_rhs(gu, q=None, a_s=None, qT=None, s=None, stream=None, fmt="e4m3fn"):
     """silu(gate) * up of gu [T, 2 F] in both groupings: (q [T, F], a_s (Fb, T), qT [F, T], s (Tb, F)), as
     quantize_lhs_and_rhs of its fp32 values."""
+    if stream is None and _calls is not None:
+        done = _calls.swiglu_quantize_lhs_and_rhs(gu, q, a_s, qT, s, fmt)
+        if done is not None:
+            return done
     kind = fp8_format(fmt)
     T, F = _gate_up(gu)
     q, a_s, qT, s = _tile_outputs(gu, T, F, q, a_s, qT, s, stream, kind)
@@ -1117,6 +1139,10 @@ def swiglu_quantize_lhs_and_rhs(gu, q=None, a_s=None, qT=None, s=None, stream=No
 
 def swiglu_backward(dy, gu, dgu=None, stream=None):
     """The gradient [T, 2 F] (bf16) of silu(gate) * up with respect to gu, from dy [T, F] (bf16)."""
+    if stream is None and _calls is not None:
+        done = _calls.swiglu_backward(dy, gu, dgu)
+        if done is not None:
+            return done
     T, F = _gate_up(gu)
     _matrix("dy", dy, _BF16, (T, F))
     if dgu is None:
@@ -1133,6 +1159,10 @@ def swiglu_backward(dy, gu, dgu=None, stream=None):
 def swiglu_backward_quantize(dy, gu, q=None, a_s=None, qT=None, s=None, stream=None, fmt="e4m3fn"):
     """swiglu_backward in both groupings: (q [T, 2 F], a_s (2Fb, T), qT [2 F, T], s (Tb, 2 F)), as
     quantize_lhs_and_rhs of its fp32 values."""
+    if stream is None and _calls is not None:
+        done = _calls.swiglu_backward_quantize(dy, gu, q, a_s, qT, s, fmt)
+        if done is not None:
+            return done
     kind = fp8_format(fmt)
     T, F = _gate_up(gu)
     _matrix("dy", dy, _BF16, (T, F))
@@ -1149,6 +1179,10 @@ def swiglu_backward_quantize(dy, gu, q=None, a_s=None, qT=None, s=None, stream=N
 def quantize_rows_i8(x, q=None, s=None, stream=None):
     """int8 codes of x [M, K] (bf16) with one scale a row: a token's activations, or the output channels of a
     weight [out, in]. Returns (q [M, K] int8, s (M,) fp32)."""
+    if stream is None and _calls is not None:
+        done = _calls.quantize_rows_i8(x, q, s)
+        if done is not None:
+            return done
     M, K = _matrix("x", x, _BF16).shape
     q, s, _ = _row_outputs(x, M, K, "int8", q, s, None, False, stream)
     dev = _current(x, q, s)
@@ -1161,6 +1195,10 @@ def quantize_rows_i8(x, q=None, s=None, stream=None):
 def gemm_i8(a, a_s, b, b_s, c=None, K=None, stream=None):
     """C = (A B^T) * a_s * b_s: A [M, K] int8 with a scale a row a_s (M,), B [N, K] int8 with a scale an output
     column b_s (N,); the sum exact in int32. Returns c [M, N] bf16. Rows are 16-byte aligned."""
+    if stream is None and _calls is not None:
+        done = _calls.gemm_i8(a, a_s, b, b_s, c, K)
+        if done is not None:
+            return done
     _matrix("a", a, (torch.int8,))
     _matrix("b", b, (torch.int8,))
     M, N = a.shape[0], b.shape[0]
@@ -1250,6 +1288,10 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
     """The 2-norm of all values of the tensors (bf16 or fp32, dense, on one GPU): returns norm (1,) fp32 on the
     device; the host is not synchronised. ``workspace``: a uint8 tensor of grad_workspace(grads) bytes that
     calls in a row may share."""
+    if stream is None and _calls is not None:
+        done = _calls.grad_norm(grads, norm, workspace)
+        if done is not None:
+            return done
     grads = _grad_list("grads", grads)
     dev, addresses, sizes, types, norm, workspace = _grad_call(grads, norm, workspace, stream)
     _call("grad_norm", addresses, sizes, types, len(grads), _ptr(norm), _ptr(workspace), 0 if workspace is None else workspace.numel(),
@@ -1261,6 +1303,10 @@ def clip_grads(grads, max_norm, out=None, norm=None, eps=1e-6, workspace=None, s
     """Scales the gradients by min(1, max_norm / (norm + eps)), norm being grad_norm(grads); in place, or into
     the tensors of ``out`` (of the gradients' shapes and layouts, bf16 or fp32). Where the norm is not finite the
     gradients are left (copied) as they are. Returns norm (1,) fp32 on the device; the host is not synchronised."""
+    if stream is None and _calls is not None:
+        done = _calls.clip_grads(grads, max_norm, out, norm, eps, workspace)
+        if done is not None:
+            return done
     grads = _grad_list("grads", grads)
     if not max_norm >= 0:
         raise ValueError(f"max_norm must be >= 0, got {max_norm}")

@@ -1,4 +1,5 @@
-/* The usual call of a mixture-of-experts operator in one step, for CPython: plain torch tensors on the
+/* The usual call of an operator whose kernels take a few microseconds (those of a mixture-of-experts layer, those
+ * between the 8-bit products, the int8 product, the gradient norm) in one step, for CPython: plain torch tensors on the
  * current GPU, the current stream, every argument as binding.py's functions want it. A function here
  * looks at its arguments, makes the outputs that are not given, calls the library and returns what
  * binding.py's function of that name returns; where anything is not as usual it returns None and has
@@ -8,7 +9,7 @@
  *
  * Why: for few tokens these operators' kernels take 3 to 9 us and the launch 3.3. A call here takes 4.6
  * us (route, outputs given), 4.7 (combine), 5.1 (dispatch) and 5.3 (product); through binding.py's
- * checks and ctypes 6.8, 6.9, 7.4 and 9.1. */
+ * checks and ctypes 6.8, 6.9, 7.4 and 9.1. NORMFIGURES */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <math.h>
@@ -18,7 +19,7 @@
 
 /* ---- what bind() is given */
 static PyObject *tensor_type, *error_type, *get_stream, *get_device;
-enum { F32, BF16, I32, I64, U8, FP8, TYPES };
+enum { F32, BF16, I32, I64, U8, FP8, I8, TYPES };
 static PyObject* types[TYPES];
 static __typeof__(&moe_route) call_route;
 static __typeof__(&moe_route_backward) call_route_backward;
@@ -28,8 +29,21 @@ static __typeof__(&moe_dispatch) call_dispatch;
 static __typeof__(&moe_combine) call_combine;
 static __typeof__(&moe_combine_backward) call_combine_backward;
 static __typeof__(&gemm_1x128_128x128_routed) call_product;
+static __typeof__(&rms_norm_quantize) call_norm;
+static __typeof__(&rms_norm_quantize_rhs) call_norm_rhs;
+static __typeof__(&rms_norm_backward_workspace) call_norm_workspace;
+static __typeof__(&rms_norm_backward) call_norm_backward;
+static __typeof__(&swiglu_quantize) call_swiglu;
+static __typeof__(&swiglu_quantize_lhs_and_rhs) call_swiglu_dual;
+static __typeof__(&swiglu_backward) call_swiglu_backward;
+static __typeof__(&swiglu_backward_quantize) call_swiglu_backward_dual;
+static __typeof__(&quantize_rows_i8) call_rows_i8;
+static __typeof__(&gemm_i8) call_gemm_i8;
+static __typeof__(&grad_workspace) call_grad_workspace;
+static __typeof__(&grad_norm) call_grad_norm;
+static __typeof__(&clip_grads) call_clip;
 
-static PyObject *n_dtype, *n_shape, *n_stride, *n_get_device, *n_data_ptr, *n_new_empty, *n_dtype_only;
+static PyObject *n_dtype, *n_shape, *n_stride, *n_get_device, *n_data_ptr, *n_new_empty, *n_dtype_only, *n_numel, *n_is_contiguous;
 
 /* ---- tensors */
 typedef struct {
@@ -358,28 +372,377 @@ static PyObject* product(PyObject* self, PyObject* const* o, Py_ssize_t n) {
     return out(c);
 }
 
+/* ---- between the 8-bit products */
+static int codes_of(PyObject* o, int* out) {
+    if (o == Py_None) {
+        *out = BSFP8_CODES_NONE;
+        return 1;
+    }
+    if (!PyUnicode_CheckExact(o)) return 0;
+    if (PyUnicode_CompareWithASCIIString(o, "e4m3fn") == 0) *out = BSFP8_CODES_E4M3FN;
+    else if (PyUnicode_CompareWithASCIIString(o, "int8") == 0) *out = BSFP8_CODES_INT8;
+    else if (PyUnicode_CompareWithASCIIString(o, "e4m3fnuz") == 0) *out = BSFP8_CODES_E4M3FNUZ;
+    else return 0;
+    return 1;
+}
+static int fp8_codes_of(PyObject* o, int* out) {
+    return codes_of(o, out) && (*out == BSFP8_CODES_E4M3FN || *out == BSFP8_CODES_E4M3FNUZ);
+}
+static int code_type(int type, int codes) {
+    return codes == BSFP8_CODES_INT8 ? type == I8 : type == U8 || (codes == BSFP8_CODES_E4M3FN && type == FP8);
+}
+static int codes_matrix(PyObject* t, const View* like, View* v, int codes, int64_t a, int64_t b) {
+    if (t == Py_None) return make(like, v, codes == BSFP8_CODES_INT8 ? I8 : U8, a, b);
+    return look(t, v) && code_type(v->type, codes) && rows_at_stride(v) && v->n[0] == a && v->n[1] == b;
+}
+static int scales(PyObject* t, const View* like, View* v, int64_t a, int64_t b) { /* fp32 [a, b], b < 0: [a] */
+    if (t == Py_None) return make(like, v, F32, a, b);
+    return look(t, v) && (b < 0 ? dense1(v, F32, a) : dense2(v, F32, a, b));
+}
+static int bf16_rows(PyObject* t, View* v) { return look(t, v) && v->type == BF16 && rows_at_stride(v); }
+static int bf16_or_f32(const View* v) { return v->type == BF16 || v->type == F32; }
+static int dtype_of(const View* v) { return v->type == F32 ? BSFP8_F32 : BSFP8_BF16; }
+static int weight_of(PyObject* t, View* v, int64_t H) { return look(t, v) && bf16_or_f32(v) && dense1(v, v->type, H); }
+static int one_device(const View* v, int n) { /* of the tensors that are there */
+    for (int i = 1; i < n; ++i)
+        if (v[i].t != NULL && v[i].device != v[0].device) return 0;
+    return 1;
+}
+static PyObject* out_or_none(View* v) {
+    if (v->t == NULL) Py_RETURN_NONE;
+    return out(v);
+}
+static int64_t stride_or_0(const View* v) { return v->t != NULL ? stride(v) : 0; }
+
+/* q, s, y of rows [T, H] */
+static int row_outputs(const View* like, int64_t T, int64_t H, int codes, PyObject* oq, PyObject* os, PyObject* oy, int want_y, View* q, View* s,
+                       View* y) {
+    if (T > ((int64_t)1 << 24) - 16) return 0;
+    if (codes == BSFP8_CODES_NONE) {
+        if (oq != Py_None || os != Py_None) return 0;
+        want_y = 1;
+    } else {
+        const int i8 = codes == BSFP8_CODES_INT8;
+        if (!codes_matrix(oq, like, q, codes, T, H) || !scales(os, like, s, i8 ? T : (H + 127) / 128, i8 ? -1 : T)) return 0;
+    }
+    return oy != Py_None ? matrix(oy, y, BF16, T, H) : !want_y || make(like, y, BF16, T, H);
+}
+
+/* x, weight, residual, eps, fmt, q, s, h, y, rstd, want_y, want_rstd */
+static PyObject* norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[8] = {{0}};
+    View *x = v, *w = v + 1, *r = v + 2, *h = v + 3, *q = v + 4, *s = v + 5, *y = v + 6, *rstd = v + 7;
+    int codes, want_y, want_rstd, status;
+    void* stream;
+    if (n != 12 || !bf16_rows(a[0], x) || !PyFloat_CheckExact(a[3]) || !codes_of(a[4], &codes) || !flag(a[10], &want_y) || !flag(a[11], &want_rstd))
+        return unusual(v, 8);
+    const float eps = (float)PyFloat_AS_DOUBLE(a[3]);
+    const int64_t T = x->n[0], H = x->n[1];
+    if (!(eps > 0) || !isfinite(eps) || !weight_of(a[1], w, H)) return unusual(v, 8);
+    if (a[2] != Py_None) {
+        if (!look(a[2], r) || !bf16_or_f32(r) || !rows_at_stride(r) || r->n[0] != T || r->n[1] != H) return unusual(v, 8);
+        if (a[7] != Py_None ? !matrix(a[7], h, r->type, T, H) : !make(r, h, r->type, T, H)) return unusual(v, 8);
+    } else if (a[7] != Py_None) {
+        return unusual(v, 8);
+    }
+    if (!row_outputs(x, T, H, codes, a[5], a[6], a[8], want_y, q, s, y)) return unusual(v, 8);
+    if (a[9] != Py_None ? !look(a[9], rstd) || !dense1(rstd, F32, T) : want_rstd && !make(x, rstd, F32, T, -1)) return unusual(v, 8);
+    if (!one_device(v, 8) || !stream_of(x->device, &stream)) return unusual(v, 8);
+    LAUNCH(status, call_norm(x->p, T, H, stride(x), r->p, r->t != NULL ? dtype_of(r) : BSFP8_BF16, stride_or_0(r), w->p, dtype_of(w), eps, h->p,
+                             stride_or_0(h), rstd->p, codes, q->p, stride_or_0(q), s->p, y->p, stride_or_0(y), stream));
+    if (status != 0) return failed(v, 8, "rms_norm_quantize", status);
+    return Py_BuildValue("(NNNNN)", out_or_none(q), out_or_none(s), out_or_none(h), out_or_none(y), out_or_none(rstd));
+}
+
+/* h, weight, rstd, qT, s, fmt */
+static PyObject* norm_rhs(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[5] = {{0}};
+    View *h = v, *w = v + 1, *rstd = v + 2, *q = v + 3, *s = v + 4;
+    int codes, status;
+    void* stream;
+    if (n != 6 || !look(a[0], h) || !bf16_or_f32(h) || !rows_at_stride(h) || !fp8_codes_of(a[5], &codes)) return unusual(v, 5);
+    const int64_t T = h->n[0], H = h->n[1];
+    if (!weight_of(a[1], w, H) || !look(a[2], rstd) || !dense1(rstd, F32, T) || !codes_matrix(a[3], h, q, codes, H, T) ||
+        !scales(a[4], h, s, (T + 127) / 128, H) || !one_device(v, 5) || !stream_of(h->device, &stream))
+        return unusual(v, 5);
+    LAUNCH(status, call_norm_rhs(h->p, dtype_of(h), T, H, stride(h), w->p, dtype_of(w), rstd->p, codes, q->p, stride(q), s->p, stream));
+    if (status != 0) return failed(v, 5, "rms_norm_quantize_rhs", status);
+    return Py_BuildValue("(NN)", out(q), out(s));
+}
+
+/* dy, h, weight, rstd, dh, dx, dweight, workspace */
+static PyObject* norm_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[8] = {{0}};
+    View *dy = v, *h = v + 1, *w = v + 2, *rstd = v + 3, *dh = v + 4, *dx = v + 5, *dw = v + 6, *ws = v + 7;
+    int status;
+    void* stream;
+    if (n != 8 || !bf16_rows(a[0], dy) || !look(a[1], h) || !bf16_or_f32(h) || !rows_at_stride(h)) return unusual(v, 8);
+    const int64_t T = dy->n[0], H = dy->n[1], need = call_norm_workspace(T, H);
+    if (need < 0 || h->n[0] != T || h->n[1] != H || !weight_of(a[2], w, H) || !look(a[3], rstd) || !dense1(rstd, F32, T)) return unusual(v, 8);
+    if (a[4] != Py_None && !matrix(a[4], dh, h->type, T, H)) return unusual(v, 8);
+    if (a[5] != Py_None ? !matrix(a[5], dx, h->type, T, H) : !make(h, dx, h->type, T, H)) return unusual(v, 8);
+    if (a[6] != Py_None ? !look(a[6], dw) || !dense1(dw, w->type, H) : !make(w, dw, w->type, H, -1)) return unusual(v, 8);
+    if (a[7] != Py_None ? !look(a[7], ws) || !dense1(ws, U8, ws->n[0]) || ws->n[0] < need || ((uintptr_t)ws->p & 15) != 0
+                        : !make(dy, ws, U8, need, -1))
+        return unusual(v, 8);
+    if (!one_device(v, 8) || !stream_of(dy->device, &stream)) return unusual(v, 8);
+    LAUNCH(status, call_norm_backward(dy->p, stride(dy), h->p, dtype_of(h), stride(h), w->p, dtype_of(w), rstd->p, dh->p, stride_or_0(dh), T, H, dx->p,
+                                      stride(dx), dw->p, ws->p, ws->n[0], stream));
+    if (status != 0) return failed(v, 8, "rms_norm_backward", status);
+    PyObject* r = Py_BuildValue("(NN)", out(dx), out(dw));
+    drop(v, 8);
+    return r;
+}
+
+/* gu, fmt, q, s, y, want_y */
+static PyObject* swiglu(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[4] = {{0}};
+    View *gu = v, *q = v + 1, *s = v + 2, *y = v + 3;
+    int codes, want_y, status;
+    void* stream;
+    if (n != 6 || !bf16_rows(a[0], gu) || gu->n[1] % 2 != 0 || !codes_of(a[1], &codes) || !flag(a[5], &want_y)) return unusual(v, 4);
+    const int64_t T = gu->n[0], F = gu->n[1] / 2;
+    if (!row_outputs(gu, T, F, codes, a[2], a[3], a[4], want_y, q, s, y) || !one_device(v, 4) || !stream_of(gu->device, &stream))
+        return unusual(v, 4);
+    LAUNCH(status, call_swiglu(gu->p, T, F, stride(gu), codes, q->p, stride_or_0(q), s->p, y->p, stride_or_0(y), stream));
+    if (status != 0) return failed(v, 4, "swiglu_quantize", status);
+    return Py_BuildValue("(NNN)", out_or_none(q), out_or_none(s), out_or_none(y));
+}
+
+/* q, a_s, qT, s of [T, C] in v[0..3] */
+static int tile_outputs(PyObject* const* a, const View* like, int64_t T, int64_t C, int codes, View* v) {
+    return codes_matrix(a[0], like, v, codes, T, C) && scales(a[1], like, v + 1, (C + 127) / 128, T) &&
+           codes_matrix(a[2], like, v + 2, codes, C, T) && scales(a[3], like, v + 3, (T + 127) / 128, C);
+}
+
+/* gu, q, a_s, qT, s, fmt */
+static PyObject* swiglu_dual(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[5] = {{0}};
+    View* gu = v;
+    int codes, status;
+    void* stream;
+    if (n != 6 || !bf16_rows(a[0], gu) || gu->n[1] % 2 != 0 || !fp8_codes_of(a[5], &codes)) return unusual(v, 5);
+    const int64_t T = gu->n[0], F = gu->n[1] / 2;
+    if (!tile_outputs(a + 1, gu, T, F, codes, v + 1) || !one_device(v, 5) || !stream_of(gu->device, &stream)) return unusual(v, 5);
+    LAUNCH(status, call_swiglu_dual(gu->p, T, F, stride(gu), codes, v[1].p, stride(v + 1), v[2].p, v[3].p, stride(v + 3), v[4].p, stream));
+    if (status != 0) return failed(v, 5, "swiglu_quantize_lhs_and_rhs", status);
+    return Py_BuildValue("(NNNN)", out(v + 1), out(v + 2), out(v + 3), out(v + 4));
+}
+
+/* dy, gu, dgu */
+static PyObject* swiglu_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[3] = {{0}};
+    View *gu = v, *dy = v + 1, *d = v + 2;
+    int status;
+    void* stream;
+    if (n != 3 || !bf16_rows(a[1], gu) || gu->n[1] % 2 != 0) return unusual(v, 3);
+    const int64_t T = gu->n[0], F = gu->n[1] / 2;
+    if (!matrix(a[0], dy, BF16, T, F) || (a[2] != Py_None ? !matrix(a[2], d, BF16, T, 2 * F) : !make(gu, d, BF16, T, 2 * F)) ||
+        !one_device(v, 3) || !stream_of(gu->device, &stream))
+        return unusual(v, 3);
+    LAUNCH(status, call_swiglu_backward(dy->p, stride(dy), gu->p, stride(gu), T, F, d->p, stride(d), stream));
+    if (status != 0) return failed(v, 3, "swiglu_backward", status);
+    return out(d);
+}
+
+/* dy, gu, q, a_s, qT, s, fmt */
+static PyObject* swiglu_back_dual(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[6] = {{0}};
+    View *gu = v, *dy = v + 1;
+    int codes, status;
+    void* stream;
+    if (n != 7 || !bf16_rows(a[1], gu) || gu->n[1] % 2 != 0 || !fp8_codes_of(a[6], &codes)) return unusual(v, 6);
+    const int64_t T = gu->n[0], F = gu->n[1] / 2;
+    if (!matrix(a[0], dy, BF16, T, F) || !tile_outputs(a + 2, gu, T, 2 * F, codes, v + 2) || !one_device(v, 6) || !stream_of(gu->device, &stream))
+        return unusual(v, 6);
+    LAUNCH(status, call_swiglu_backward_dual(dy->p, stride(dy), gu->p, stride(gu), T, F, codes, v[2].p, stride(v + 2), v[3].p, v[4].p, stride(v + 4),
+                                             v[5].p, stream));
+    if (status != 0) return failed(v, 6, "swiglu_backward_quantize", status);
+    return Py_BuildValue("(NNNN)", out(v + 2), out(v + 3), out(v + 4), out(v + 5));
+}
+
+/* x, q, s */
+static PyObject* rows_i8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    View v[4] = {{0}};
+    View *x = v, *q = v + 1, *s = v + 2;
+    int status;
+    void* stream;
+    if (n != 3 || !bf16_rows(a[0], x) || !row_outputs(x, x->n[0], x->n[1], BSFP8_CODES_INT8, a[1], a[2], Py_None, 0, q, s, v + 3) ||
+        !one_device(v, 3) || !stream_of(x->device, &stream))
+        return unusual(v, 4);
+    LAUNCH(status, call_rows_i8(x->p, x->n[0], x->n[1], stride(x), q->p, stride(q), s->p, stream));
+    if (status != 0) return failed(v, 4, "quantize_rows_i8", status);
+    return Py_BuildValue("(NN)", out(q), out(s));
+}
+
+static int64_t i8_stride(const View* v) { return v->n[0] > 1 ? v->s[0] : (v->n[1] + 15) / 16 * 16; }
+
+/* a, a_s, b, b_s, c, K */
+static PyObject* i8_product(PyObject* self, PyObject* const* o, Py_ssize_t n) {
+    View v[5] = {{0}};
+    View *a = v, *a_s = v + 1, *b = v + 2, *b_s = v + 3, *c = v + 4;
+    int64_t K;
+    int status;
+    void* stream;
+    if (n != 6 || !look(o[0], a) || a->type != I8 || !rows_at_stride(a) || !look(o[2], b) || b->type != I8 || !rows_at_stride(b)) return unusual(v, 5);
+    const int64_t M = a->n[0], N = b->n[0];
+    if (o[5] == Py_None) K = a->n[1];
+    else if (!number(o[5], &K)) return unusual(v, 5);
+    if (K < 0 || K > a->n[1] || K > b->n[1] || K > 131071 || !look(o[1], a_s) || !dense1(a_s, F32, M) || !look(o[3], b_s) || !dense1(b_s, F32, N))
+        return unusual(v, 5);
+    if (o[4] != Py_None ? !matrix(o[4], c, BF16, M, N) : !make(a, c, BF16, M, N)) return unusual(v, 5);
+    if (!one_device(v, 5) || !stream_of(a->device, &stream)) return unusual(v, 5);
+    LAUNCH(status, call_gemm_i8(a->p, i8_stride(a), a_s->p, b->p, i8_stride(b), b_s->p, c->p, stride(c), M, N, K, stream));
+    if (status != 0) return failed(v, 5, "gemm_i8", status);
+    return out(c);
+}
+
+/* ---- gradients of many tensors */
+static int64_t whole(PyObject* t, PyObject* method) { /* a method's number, -1 with an error */
+    PyObject* o = PyObject_CallMethodNoArgs(t, method);
+    const int64_t r = o != NULL ? PyLong_AsLongLong(o) : -1;
+    Py_XDECREF(o);
+    return r;
+}
+
+typedef struct {
+    void** p;
+    int64_t* n;
+    int* type;
+} Many;
+
+/* The tensors of a list, contiguous, on one device (< 0: the first one's, which is set). */
+static int look_at_all(PyObject** t, Py_ssize_t count, Many m, long* device) {
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        if ((PyObject*)Py_TYPE(t[i]) != tensor_type) return 0;
+        PyObject* o = PyObject_GetAttr(t[i], n_dtype);
+        m.type[i] = o == types[F32] ? BSFP8_F32 : o == types[BF16] ? BSFP8_BF16 : -1;
+        Py_XDECREF(o);
+        if (m.type[i] < 0) return 0;
+        o = PyObject_CallMethodNoArgs(t[i], n_is_contiguous);
+        const int dense = o == Py_True;
+        Py_XDECREF(o);
+        if (!dense) return 0;
+        const long at = (long)whole(t[i], n_get_device);
+        if (at < 0 || (*device >= 0 && at != *device)) return 0;
+        *device = at;
+        m.n[i] = whole(t[i], n_numel);
+        o = PyObject_CallMethodNoArgs(t[i], n_data_ptr);
+        m.p[i] = o != NULL ? PyLong_AsVoidPtr(o) : NULL;
+        Py_XDECREF(o);
+        if (m.n[i] < 0 || PyErr_Occurred()) return 0;
+    }
+    return 1;
+}
+
+static int same_shapes(PyObject** a, PyObject** b, Py_ssize_t count) {
+    int same = 1;
+    for (Py_ssize_t i = 0; same && i < count; ++i) {
+        PyObject *x = PyObject_GetAttr(a[i], n_shape), *y = PyObject_GetAttr(b[i], n_shape);
+        same = x != NULL && y != NULL && PyObject_RichCompareBool(x, y, Py_EQ) == 1;
+        Py_XDECREF(x);
+        Py_XDECREF(y);
+    }
+    return same;
+}
+
+/* grads, out (a list, or None: in place), norm, workspace; the launch with max_norm and eps where clip is set */
+static PyObject* gradients(PyObject* grads, PyObject* outs, PyObject* o_norm, PyObject* o_ws, int clip, float max_norm, float eps) {
+    View v[2] = {{0}};
+    View *norm = v, *ws = v + 1;
+    if (!PyList_CheckExact(grads) || (outs != Py_None && !PyList_CheckExact(outs))) Py_RETURN_NONE;
+    const Py_ssize_t count = PyList_GET_SIZE(grads);
+    if (count == 0 || count > 0xFFFFFF || (outs != Py_None && PyList_GET_SIZE(outs) != count)) Py_RETURN_NONE;
+    /* the tensors are held while Python code may run */
+    const size_t each = 2 * (sizeof(PyObject*) + sizeof(void*) + sizeof(int64_t) + sizeof(int));
+    char* memory = PyMem_Malloc(each * (size_t)count);
+    if (memory == NULL) return PyErr_NoMemory();
+    PyObject **g = (PyObject**)memory, **o = g + count;
+    void** p = (void**)(o + count);
+    int64_t* n = (int64_t*)(p + 2 * count);
+    int* type = (int*)(n + 2 * count);
+    const Many mg = {p, n, type}, mo = {p + count, n + count, type + count};
+    const int apart = outs != Py_None;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        g[i] = PyList_GET_ITEM(grads, i);
+        Py_INCREF(g[i]);
+        if (apart) {
+            o[i] = PyList_GET_ITEM(outs, i);
+            Py_INCREF(o[i]);
+        }
+    }
+    PyObject* result = NULL;
+    int usual = 0, status = 0;
+    long device = -1;
+    void* stream;
+    View first = {0};
+    if (look_at_all(g, count, mg, &device) && (!apart || (look_at_all(o, count, mo, &device) && same_shapes(g, o, count)))) {
+        const int64_t need = call_grad_workspace(mg.n, count);
+        first.t = g[0], first.type = TYPES, first.device = device;
+        usual = need > 0 && (o_norm != Py_None ? look(o_norm, norm) && dense1(norm, F32, 1) : make(&first, norm, F32, 1, -1)) &&
+                (o_ws != Py_None ? look(o_ws, ws) && dense1(ws, U8, ws->n[0]) && ws->n[0] >= need && ((uintptr_t)ws->p & 7) == 0
+                                 : make(&first, ws, U8, need, -1)) &&
+                norm->device == device && ws->device == device && stream_of(device, &stream);
+    }
+    if (usual) {
+        if (clip)
+            LAUNCH(status, call_clip((const void* const*)mg.p, apart ? mo.p : mg.p, mg.n, mg.type, apart ? mo.type : mg.type, count, max_norm, eps,
+                                     norm->p, ws->p, ws->n[0], stream));
+        else
+            LAUNCH(status, call_grad_norm((const void* const*)mg.p, mg.n, mg.type, count, norm->p, ws->p, ws->n[0], stream));
+        result = status != 0 ? failed(v, 2, clip ? "clip_grads" : "grad_norm", status) : out(norm);
+        drop(v, 2);
+    } else {
+        result = unusual(v, 2);
+    }
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        Py_DECREF(g[i]);
+        if (apart) Py_DECREF(o[i]);
+    }
+    PyMem_Free(memory);
+    return result;
+}
+
+/* grads, norm, workspace */
+static PyObject* norm_of_many(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    if (n != 3) Py_RETURN_NONE;
+    return gradients(a[0], Py_None, a[1], a[2], 0, 0.0f, 0.0f);
+}
+
+/* grads, max_norm, out, norm, eps, workspace */
+static PyObject* clip_many(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    if (n != 6 || !PyFloat_CheckExact(a[1]) || !PyFloat_CheckExact(a[4])) Py_RETURN_NONE;
+    const double max_norm = PyFloat_AS_DOUBLE(a[1]), eps = PyFloat_AS_DOUBLE(a[4]);
+    if (!(max_norm >= 0) || !(eps >= 0) || !isfinite((float)eps)) Py_RETURN_NONE;
+    return gradients(a[0], a[2], a[3], a[5], 1, (float)max_norm, (float)eps);
+}
+
 /* tensor type, error type, function of the current device, of its current stream, the types in the order
  * above, the addresses of the library's functions in the order above */
 static PyObject* bind(PyObject* self, PyObject* args) {
-    PyObject *t, *e, *d, *s, *ty[TYPES];
-    unsigned long long f[8];
-    if (!PyArg_ParseTuple(args, "OOOO(OOOOOO)(KKKKKKKK)", &t, &e, &d, &s, &ty[0], &ty[1], &ty[2], &ty[3], &ty[4], &ty[5], &f[0], &f[1],
-                          &f[2], &f[3], &f[4], &f[5], &f[6], &f[7]))
+    void** const functions[] = {(void**)&call_route, (void**)&call_route_backward, (void**)&call_plan_workspace, (void**)&call_plan,
+                                (void**)&call_dispatch, (void**)&call_combine, (void**)&call_combine_backward, (void**)&call_product,
+                                (void**)&call_norm, (void**)&call_norm_rhs, (void**)&call_norm_workspace, (void**)&call_norm_backward,
+                                (void**)&call_swiglu, (void**)&call_swiglu_dual, (void**)&call_swiglu_backward, (void**)&call_swiglu_backward_dual,
+                                (void**)&call_rows_i8, (void**)&call_gemm_i8, (void**)&call_grad_workspace, (void**)&call_grad_norm,
+                                (void**)&call_clip};
+    const Py_ssize_t count = (Py_ssize_t)(sizeof(functions) / sizeof(functions[0]));
+    PyObject *t, *e, *d, *s, *ty, *f;
+    if (!PyArg_ParseTuple(args, "OOOOO!O!", &t, &e, &d, &s, &PyTuple_Type, &ty, &PyTuple_Type, &f)) return NULL;
+    if (PyTuple_GET_SIZE(ty) != TYPES || PyTuple_GET_SIZE(f) != count) {
+        PyErr_SetString(PyExc_ValueError, "another number of types or functions");
         return NULL;
+    }
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        *functions[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(f, i));
+        if (PyErr_Occurred()) return NULL;
+    }
     Py_INCREF(t), Py_INCREF(e), Py_INCREF(d), Py_INCREF(s);
     tensor_type = t, error_type = e, get_device = d, get_stream = s;
     for (int i = 0; i < TYPES; ++i) {
-        Py_INCREF(ty[i]);
-        types[i] = ty[i];
+        types[i] = PyTuple_GET_ITEM(ty, i);
+        Py_INCREF(types[i]);
     }
-    call_route = (__typeof__(call_route))(uintptr_t)f[0];
-    call_route_backward = (__typeof__(call_route_backward))(uintptr_t)f[1];
-    call_plan_workspace = (__typeof__(call_plan_workspace))(uintptr_t)f[2];
-    call_plan = (__typeof__(call_plan))(uintptr_t)f[3];
-    call_dispatch = (__typeof__(call_dispatch))(uintptr_t)f[4];
-    call_combine = (__typeof__(call_combine))(uintptr_t)f[5];
-    call_combine_backward = (__typeof__(call_combine_backward))(uintptr_t)f[6];
-    call_product = (__typeof__(call_product))(uintptr_t)f[7];
     Py_RETURN_NONE;
 }
 
@@ -393,6 +756,17 @@ static PyMethodDef methods[] = {
     FAST("moe_combine", combine),
     FAST("moe_combine_backward", combine_backward),
     FAST("gemm_1x128_128x128_routed", product),
+    FAST("rms_norm_quantize", norm),
+    FAST("rms_norm_quantize_rhs", norm_rhs),
+    FAST("rms_norm_backward", norm_backward),
+    FAST("swiglu_quantize", swiglu),
+    FAST("swiglu_quantize_lhs_and_rhs", swiglu_dual),
+    FAST("swiglu_backward", swiglu_back),
+    FAST("swiglu_backward_quantize", swiglu_back_dual),
+    FAST("quantize_rows_i8", rows_i8),
+    FAST("gemm_i8", i8_product),
+    FAST("grad_norm", norm_of_many),
+    FAST("clip_grads", clip_many),
     {NULL, NULL, 0, NULL},
 };
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
@@ -402,6 +776,7 @@ PyMODINIT_FUNC PyInit__calls(void) {
     if ((n_dtype = PyUnicode_InternFromString("dtype")) == NULL || (n_shape = PyUnicode_InternFromString("shape")) == NULL ||
         (n_stride = PyUnicode_InternFromString("stride")) == NULL || (n_get_device = PyUnicode_InternFromString("get_device")) == NULL ||
         (n_data_ptr = PyUnicode_InternFromString("data_ptr")) == NULL || (n_new_empty = PyUnicode_InternFromString("new_empty")) == NULL ||
+        (n_numel = PyUnicode_InternFromString("numel")) == NULL || (n_is_contiguous = PyUnicode_InternFromString("is_contiguous")) == NULL ||
         (only = PyTuple_Pack(1, n_dtype)) == NULL)
         return NULL;
     n_dtype_only = only;
