@@ -391,6 +391,12 @@ int64_t grad_partials(const int64_t* sizes, int64_t count) {
     return partials + (in_launch > 0 ? bsfp8::sched::grad_blocks(units) : 0);
 }
 
+double grad_bytes(const int64_t* sizes, const int* dtypes, int64_t count) {
+    double bytes = 0;
+    for (int64_t i = 0; i < count; ++i) bytes += static_cast<double>(sizes[i]) * (dtypes[i] == BSFP8_F32 ? 4 : 2);
+    return bytes;
+}
+
 // No output shares memory with another tensor of the call, but with its own gradient as a whole.
 bool outputs_apart(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, const int* out_dtypes,
                    int64_t count) {
@@ -878,8 +884,9 @@ int grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes,
     if (int rc = check_device()) return rc;
     double* partial = static_cast<double*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool past = bsfp8::sched::grads_past_caches(grad_bytes(sizes, dtypes, count));
     const hipError_t e = for_grad_tables(grads, nullptr, sizes, dtypes, nullptr, count, [&](const bsfp8::GradTable& t, int64_t before) {
-        return bsfp8::launch_grad_squares(t, partial + before, st);
+        return bsfp8::launch_grad_squares(t, past, partial + before, st);
     });
     if (e != hipSuccess) return BSFP8_EHIP;
     return finish(bsfp8::launch_grad_norm(partial, grad_partials(sizes, count), norm, st));
@@ -904,13 +911,14 @@ int clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t partials = grad_partials(sizes, count);
     if (partials == 0) return finish(bsfp8::launch_grad_norm(partial, 0, norm, st));
+    const bool past = bsfp8::sched::grads_past_caches(grad_bytes(sizes, dtypes, count) + grad_bytes(sizes, out_dtypes, count));
     hipError_t e = for_grad_tables(grads, outs, sizes, dtypes, out_dtypes, count, [&](const bsfp8::GradTable& t, int64_t before) {
-        return bsfp8::launch_grad_squares(t, partial + before, st);
+        return bsfp8::launch_grad_squares(t, past, partial + before, st);
     });
     if (e != hipSuccess) return BSFP8_EHIP;
     // the first launch of the clipped copies writes the norm
     return finish(for_grad_tables(grads, outs, sizes, dtypes, out_dtypes, count, [&](const bsfp8::GradTable& t, int64_t before) {
-        return bsfp8::launch_grad_clip(t, partial, partials, max_norm, eps, before == 0 ? norm : nullptr, st);
+        return bsfp8::launch_grad_clip(t, past, partial, partials, max_norm, eps, before == 0 ? norm : nullptr, st);
     }));
 }
 

@@ -207,10 +207,11 @@ struct GradTable {
     int count;
 };
 static_assert(sizeof(GradTable) <= 3800, "kernel arguments fit 4 KB");
-hipError_t launch_grad_squares(const GradTable& t, double* partial, hipStream_t stream);
+// past: past the caches (sched::grads_past_caches)
+hipError_t launch_grad_squares(const GradTable& t, bool past, double* partial, hipStream_t stream);
 hipError_t launch_grad_norm(const double* partial, int64_t count, float* norm, hipStream_t stream);
 // norm: nullptr where another launch of the call writes it
-hipError_t launch_grad_clip(const GradTable& t, const double* partial, int64_t count, float max_norm, float eps, float* norm,
+hipError_t launch_grad_clip(const GradTable& t, bool past, const double* partial, int64_t count, float max_norm, float eps, float* norm,
                             hipStream_t stream);
 
 }  // namespace bsfp8

@@ -37,8 +37,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a, RowCodes out
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int64_t c = 8 * (static_cast<int64_t>(i) * TPR + tid), at = c < a.H ? c : 0;
-        xw[i] = *reinterpret_cast<const rc_u32x4*>(a.x + row * a.ldx + at);
-        if (RES != kResNone) load8_of<RES == kResF32>(a.residual, row * a.ldr + at, h[i]);
+        xw[i] = load_piece<true>(reinterpret_cast<const rc_u32x4*>(a.x + row * a.ldx + at));
+        if (RES != kResNone) load8_of<RES == kResF32, true>(a.residual, row * a.ldr + at, h[i]);
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -242,15 +242,22 @@ __global__ __launch_bounds__(kThreads) void norm_backward_any_kernel(NormBackwar
     }
 }
 
-// dw[c] = the sum of the G parts of column c: 32 columns a workgroup, 32 runs of parts side by side.
-constexpr int kSumCols = 32, kSumRuns = 32;
+// dw[c] = the sum of the G parts of column c: 16 columns a workgroup, 64 runs of parts side by side.
+constexpr int kSumCols = 16, kSumRuns = 64, kSumEach = 8;
 __global__ __launch_bounds__(kSumCols* kSumRuns) void norm_weight_kernel(const float* partial, int64_t G, int64_t H, void* dweight, bool w_f32) {
     __shared__ float part[kSumRuns][kSumCols + 1];
     const int col = threadIdx.x % kSumCols, run = threadIdx.x / kSumCols;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumCols + col;
-    float sum = 0.0f;
-    if (c < H)
-        for (int64_t g = run; g < G; g += kSumRuns) sum += partial[g * H + c];
+    static_assert(sched::kNormBackwardBlocks == kSumRuns * kSumEach, "a run's parts are on the way together");
+    float v[kSumEach];
+#pragma unroll
+    for (int k = 0; k < kSumEach; ++k) {
+        const int64_t g = run + k * kSumRuns;
+        v[k] = g < G && c < H ? partial[g * H + c] : 0.0f;
+    }
+    float sum = v[0];
+#pragma unroll
+    for (int k = 1; k < kSumEach; ++k) sum += v[k];
     part[run][col] = sum;
     __syncthreads();
     if (run != 0 || c >= H) return;

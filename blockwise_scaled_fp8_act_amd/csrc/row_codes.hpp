@@ -132,7 +132,8 @@ __device__ __forceinline__ uint32_t block_umax(uint32_t v, uint32_t* part) {
     return top;
 }
 
-// Eight consecutive bf16 or fp32 from a 16-byte aligned address.
+// Eight consecutive bf16 or fp32 from a 16-byte aligned address. ONCE: nothing here reads them again, so they
+// are not kept in the caches (the norm with an fp32 residual, 8192 x 4096: 80 -> 75 us).
 __device__ __forceinline__ void unpack8(rc_u32x4 w, float (&f)[8]) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -140,18 +141,22 @@ __device__ __forceinline__ void unpack8(rc_u32x4 w, float (&f)[8]) {
         f[2 * d + 1] = bf16_hi(w[d]);
     }
 }
-template <bool F32>
+template <bool ONCE, typename V>
+__device__ __forceinline__ V load_piece(const V* p) {
+    return ONCE ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool F32, bool ONCE = false>
 __device__ __forceinline__ void load8_of(const void* p, int64_t at, float (&f)[8]) {
     if constexpr (F32) {
         const rc_f32x4* q = reinterpret_cast<const rc_f32x4*>(static_cast<const float*>(p) + at);
-        const rc_f32x4 lo = q[0], hi = q[1];
+        const rc_f32x4 lo = load_piece<ONCE>(q), hi = load_piece<ONCE>(q + 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[j] = lo[j];
             f[4 + j] = hi[j];
         }
     } else {
-        unpack8(*reinterpret_cast<const rc_u32x4*>(static_cast<const uint16_t*>(p) + at), f);
+        unpack8(load_piece<ONCE>(reinterpret_cast<const rc_u32x4*>(static_cast<const uint16_t*>(p) + at)), f);
     }
 }
 __device__ __forceinline__ float load_of(const void* p, int64_t at, bool f32) {

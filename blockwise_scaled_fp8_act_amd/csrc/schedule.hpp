@@ -309,11 +309,16 @@ inline bool routed_reads_once(int64_t M, int64_t N, int64_t E, bool swiglu) {
 constexpr int64_t kRowWaveMax = 1024, kRowMax = 16384;
 
 // Workgroups of the norm's gradient, each with its own part of the weight's gradient.
-inline int64_t norm_backward_blocks(int64_t T) { return T < 512 ? T : 512; }
+constexpr int64_t kNormBackwardBlocks = 512;
+inline int64_t norm_backward_blocks(int64_t T) { return T < kNormBackwardBlocks ? T : kNormBackwardBlocks; }
 
 // Gradients of many tensors: units of kGradUnit values, dealt in consecutive runs to at most kGradBlocks
 // workgroups of a launch.
 constexpr int64_t kGradUnit = 8192, kGradBlocks = 512;
+// Whether a call's tensors, with the clipped copies, are more than the 256 MB last-level cache can hold: then
+// they go past it (grads.hip has both sides' times); fewer are read from it in the second pass, and by what
+// takes the copies.
+inline bool grads_past_caches(double bytes) { return bytes > 200e6; }
 inline int64_t grad_blocks(int64_t units) { return units < kGradBlocks ? units : kGradBlocks; }
 
 // gemm_i8: the kernel of M x N x K. A tile kernel's time goes by rounds: its tiles over the compute units, one or

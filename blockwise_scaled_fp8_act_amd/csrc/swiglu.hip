@@ -12,11 +12,9 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 
-// exp(x) for x <= 0: x log2(e) in two parts, since rounding the product alone costs |x| 2^-24. Below -200
-// it is 0 (and 0 for NaN: every use multiplies by the gate itself, too).
-__device__ __forceinline__ float exp_neg(float x) {
-    x = fmaxf(x, -200.0f);
-    const float hi = x * 1.44269504f, lo = fmaf(x, 1.44269504f, -hi) + x * 1.92596e-8f;
+// exp(x): x log2(e) in two parts, since rounding the product alone costs |x| 2^-24.
+__device__ __forceinline__ float exp_of(float x) {
+    const float hi = x * 1.44269504f, lo = fmaf(x, 1.92596e-8f, fmaf(x, 1.44269504f, -hi));
     const float e = __builtin_amdgcn_exp2f(hi);
     return fmaf(e * 0.693147181f, lo, e);
 }
@@ -27,36 +25,55 @@ __device__ __forceinline__ float reciprocal(float d) {
     return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
-// sig(g) and 1 - sig(g), each without cancellation.
-struct Sig {
-    float s, rest;
-};
-__device__ __forceinline__ Sig sigmoid(float g) {
-    const float t = exp_neg(-fabsf(g)), near = reciprocal(1.0f + t), far = t * near;
-    return g >= 0.0f ? Sig{near, far} : Sig{far, near};
-}
-
-// From g = -80 on exp(g) leaves fp32's ordinary range while g sig(g) u need not (u is as large as 3e38):
-// there sig(g) = exp(g) to 2^-115, taken in 64 bits from the fourth power of exp(g / 4).
-constexpr float kFar = -80.0f;
+// Where |g| <= 80 nothing leaves fp32's ordinary range: with t = exp(-g), sig = 1 / (1 + t) and
+// 1 - sig = t sig, neither with cancellation. Beyond, sig is 1 to fp32, or exp(g) to 2^-115: that leaves
+// fp32's ordinary range while g sig u need not (u is as large as 3e38), so it is taken in 64 bits, from the
+// fourth power of exp(g / 4). Eight values share the test for it.
+constexpr float kFar = 80.0f;
 __device__ __forceinline__ float far_product(float a, float b, float c, float g) {
-    double e = exp_neg(0.25f * g);
+    double e = exp_of(0.25f * fmaxf(g, -800.0f));
     e *= e;
     return static_cast<float>(static_cast<double>(a) * b * c * (e * e));
 }
-
-__device__ __forceinline__ float swiglu(float g, float u) {
-    float v = (g * sigmoid(g).s) * u;
-    if (__builtin_expect(g < kFar, 0)) v = far_product(g, u, 1.0f, g);
-    return v;
+__device__ __forceinline__ bool any_far(const float (&g)[8]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(g[j]));
+    return top > kFar;
 }
-__device__ __forceinline__ void swiglu_grad(float dy, float g, float u, float& dg, float& du) {
-    const Sig s = sigmoid(g);
-    dg = (u * (s.s * fmaf(g, s.rest, 1.0f))) * dy;
-    du = (g * s.s) * dy;
-    if (__builtin_expect(g < kFar, 0)) {
-        dg = far_product(1.0f + g, u, dy, g);
-        du = far_product(g, dy, 1.0f, g);
+
+// v = g sig(g) u
+__device__ __forceinline__ void swiglu8(const float (&g)[8], const float (&u)[8], float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (g[j] * reciprocal(1.0f + exp_of(-g[j]))) * u[j];
+    if (__builtin_expect(any_far(g), 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (fabsf(g[j]) > kFar) v[j] = g[j] > 0.0f ? g[j] * u[j] : far_product(g[j], u[j], 1.0f, g[j]);
+    }
+}
+__device__ __forceinline__ float swiglu(float g, float u) {
+    const float g8[8] = {g}, u8[8] = {u};
+    float v[8];
+    swiglu8(g8, u8, v);
+    return v[0];
+}
+
+// dg = dy u sig (1 + g (1 - sig)), du = dy g sig
+__device__ __forceinline__ void swiglu_grad8(const float (&dy)[8], const float (&g)[8], const float (&u)[8], float (&dg)[8], float (&du)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float t = exp_of(-g[j]), sig = reciprocal(1.0f + t);
+        dg[j] = (u[j] * (sig * fmaf(g[j], t * sig, 1.0f))) * dy[j];
+        du[j] = (g[j] * sig) * dy[j];
+    }
+    if (__builtin_expect(any_far(g), 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (fabsf(g[j]) > kFar) {
+                dg[j] = g[j] > 0.0f ? u[j] * dy[j] : far_product(1.0f + g[j], u[j], dy[j], g[j]);
+                du[j] = g[j] > 0.0f ? g[j] * dy[j] : far_product(g[j], dy[j], 1.0f, g[j]);
+            }
     }
 }
 
@@ -81,8 +98,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const uint16_t* gu, in
         float gf[8], uf[8];
         unpack8(g[i], gf);
         unpack8(u[i], uf);
+        swiglu8(gf, uf, v[i]);
+        if (!in)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = in ? swiglu(gf[j], uf[j]) : 0.0f;
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     }
     emit_row<TPR, NC>(out, row, T, F, tid, v, part_max);
 }
@@ -95,11 +114,11 @@ __global__ __launch_bounds__(kThreads) void swiglu_any_kernel(const uint16_t* gu
 }
 
 // Eight columns of a row of a [*, ld] bf16 tensor; zero outside.
-template <bool VEC>
+template <bool VEC, bool ONCE = false>
 __device__ __forceinline__ void load_cols(const uint16_t* p, int64_t ld, int64_t row, int64_t T, int64_t c, int64_t C, float (&f)[8]) {
     const bool in = row < T;
     if (VEC) {
-        load8_of<false>(p, in && c < C ? row * ld + c : 0, f);
+        load8_of<false, ONCE>(p, in && c < C ? row * ld + c : 0, f);
         if (!(in && c < C))
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = 0.0f;
@@ -122,9 +141,12 @@ __global__ __launch_bounds__(kTileThreads) void swiglu_dual_kernel(const uint16_
         load_cols<VEC>(gu + F, ldgu, row + i, T, c, F, u[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i)
+    for (int i = 0; i < kTileRows; ++i) {
+        float w[8];
+        swiglu8(v[i], u[i], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = swiglu(v[i][j], u[i][j]);
+        for (int j = 0; j < 8; ++j) v[i][j] = w[j];
+    }
     emit_tile<FNUZ, true, VEC, VEC>(out, r0, c0, T, F, v, lds);
 }
 
@@ -138,18 +160,21 @@ __global__ __launch_bounds__(kTileThreads) void swiglu_backward_dual_kernel(cons
     const int64_t row = r0 + (t >> 4) * kTileRows, c = c0 + (t & 15) * 8;
     float v[kTileRows][8];
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i)
+    for (int i = 0; i < kTileRows; ++i) {
+        float d[8], g[8], u[8], dg[8], du[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t at = c + j;
-            v[i][j] = 0.0f;
-            if (row + i >= T || at >= 2 * F) continue;
-            const int64_t f = at < F ? at : at - F;
+            const int64_t at = c + j, f = at < F ? at : at - F;
+            const bool in = row + i < T && at < 2 * F;
             const uint16_t* p = gu + (row + i) * ldgu + f;
-            float dg, du;
-            swiglu_grad(bf16_to_f32(dy[(row + i) * lddy + f]), bf16_to_f32(p[0]), bf16_to_f32(p[F]), dg, du);
-            v[i][j] = at < F ? dg : du;
+            d[j] = in ? bf16_to_f32(dy[(row + i) * lddy + f]) : 0.0f;
+            g[j] = in ? bf16_to_f32(p[0]) : 0.0f;
+            u[j] = in ? bf16_to_f32(p[F]) : 0.0f;
         }
+        swiglu_grad8(d, g, u, dg, du);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = c + j < F ? dg[j] : du[j];
+    }
     emit_tile<FNUZ, true, false, false>(out, r0, c0, T, 2 * F, v, lds);
 }
 
@@ -168,11 +193,10 @@ __global__ __launch_bounds__(kTileThreads) void swiglu_backward_tiles_kernel(con
         load_cols<true>(dy, lddy, row + i, T, c, F, d);
         load_cols<true>(gu, ldgu, row + i, T, c, F, g);
         load_cols<true>(gu + F, ldgu, row + i, T, c, F, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) swiglu_grad(d[j], g[j], u[j], dg[i][j], du[i][j]);
+        swiglu_grad8(d, g, u, dg[i], du[i]);
     }
     emit_tile<FNUZ, true, true, true>(out, r0, c0, T, 2 * F, dg, lds);
-    emit_tile<FNUZ, true, true, true>(out, r0, c0 + F, T, 2 * F, du, lds);
+    emit_tile<FNUZ, true, true, true, true>(out, r0, c0 + F, T, 2 * F, du, lds);
 }
 
 template <bool VEC>
@@ -185,8 +209,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const uint16_
     load_cols<VEC>(dy, lddy, row, T, c, F, d);
     load_cols<VEC>(gu, ldgu, row, T, c, F, g);
     load_cols<VEC>(gu + F, ldgu, row, T, c, F, u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) swiglu_grad(d[j], g[j], u[j], dg[j], du[j]);
+    swiglu_grad8(d, g, u, dg, du);
     uint16_t* p = dgu + row * lddgu + c;
     if (VEC) {
         store8_of<false>(p, 0, dg);

@@ -10,17 +10,25 @@ namespace bsfp8 {
 constexpr int kTileThreads = 512;
 constexpr int kTileRows = 4;  // a thread's consecutive rows, of 8 columns: 16 lanes make a row of the tile
 
-// The transposed code tile and, before it, the column maxima of the 32 row groups.
+// The transposed code tile and, before it in the same place, the column maxima of the 32 row groups.
 struct TileLds {
-    uint4 tile[kGroup * 8];  // [column][8 chunks of 16 rows], the chunk swizzled by the column's eights
-    uint32_t red[32][kGroup + 1];
+    union {
+        uint4 tile[kGroup * 8];  // [column][8 chunks of 16 rows], the chunk swizzled by the column's eights
+        uint32_t red[32][kGroup + 1];
+    };
     float mult[kGroup];
 };
 
+// The value of lane l of the 16 lanes of a DPP row, in all of them.
+template <int L>
+__device__ __forceinline__ float row16_lane(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + L, 0xF, 0xF, false));
+}
+
 // v[i][j]: row r0 + 4 (t / 16) + i, column c0 + 8 (t % 16) + j; zero outside the [T, C] tensor. VEC_Q: code
 // rows 8-byte aligned and C a multiple of 8; VEC_T: rows of qT 16-byte aligned and T a multiple of 16.
-// Every thread of the workgroup calls it; it may be called again at once.
-template <bool FNUZ, bool ROWS, bool VEC_Q, bool VEC_T>
+// Every thread of the workgroup calls it, with AGAIN for a second tile through the same LDS.
+template <bool FNUZ, bool ROWS, bool VEC_Q, bool VEC_T, bool AGAIN = false>
 __device__ __forceinline__ void emit_tile(const TileCodes& out, int64_t r0, int64_t c0, int64_t T, int64_t C, const float (&v)[kTileRows][8],
                                           TileLds& lds) {
     const int t = threadIdx.x, cg = t & 15, rg = t >> 4;
@@ -28,21 +36,34 @@ __device__ __forceinline__ void emit_tile(const TileCodes& out, int64_t r0, int6
     const auto encode = [](float a, float b, float d, float e) { return encode4_in_range<FNUZ>(a, b, d, e); };
 
     // column maxima of this thread's rows, then of all in LDS
+    if (AGAIN) __syncthreads();  // every thread has read the tile before
+    uint32_t mag[kTileRows][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t am = 0;
+    for (int i = 0; i < kTileRows; ++i)
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) am = max(am, abs_bits(v[i][j]));
-        lds.red[rg][cg * 8 + j] = am;
-    }
+        for (int j = 0; j < 8; ++j) mag[i][j] = abs_bits(v[i][j]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) lds.red[rg][cg * 8 + j] = max(max(mag[0][j], mag[1][j]), max(mag[2][j], mag[3][j]));
     if (ROWS) {
+        // lane l of a row's 16 forms the scale pair of row l % 4 (two divisions), and all take each row's
+        uint32_t mine = 0;
 #pragma unroll
         for (int i = 0; i < kTileRows; ++i) {
-            const GroupScale g = fp8_scale<FNUZ>(umax_row16(amax8(v[i])));
+            uint32_t am = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) am = max(am, mag[i][j]);
+            am = umax_row16(am);
+            mine = (cg & 3) == i ? am : mine;
+        }
+        const GroupScale own = fp8_scale<FNUZ>(mine);
+        const GroupScale g[kTileRows] = {{row16_lane<0>(own.s), row16_lane<0>(own.m)}, {row16_lane<1>(own.s), row16_lane<1>(own.m)},
+                                         {row16_lane<2>(own.s), row16_lane<2>(own.m)}, {row16_lane<3>(own.s), row16_lane<3>(own.m)}};
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) {
             const int64_t r = r0 + rg * kTileRows + i;
             if (r >= T) continue;
-            const uint32_t w0 = encode(v[i][0] * g.m, v[i][1] * g.m, v[i][2] * g.m, v[i][3] * g.m);
-            const uint32_t w1 = encode(v[i][4] * g.m, v[i][5] * g.m, v[i][6] * g.m, v[i][7] * g.m);
+            const uint32_t w0 = encode(v[i][0] * g[i].m, v[i][1] * g[i].m, v[i][2] * g[i].m, v[i][3] * g[i].m);
+            const uint32_t w1 = encode(v[i][4] * g[i].m, v[i][5] * g[i].m, v[i][6] * g[i].m, v[i][7] * g[i].m);
             uint8_t* q = out.q + r * out.ldq + c;
             if (VEC_Q) {
                 if (c < C) *reinterpret_cast<uint2*>(q) = make_uint2(w0, w1);
@@ -51,7 +72,7 @@ __device__ __forceinline__ void emit_tile(const TileCodes& out, int64_t r0, int6
                 for (int j = 0; j < 8; ++j)
                     if (c + j < C) q[j] = static_cast<uint8_t>((j < 4 ? w0 : w1) >> (8 * (j & 3)));
             }
-            if (cg == 0) out.a_s[c0 / kGroup * T + r] = g.s;
+            if (cg == 0) out.a_s[c0 / kGroup * T + r] = g[i].s;
         }
     }
     __syncthreads();
@@ -91,8 +112,6 @@ __device__ __forceinline__ void emit_tile(const TileCodes& out, int64_t r0, int6
                 if (r + j < T) q[j] = static_cast<uint8_t>(d[j >> 2] >> (8 * (j & 3)));
         }
     }
-    // the next call's maxima go into lds.red, which every thread has read before the last barrier; its
-    // multipliers and codes come behind a barrier that follows the reads above
 }
 
 }  // namespace bsfp8
