@@ -6,8 +6,9 @@ bf16 to float8_e4m3fn (or float8_e4m3fnuz, ``fmt="e4m3fnuz"``) with fp32 scales,
 behind the C ABI of include/blockwise_fp8.h. This package is the thin Python binding over that
 library (``binding``), the blockwise-FP8 linear layer composed from those kernels for training
 (``linear``), the gated mixture-of-experts layer for training and serving composed from the routing,
-dispatch, expert-product and combine kernels (``moe``), its in-tree build (``build``) and the seeded
-input generators (``inputs``).
+dispatch, expert-product and combine kernels (``moe``), the gated feed-forward layer with its norm, in FP8
+for training and in int8 for serving, and gradient clipping (``ffn``), its in-tree build (``build``) and the
+seeded input generators (``inputs``).
 """
 from .binding import (  # noqa: F401
     Bsfp8Error,
@@ -47,5 +48,6 @@ from .binding import (  # noqa: F401
     swiglu_quantize,
     swiglu_quantize_lhs_and_rhs,
 )
+from .ffn import BlockwiseFp8FeedForward, ServingInt8FeedForward, blockwise_fp8_feed_forward, clip_grad_norm_  # noqa: F401
 from .linear import BlockwiseFp8Linear, blockwise_fp8_linear  # noqa: F401
 from .moe import BlockwiseFp8MoE, ServingMoE, blockwise_fp8_moe, route_experts  # noqa: F401
