@@ -68,6 +68,9 @@ __device__ __forceinline__ int64_t tile_bytes(int64_t rows, int64_t ld, int64_t 
 // 2^31), so its loads write zeros to LDS and the count of loads under way stays the same.
 constexpr uint32_t kPastEnd = 0x80000000u;
 
+// The block of K with which the workgroups of an XCD begin, of Kb.
+__device__ __forceinline__ int first_block(int Kb) { return static_cast<int>(blockIdx.x % geom::kXcds) * Kb / geom::kXcds; }
+
 // Zeroes the bytes of a lane's 16 that lie at or past `left`.
 __device__ __forceinline__ void keep_bytes(i32x4& v, int left) {
 #pragma unroll
@@ -105,9 +108,13 @@ __device__ __forceinline__ void store4(const I8Args& g, int64_t m, int64_t n, ui
 // ahead of the products. A row of a stage has its 16-byte chunks swizzled by the row, so that the 16 rows of a
 // fragment's read fall on all banks: chunk c at c ^ swizzle(row). One barrier a block. With few workgroups a
 // block's time is one wait, barrier and chain of reads and products, so blocks are long (256 bytes) for the
-// small tiles; with two workgroups on a CU each hides the other's waits. PAST: B is read past the caches,
-// for weights that are read once and by so many workgroups that HBM is the bound (14336 x 4096, 16 rows: 14.4
-// us through the caches, 12.7 past them).
+// small tiles; with two workgroups on a CU each hides the other's waits.
+// The blocks of K come in an order that begins elsewhere for other workgroups (the sum is whole, so any order gives
+// the same bits): rows lie a multiple of a KB apart, so workgroups that all read one block at a time reach only
+// an eighth or fewer of HBM's channels. PAST, for weights that are read once and by so many workgroups that
+// HBM is the bound: every column of tiles begins with another block, and B is read past the caches (16 rows by
+// 14336 x 4096 14.7 us without both, 13.2 with the second, 11.5 with both, 5.1 TB/s). Else the workgroups of an
+// XCD, which share rows in its L2, begin together (512 x 5120 x 5120 in 64 x 128 tiles 39.8 -> 36.3 us).
 template <int BM, int BN, int WM, int WN, int STAGES, int KS, bool PAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args g, int mt, int nt, int c_vec) {
     constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kMS = WM / 16, kNS = WN / 16;
@@ -127,6 +134,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b + n0 * g.ldb, tile_bytes(min(g.N - n0, int64_t{BN}), g.ldb, g.K));
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)));
     const int Kb = static_cast<int>((g.K + KS - 1) / KS);
+    const int start = PAST ? tn % max(Kb, 1) : first_block(Kb);
+    const auto block = [&](int i) { return i + start < Kb ? i + start : i + start - Kb; };  // the i-th
 
     // load p of a wave: kRows rows of A, or of B behind them
     uint32_t off[kLoads];
@@ -137,8 +146,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
         const int row = kRows * (is_a ? r : r - BM / kRows) + lane / kChunks;
         off[p] = static_cast<uint32_t>(row * (is_a ? g.lda : g.ldb)) + 16 * ((lane % kChunks) ^ swizzle(row));
     }
-    const auto issue = [&](int kb, int stage) {
-        const uint32_t k = kb < Kb ? static_cast<uint32_t>(kb * KS) : kPastEnd;
+    const auto issue = [&](int i, int stage) {
+        const uint32_t k = i < Kb ? static_cast<uint32_t>(block(i) * KS) : kPastEnd;
 #pragma unroll
         for (int p = 0; p < kLoads; ++p) {
             const int r = wave * kLoads + p;
@@ -159,10 +168,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
     }
     const int sw = swizzle(l16);
     int stage = 0;
-    for (int kb = 0; kb < Kb; ++kb) {
+    for (int n = 0; n < Kb; ++n) {
         wait_loads<(STAGES - 2) * kLoads>();
-        lds_barrier();  // block kb is there, and no wave reads the stage before it any more
-        issue(kb + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+        lds_barrier();  // the n-th block is there, and no wave reads the stage before it any more
+        issue(n + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
         const u32x4* st = smem + stage * kStage;
         i32x4 a[KS / 64][kMS], b[KS / 64][kNS];
 #pragma unroll
@@ -173,7 +182,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
 #pragma unroll
             for (int j = 0; j < kNS; ++j) b[h][j] = __builtin_bit_cast(i32x4, st[(BM + WN * wn + 16 * j + l16) * kChunks + pos]);
         }
-        const int64_t keep = g.K - static_cast<int64_t>(kb) * KS;
+        const int64_t keep = g.K - static_cast<int64_t>(block(n)) * KS;
         if (keep < KS) {
 #pragma unroll
             for (int h = 0; h < KS / 64; ++h)
@@ -206,8 +215,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
 // ---- 256 x 256 tiles, eight waves of 64 x 128 (two a SIMD), two stages of 128 bytes of K. A wave reads the
 // fragments of half a block (64 bytes) while it multiplies the half before, and the one barrier a block comes
 // after its first half: by then every wave has read the whole stage, so the loads of the block after next go
-// there, a block's time before they are needed. 16384 x 5120 x 5120 383 us, 2.24 Pop/s (400 us with reads and
-// products of a block in turn); 8192^3 437 us, 2.51. Bound by power: the same loop over zeros takes 402. Not
+// there, a block's time before they are needed. 16384 x 5120 x 5120 381 us, 2.25 Pop/s (400 us with reads and
+// products of a block in turn); 4096^3 65 us (67 with all workgroups beginning at one block); 8192^3 437 us, 2.51. Bound by power: the same loop over zeros takes 402. Not
 // better: 32 x 32 x 32 instructions (488), a ring of five half blocks (473, in 6% fewer cycles at a lower
 // clock), four waves of 128 x 128 (550).
 constexpr int kBig = 256;
@@ -222,7 +231,9 @@ __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, i
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a + m0 * g.lda, tile_bytes(min(g.M - m0, int64_t{kBig}), g.lda, g.K));
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b + n0 * g.ldb, tile_bytes(min(g.N - n0, int64_t{kBig}), g.ldb, g.K));
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)));
-    const int Kb = static_cast<int>((g.K + kGroup - 1) / kGroup);
+    // the whole blocks, from first_block on and around, then the partial one
+    const int Kb = static_cast<int>((g.K + kGroup - 1) / kGroup), whole = static_cast<int>(g.K / kGroup), start = first_block(whole);
+    const auto block = [&](int i) { return i >= whole ? i : i + start < whole ? i + start : i + start - whole; };
 
     // a wave loads 32 rows of A and 32 of B a block, 8 a load; the chunk differs between even and odd loads
     uint32_t offa[2], offb[2];
@@ -232,8 +243,8 @@ __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, i
         offb[q] = static_cast<uint32_t>((32 * wave + 8 * q + (lane >> 3)) * g.ldb) + 16 * geom::fast_operand_chunk(q, lane);
     }
     const uint32_t stepa = static_cast<uint32_t>(16 * g.lda), stepb = static_cast<uint32_t>(16 * g.ldb);
-    const auto issue = [&](int kb, int stage) {
-        const uint32_t k = static_cast<uint32_t>(kb * kGroup), to = lds0 + static_cast<uint32_t>(stage * kStage + 256 * wave) * 16;
+    const auto issue = [&](int i, int stage) {
+        const uint32_t k = static_cast<uint32_t>(block(i) * kGroup), to = lds0 + static_cast<uint32_t>(stage * kStage + 256 * wave) * 16;
 #pragma unroll
         for (int p = 0; p < 4; ++p) dma16(to + p * 1024, ra, offa[p & 1] + (p >> 1) * stepa + k);
 #pragma unroll
@@ -279,7 +290,7 @@ __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, i
         lds_barrier();
         if (Kb > 1) issue(1, 1);
         read(0, 0);
-        const int left = static_cast<int>(g.K - static_cast<int64_t>(Kb - 1) * kGroup);  // bytes of the last block
+        const int left = whole < Kb ? static_cast<int>(g.K - static_cast<int64_t>(whole) * kGroup) : kGroup;  // bytes of the last block
         for (int kb = 0; kb < Kb - 1; ++kb) {
             const int s = kb & 1;
             __builtin_amdgcn_sched_barrier(0);
@@ -308,7 +319,7 @@ __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, i
     // each wave's 64 x 128 block goes through LDS, 16-byte chunk c of row r at c ^ (r % 16), so that a store
     // writes whole lines; they are not read again here and go past the caches
     lds_barrier();
-    uint8_t* block = reinterpret_cast<uint8_t*>(smem) + wave * (WM * WN * 2);
+    uint8_t* own = reinterpret_cast<uint8_t*>(smem) + wave * (WM * WN * 2);
 #pragma unroll
     for (int j = 0; j < kNS; ++j) {
         float bs[4];
@@ -318,13 +329,13 @@ __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, i
             const int r = 16 * i + l16;
             const int64_t m = m0 + WM * wm + r;
             const float as = g.K > 0 && m < g.M ? g.a_s[m] : 0.0f;
-            *reinterpret_cast<uint2*>(block + r * 256 + (((2 * j + (lg >> 1)) ^ (r & 15)) * 16) + 8 * (lg & 1)) = scaled4(acc[i][j], as, bs);
+            *reinterpret_cast<uint2*>(own + r * 256 + (((2 * j + (lg >> 1)) ^ (r & 15)) * 16) + 8 * (lg & 1)) = scaled4(acc[i][j], as, bs);
         }
     }
 #pragma unroll
     for (int p = 0; p < WM / 4; ++p) {
         const int r = 4 * p + lg;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(block + r * 256 + ((l16 ^ (r & 15)) * 16));
+        const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * 256 + ((l16 ^ (r & 15)) * 16));
         const int64_t m = m0 + WM * wm + r, n = n0 + WN * wn + 8 * l16;
         if (m >= g.M) continue;
         uint16_t* c = g.c + m * g.ldc + n;
