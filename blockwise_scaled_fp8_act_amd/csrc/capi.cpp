@@ -762,7 +762,7 @@ int rms_norm_quantize(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
     if (residual != nullptr && (ldr < H || ldh < H)) return BSFP8_EINVAL;
     if (int rc = check_device()) return rc;
     const bsfp8::NormArgs a{static_cast<const uint16_t*>(x), ldx, residual, ldr, res_dtype == BSFP8_F32, weight,
-                            w_dtype == BSFP8_F32, eps, h, ldh, rstd, T, H, 0};
+                            w_dtype == BSFP8_F32, eps, h, ldh, rstd, T, H, 0, 0.0};
     const bsfp8::RowCodes out{codes, static_cast<uint8_t*>(q), ldq, s, static_cast<uint16_t*>(y), ldy};
     return finish(bsfp8::launch_rms_norm(a, out, static_cast<hipStream_t>(stream)));
 }

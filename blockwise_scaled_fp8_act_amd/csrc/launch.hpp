@@ -141,7 +141,8 @@ struct NormArgs {
     int64_t ldh;
     float* rstd;  // nullptr: not written
     int64_t T, H;
-    int64_t per_xcd;  // set by the launcher
+    int64_t per_xcd;  // these two are set by the launcher
+    double per_column;
 };
 hipError_t launch_rms_norm(NormArgs a, const RowCodes& out, hipStream_t stream);
 hipError_t launch_rms_norm_rhs(const void* h, bool h_f32, int64_t ldh, const void* weight, bool w_f32, const float* rstd, int64_t T,

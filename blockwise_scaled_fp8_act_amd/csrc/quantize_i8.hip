@@ -1,6 +1,7 @@
 // gfx950 int8 row quantizer: x [T, H] bf16 -> codes with one scale a row (a token's activations, or an
 // output channel's weights): s = max(amax, 1e-12) / 127, q = rint(x * (127 / max(amax, 1e-12))). A row
-// stays in registers between its maximum and its codes; bound by the memory traffic.
+// stays in registers between its maximum and its codes (of up to sched::kRowMax values; longer ones are read
+// twice); bound by the memory traffic.
 #include "row_codes.hpp"
 #include "schedule.hpp"
 
@@ -9,7 +10,8 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 
-template <int TPR, int NC>
+// ANY: rows that begin anywhere, of any length; without it 16-byte pieces (codes 8-byte ones).
+template <int TPR, int NC, bool ANY>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t per_xcd, RowCodes out) {
     __shared__ uint32_t part[kWaves];
     const int tid = threadIdx.x % TPR;
@@ -19,36 +21,27 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const uint16_t* x, int64
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int64_t c = 8 * (static_cast<int64_t>(i) * TPR + tid);
-        load8_of<false>(x, row * ldx + (c < H ? c : 0), v[i]);
-        if (c >= H)
+        load8_of<false, false, ANY>(x, row * ldx + (c < H ? c : 0), v[i], H - c);
+        if (!ANY && c >= H)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     }
-    emit_row<TPR, NC>(out, row, T, H, tid, v, part);
+    emit_row<TPR, NC, ANY>(out, row, T, H, tid, v, part);
 }
 
-__global__ __launch_bounds__(kThreads) void rows_any_kernel(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, RowCodes out) {
+__global__ __launch_bounds__(kThreads) void rows_long_kernel(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, RowCodes out) {
     __shared__ uint32_t part[kWaves];
     const int64_t row = blockIdx.x;
     const uint16_t* p = x + row * ldx;
     emit_row_any<kWaves>(out, row, T, H, [&](int64_t c) { return bf16_to_f32(p[c]); }, part);
 }
 
-}  // namespace
-
-hipError_t launch_quantize_rows_i8(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, uint8_t* q, int64_t ldq, float* s,
-                                   hipStream_t stream) {
-    const RowCodes out{kCodesI8, q, ldq, s, nullptr, 0};
-    const bool vec = H % 8 == 0 && H <= sched::kRowMax && reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0 &&
-                     reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0;
-    if (!vec) {
-        rows_any_kernel<<<static_cast<unsigned>(T), kThreads, 0, stream>>>(x, ldx, T, H, out);
-        return hipGetLastError();
-    }
+template <bool ANY>
+void launch_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, const RowCodes& out, hipStream_t stream) {
     const bool wave = H <= sched::kRowWaveMax;
     const int64_t blocks = wave ? (T + kWaves - 1) / kWaves : T, per_xcd = (blocks + kXcds - 1) / kXcds;
     const unsigned grid = static_cast<unsigned>(per_xcd * kXcds);
-#define BSFP8_ROWS(TPR, NC) rows_kernel<TPR, NC><<<grid, kThreads, 0, stream>>>(x, ldx, T, H, per_xcd, out)
+#define BSFP8_ROWS(TPR, NC) rows_kernel<TPR, NC, ANY><<<grid, kThreads, 0, stream>>>(x, ldx, T, H, per_xcd, out)
     if (wave) {
         if (H <= 512) BSFP8_ROWS(64, 1);
         else BSFP8_ROWS(64, 2);
@@ -63,6 +56,16 @@ hipError_t launch_quantize_rows_i8(const uint16_t* x, int64_t ldx, int64_t T, in
         }
     }
 #undef BSFP8_ROWS
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows_i8(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, uint8_t* q, int64_t ldq, float* s,
+                                   hipStream_t stream) {
+    const RowCodes out{kCodesI8, q, ldq, s, nullptr, 0};
+    if (H > sched::kRowMax) rows_long_kernel<<<static_cast<unsigned>(T), kThreads, 0, stream>>>(x, ldx, T, H, out);
+    else if (H % 8 == 0 && rows16(x, 2 * ldx) && whole_codes(out)) launch_rows<false>(x, ldx, T, H, out, stream);
+    else launch_rows<true>(x, ldx, T, H, out, stream);
     return hipGetLastError();
 }
 

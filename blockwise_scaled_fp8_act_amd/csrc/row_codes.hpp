@@ -132,8 +132,14 @@ __device__ __forceinline__ uint32_t block_umax(uint32_t v, uint32_t* part) {
     return top;
 }
 
-// Eight consecutive bf16 or fp32 from a 16-byte aligned address. ONCE: nothing here reads them again, so they
-// are not kept in the caches (the norm with an fp32 residual, 8192 x 4096: 80 -> 75 us).
+// The same types at any address: loads and stores of these are single instructions too.
+typedef uint32_t rc_u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t rc_u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float rc_f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight consecutive bf16 or fp32. ONCE: nothing here reads them again, so they are not kept in the caches (the
+// norm with an fp32 residual, 8192 x 4096: 80 -> 75 us). ANY: at any address, and of the eight the first n alone (the
+// others are 0, and are not touched); without it all eight are there, 16-byte aligned.
 __device__ __forceinline__ void unpack8(rc_u32x4 w, float (&f)[8]) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -145,46 +151,105 @@ template <bool ONCE, typename V>
 __device__ __forceinline__ V load_piece(const V* p) {
     return ONCE ? __builtin_nontemporal_load(p) : *p;
 }
-template <bool F32, bool ONCE = false>
-__device__ __forceinline__ void load8_of(const void* p, int64_t at, float (&f)[8]) {
-    if constexpr (F32) {
-        const rc_f32x4* q = reinterpret_cast<const rc_f32x4*>(static_cast<const float*>(p) + at);
-        const rc_f32x4 lo = load_piece<ONCE>(q), hi = load_piece<ONCE>(q + 1);
+template <bool ONCE = false, bool ANY = false>
+__device__ __forceinline__ rc_u32x4 load8_bf16(const uint16_t* p, int64_t n = 8) {
+    if (!ANY) return load_piece<ONCE>(reinterpret_cast<const rc_u32x4*>(p));
+    if (n >= 8) return load_piece<ONCE>(reinterpret_cast<const rc_u32x4_any*>(p));
+    rc_u32x4 w = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] = lo[j];
-            f[4 + j] = hi[j];
-        }
+    for (int j = 0; j < 7; ++j)
+        if (j < n) w[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+    return w;
+}
+template <bool F32, bool ONCE = false, bool ANY = false>
+__device__ __forceinline__ void load8_of(const void* p, int64_t at, float (&f)[8], int64_t n = 8) {
+    if constexpr (!F32) {
+        unpack8(load8_bf16<ONCE, ANY>(static_cast<const uint16_t*>(p) + at, n), f);
     } else {
-        unpack8(load_piece<ONCE>(reinterpret_cast<const rc_u32x4*>(static_cast<const uint16_t*>(p) + at)), f);
+        const float* q = static_cast<const float*>(p) + at;
+        if (!ANY || n >= 8) {
+            rc_f32x4 lo, hi;
+            if (ANY) {
+                lo = load_piece<ONCE>(reinterpret_cast<const rc_f32x4_any*>(q));
+                hi = load_piece<ONCE>(reinterpret_cast<const rc_f32x4_any*>(q + 4));
+            } else {
+                lo = load_piece<ONCE>(reinterpret_cast<const rc_f32x4*>(q));
+                hi = load_piece<ONCE>(reinterpret_cast<const rc_f32x4*>(q + 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[j] = lo[j];
+                f[4 + j] = hi[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = j < n ? q[j] : 0.0f;
+        }
     }
 }
 __device__ __forceinline__ float load_of(const void* p, int64_t at, bool f32) {
     return f32 ? static_cast<const float*>(p)[at] : bf16_to_f32(static_cast<const uint16_t*>(p)[at]);
 }
-template <bool F32>
-__device__ __forceinline__ void store8_of(void* p, int64_t at, const float (&f)[8]) {
-    if constexpr (F32) {
-        rc_f32x4* q = reinterpret_cast<rc_f32x4*>(static_cast<float*>(p) + at);
-        q[0] = rc_f32x4{f[0], f[1], f[2], f[3]};
-        q[1] = rc_f32x4{f[4], f[5], f[6], f[7]};
+// What store8_of writes of bf16.
+__device__ __forceinline__ rc_u32x4 pack8(const float (&f)[8]) {
+    return rc_u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+}
+template <bool ANY = false>
+__device__ __forceinline__ void store8_bf16(uint16_t* p, rc_u32x4 w, int64_t n = 8) {
+    if (!ANY) {
+        *reinterpret_cast<rc_u32x4*>(p) = w;
+    } else if (n >= 8) {
+        *reinterpret_cast<rc_u32x4_any*>(p) = w;
     } else {
-        *reinterpret_cast<rc_u32x4*>(static_cast<uint16_t*>(p) + at) =
-            rc_u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) p[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+    }
+}
+template <bool F32, bool ANY = false>
+__device__ __forceinline__ void store8_of(void* p, int64_t at, const float (&f)[8], int64_t n = 8) {
+    if constexpr (!F32) {
+        store8_bf16<ANY>(static_cast<uint16_t*>(p) + at, pack8(f), n);
+    } else {
+        float* q = static_cast<float*>(p) + at;
+        const rc_f32x4 lo = {f[0], f[1], f[2], f[3]}, hi = {f[4], f[5], f[6], f[7]};
+        if (!ANY) {
+            reinterpret_cast<rc_f32x4*>(q)[0] = lo;
+            reinterpret_cast<rc_f32x4*>(q)[1] = hi;
+        } else if (n >= 8) {
+            *reinterpret_cast<rc_f32x4_any*>(q) = lo;
+            *reinterpret_cast<rc_f32x4_any*>(q + 4) = hi;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < n) q[j] = f[j];
+        }
+    }
+}
+template <bool ANY = false>
+__device__ __forceinline__ void store8_codes(uint8_t* p, uint2 w, int64_t n = 8) {
+    if (!ANY) {
+        *reinterpret_cast<uint2*>(p) = w;
+    } else if (n >= 8) {
+        *reinterpret_cast<rc_u32x2_any*>(p) = rc_u32x2_any{w.x, w.y};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) p[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
     }
 }
 
 // Writes the values v of one row as codes and scales, and in bf16 where out.y is set. The row's TPR
 // threads (thread `tid`) hold the columns 8 (i TPR + tid) .. + 7 in v[i]; columns >= H are zero there,
-// and H is a multiple of 8. A 1x128 group is one DPP row of 16 lanes.
-template <int TPR, int NC>
+// and without ANY H is a multiple of 8. A 1x128 group is one DPP row of 16 lanes.
+template <int TPR, int NC, bool ANY>
 __device__ __forceinline__ void emit_row(const RowCodes& out, int64_t row, int64_t T, int64_t H, int tid, const float (&v)[NC][8],
                                          uint32_t* part) {
     if (out.y != nullptr) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int64_t c = 8 * (static_cast<int64_t>(i) * TPR + tid);
-            if (c < H) store8_of<false>(out.y, row * out.ldy + c, v[i]);
+            if (c < H) store8_of<false, ANY>(out.y, row * out.ldy + c, v[i], H - c);
         }
     }
     if (out.codes == kCodesNone) return;
@@ -197,7 +262,7 @@ __device__ __forceinline__ void emit_row(const RowCodes& out, int64_t row, int64
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int64_t c = 8 * (static_cast<int64_t>(i) * TPR + tid);
-            if (c < H) *reinterpret_cast<uint2*>(out.q + row * out.ldq + c) = codes8(v[i], g.m, kCodesI8);
+            if (c < H) store8_codes<ANY>(out.q + row * out.ldq + c, codes8(v[i], g.m, kCodesI8), H - c);
         }
         return;
     }
@@ -207,13 +272,13 @@ __device__ __forceinline__ void emit_row(const RowCodes& out, int64_t row, int64
         const uint32_t am = umax_row16(amax8(v[i]));
         const GroupScale g = out.codes == kCodesE4m3Fnuz ? fp8_scale<true>(am) : fp8_scale<false>(am);
         if (c < H) {
-            *reinterpret_cast<uint2*>(out.q + row * out.ldq + c) = codes8(v[i], g.m, out.codes);
+            store8_codes<ANY>(out.q + row * out.ldq + c, codes8(v[i], g.m, out.codes), H - c);
             if ((tid & 15) == 0) out.s[c / kGroup * T + row] = g.s;
         }
     }
 }
 
-// The same for a row of any length and alignment: `value(c)` gives the value of column c, and is called
+// The same for a row of any length: `value(c)` gives the value of column c, and is called
 // again for each pass. One workgroup of WAVES waves; a wave takes a group of 128 columns at a time, lane
 // l its columns l and l + 64.
 template <int WAVES, typename F>
@@ -256,6 +321,13 @@ __device__ __forceinline__ void emit_row_any(const RowCodes& out, int64_t row, i
             out.q[row * out.ldq + c] = static_cast<uint8_t>(w);
         }
     }
+}
+
+// Whether rows of a byte stride begin on whole pieces.
+inline bool rows16(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; }
+inline bool rows8(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 8 == 0 && bytes % 8 == 0; }
+inline bool whole_codes(const RowCodes& o) {
+    return (o.codes == kCodesNone || rows8(o.q, o.ldq)) && (o.y == nullptr || rows16(o.y, 2 * o.ldy));
 }
 
 }  // namespace bsfp8

@@ -359,7 +359,7 @@ inline I8Kernel i8_kernel(int64_t M, int64_t N, int64_t K, int cus) {
     return static_cast<I8Kernel>(best);
 }
 
-// Whether a small tile kernel reads B past the caches: one row of tiles, more of them than compute units. Us
+// Whether a small tile kernel reads B past the caches: one row of tiles, more of them than three in four compute units. Us
 // through the caches and past them: 16 x 14336 x 4096 in 32x64 14.4, 13.0; 64 x 14336 x 4096 in 64x64 17.2, 15.4; with
 // fewer, 16 x 4096 x 14336 in 32x32 18.4, 19.3, and 64 x 5120 x 5120 in 64x64 16.7, 16.3.
 inline bool i8_reads_once(int64_t M, int64_t N, I8Kernel kernel, int cus) {

@@ -77,8 +77,9 @@ __device__ __forceinline__ void swiglu_grad8(const float (&dy)[8], const float (
     }
 }
 
-// A row of TPR threads, NC pieces of 8 columns each.
-template <int TPR, int NC>
+// A row of TPR threads, NC pieces of 8 columns each. ANY: rows that begin anywhere, of any length; without it all rows in
+// 16-byte pieces (codes in 8-byte ones).
+template <int TPR, int NC, bool ANY>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, int64_t per_xcd, RowCodes out) {
     __shared__ uint32_t part_max[kWaves];
     const int tid = threadIdx.x % TPR;
@@ -88,94 +89,103 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const uint16_t* gu, in
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int64_t c = 8 * (static_cast<int64_t>(i) * TPR + tid), at = row * ldgu + (c < F ? c : 0);
-        g[i] = *reinterpret_cast<const rc_u32x4*>(gu + at);
-        u[i] = *reinterpret_cast<const rc_u32x4*>(gu + at + F);
+        g[i] = load8_bf16<false, ANY>(gu + at, F - c);
+        u[i] = load8_bf16<false, ANY>(gu + at + F, F - c);
     }
     float v[NC][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const bool in = 8 * (static_cast<int64_t>(i) * TPR + tid) < F;
         float gf[8], uf[8];
         unpack8(g[i], gf);
         unpack8(u[i], uf);
-        swiglu8(gf, uf, v[i]);
-        if (!in)
+        swiglu8(gf, uf, v[i]);  // of zeros: zero
+        if (!ANY && 8 * (static_cast<int64_t>(i) * TPR + tid) >= F)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     }
-    emit_row<TPR, NC>(out, row, T, F, tid, v, part_max);
+    emit_row<TPR, NC, ANY>(out, row, T, F, tid, v, part_max);
 }
 
-__global__ __launch_bounds__(kThreads) void swiglu_any_kernel(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, RowCodes out) {
+// Longer rows.
+__global__ __launch_bounds__(kThreads) void swiglu_long_kernel(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, RowCodes out) {
     __shared__ uint32_t part_max[kWaves];
     const int64_t row = blockIdx.x;
     const uint16_t* p = gu + row * ldgu;
     emit_row_any<kWaves>(out, row, T, F, [&](int64_t c) { return swiglu(bf16_to_f32(p[c]), bf16_to_f32(p[F + c])); }, part_max);
 }
 
-// Eight columns of a row of a [*, ld] bf16 tensor; zero outside.
-template <bool VEC, bool ONCE = false>
-__device__ __forceinline__ void load_cols(const uint16_t* p, int64_t ld, int64_t row, int64_t T, int64_t c, int64_t C, float (&f)[8]) {
-    const bool in = row < T;
-    if (VEC) {
-        load8_of<false, ONCE>(p, in && c < C ? row * ld + c : 0, f);
-        if (!(in && c < C))
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = in && c + j < C ? bf16_to_f32(p[row * ld + c + j]) : 0.0f;
-    }
-}
-
-template <bool FNUZ, bool VEC>
+template <bool FNUZ, bool WHOLE>
 __global__ __launch_bounds__(kTileThreads) void swiglu_dual_kernel(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, TileCodes out) {
     __shared__ TileLds lds;
     const int t = threadIdx.x;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kGroup, c0 = static_cast<int64_t>(blockIdx.x) * kGroup;
     const int64_t row = r0 + (t >> 4) * kTileRows, c = c0 + (t & 15) * 8;
-    float v[kTileRows][8], u[kTileRows][8];
+    rc_u32x4 g[kTileRows], u[kTileRows];
+    load_tile<WHOLE>(gu, ldgu, row, T, c0, c, F, g);
+    load_tile<WHOLE>(gu + F, ldgu, row, T, c0, c, F, u);
+    float v[kTileRows][8];
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) {
-        load_cols<VEC>(gu, ldgu, row + i, T, c, F, v[i]);
-        load_cols<VEC>(gu + F, ldgu, row + i, T, c, F, u[i]);
+        float gf[8], uf[8];
+        unpack8(g[i], gf);
+        unpack8(u[i], uf);
+        swiglu8(gf, uf, v[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        float w[8];
-        swiglu8(v[i], u[i], w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = w[j];
-    }
-    emit_tile<FNUZ, true, VEC, VEC>(out, r0, c0, T, F, v, lds);
+    emit_tile<FNUZ, true>(out, r0, c0, T, F, v, lds);
 }
 
-// The gradient's tile of the columns c0 .. c0 + 127 of [T, 2 F], which may hold columns of both halves.
+// The gradient's tile of the columns c0 .. c0 + 127 of [T, 2 F]: of one half, or of both (a group of 128 may lie in
+// both, and so may a thread's eight columns).
 template <bool FNUZ>
-__global__ __launch_bounds__(kTileThreads) void swiglu_backward_dual_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* gu, int64_t ldgu,
-                                                                           int64_t T, int64_t F, TileCodes out) {
+__global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward_dual_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* gu, int64_t ldgu,
+                                                                              int64_t T, int64_t F, TileCodes out) {
     __shared__ TileLds lds;
     const int t = threadIdx.x;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kGroup, c0 = static_cast<int64_t>(blockIdx.x) * kGroup;
     const int64_t row = r0 + (t >> 4) * kTileRows, c = c0 + (t & 15) * 8;
-    float v[kTileRows][8];
+    float v[kTileRows][8], dg[8], du[8];
+    if (c0 + kGroup <= F || (c0 >= F && c0 + kGroup <= 2 * F)) {
+        const int64_t half = c0 < F ? 0 : F;
+        rc_u32x4 d[kTileRows], g[kTileRows], u[kTileRows];
+        load_tile<true>(dy, lddy, row, T, c0 - half, c - half, F, d);
+        load_tile<true>(gu, ldgu, row, T, c0 - half, c - half, F, g);
+        load_tile<true>(gu + F, ldgu, row, T, c0 - half, c - half, F, u);
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        float d[8], g[8], u[8], dg[8], du[8];
+        for (int i = 0; i < kTileRows; ++i) {
+            float df[8], gf[8], uf[8];
+            unpack8(d[i], df);
+            unpack8(g[i], gf);
+            unpack8(u[i], uf);
+            swiglu_grad8(df, gf, uf, dg, du);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t at = c + j, f = at < F ? at : at - F;
-            const bool in = row + i < T && at < 2 * F;
-            const uint16_t* p = gu + (row + i) * ldgu + f;
-            d[j] = in ? bf16_to_f32(dy[(row + i) * lddy + f]) : 0.0f;
-            g[j] = in ? bf16_to_f32(p[0]) : 0.0f;
-            u[j] = in ? bf16_to_f32(p[F]) : 0.0f;
+            for (int j = 0; j < 8; ++j) v[i][j] = half == 0 ? dg[j] : du[j];
         }
-        swiglu_grad8(d, g, u, dg, du);
+    } else {
+        const bool both = c < F && c + 8 > F;
+        const int64_t f = c < F ? c : c - F;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = c + j < F ? dg[j] : du[j];
+        for (int i = 0; i < kTileRows; ++i) {
+            float d[8], g[8], u[8];
+            const int64_t n = row + i < T ? F - f : 0;  // of the half, from f on
+            load8_of<false, false, true>(dy, (row + i) * lddy + f, d, n);
+            load8_of<false, false, true>(gu, (row + i) * ldgu + f, g, n);
+            load8_of<false, false, true>(gu + F, (row + i) * ldgu + f, u, n);
+            if (both && n > 0) {  // the rest from the other half's beginning
+#pragma unroll
+                for (int j = 1; j < 8; ++j) {
+                    const int64_t k = c + j - F;
+                    if (k < 0 || k >= F) continue;
+                    d[j] = bf16_to_f32(dy[(row + i) * lddy + k]);
+                    g[j] = bf16_to_f32(gu[(row + i) * ldgu + k]);
+                    u[j] = bf16_to_f32(gu[(row + i) * ldgu + F + k]);
+                }
+            }
+            swiglu_grad8(d, g, u, dg, du);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = c + j < F ? dg[j] : du[j];
+        }
     }
-    emit_tile<FNUZ, true, false, false>(out, r0, c0, T, 2 * F, v, lds);
+    emit_tile<FNUZ, true>(out, r0, c0, T, 2 * F, v, lds);
 }
 
 // Whole tiles of both halves (F a multiple of 128): gate and up gradients of the same inputs.
@@ -186,64 +196,48 @@ __global__ __launch_bounds__(kTileThreads) void swiglu_backward_tiles_kernel(con
     const int t = threadIdx.x;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kGroup, c0 = static_cast<int64_t>(blockIdx.x) * kGroup;
     const int64_t row = r0 + (t >> 4) * kTileRows, c = c0 + (t & 15) * 8;
+    rc_u32x4 d[kTileRows], g[kTileRows], u[kTileRows];
+    load_tile<true>(dy, lddy, row, T, c0, c, F, d);
+    load_tile<true>(gu, ldgu, row, T, c0, c, F, g);
+    load_tile<true>(gu + F, ldgu, row, T, c0, c, F, u);
     float dg[kTileRows][8], du[kTileRows][8];
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) {
-        float d[8], g[8], u[8];
-        load_cols<true>(dy, lddy, row + i, T, c, F, d);
-        load_cols<true>(gu, ldgu, row + i, T, c, F, g);
-        load_cols<true>(gu + F, ldgu, row + i, T, c, F, u);
-        swiglu_grad8(d, g, u, dg[i], du[i]);
+        float df[8], gf[8], uf[8];
+        unpack8(d[i], df);
+        unpack8(g[i], gf);
+        unpack8(u[i], uf);
+        swiglu_grad8(df, gf, uf, dg[i], du[i]);
     }
-    emit_tile<FNUZ, true, true, true>(out, r0, c0, T, 2 * F, dg, lds);
-    emit_tile<FNUZ, true, true, true, true>(out, r0, c0 + F, T, 2 * F, du, lds);
+    emit_tile<FNUZ, true>(out, r0, c0, T, 2 * F, dg, lds);
+    emit_tile<FNUZ, true, true>(out, r0, c0 + F, T, 2 * F, du, lds);
 }
 
-template <bool VEC>
+template <bool ANY>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* gu, int64_t ldgu, int64_t T,
                                                                   int64_t F, int64_t chunks, uint16_t* dgu, int64_t lddgu) {
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
     const int64_t row = unit / chunks, c = (unit - row * chunks) * 512 + (threadIdx.x & 63) * 8;
     if (row >= T || c >= F) return;
     float d[8], g[8], u[8], dg[8], du[8];
-    load_cols<VEC>(dy, lddy, row, T, c, F, d);
-    load_cols<VEC>(gu, ldgu, row, T, c, F, g);
-    load_cols<VEC>(gu + F, ldgu, row, T, c, F, u);
+    load8_of<false, false, ANY>(dy, row * lddy + c, d, F - c);
+    load8_of<false, false, ANY>(gu, row * ldgu + c, g, F - c);
+    load8_of<false, false, ANY>(gu + F, row * ldgu + c, u, F - c);
     swiglu_grad8(d, g, u, dg, du);
-    uint16_t* p = dgu + row * lddgu + c;
-    if (VEC) {
-        store8_of<false>(p, 0, dg);
-        store8_of<false>(p, F, du);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < F) {
-                p[j] = to_bf16_bits(dg[j]);
-                p[F + j] = to_bf16_bits(du[j]);
-            }
-    }
+    store8_of<false, ANY>(dgu, row * lddgu + c, dg, F - c);
+    store8_of<false, ANY>(dgu + F, row * lddgu + c, du, F - c);
 }
 
-bool rows16(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; }
-bool rows8(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 8 == 0 && bytes % 8 == 0; }
-bool tiles_vec(const TileCodes& o, int64_t T) { return rows8(o.q, o.ldq) && T % 16 == 0 && rows16(o.qT, o.ldqT); }
 dim3 tiles(int64_t T, int64_t C) {
     return dim3(static_cast<unsigned>((C + kGroup - 1) / kGroup), static_cast<unsigned>((T + kGroup - 1) / kGroup));
 }
 
-}  // namespace
-
-hipError_t launch_swiglu(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, const RowCodes& out, hipStream_t stream) {
-    const bool vec = F % 8 == 0 && F <= sched::kRowMax && rows16(gu, 2 * ldgu) && (out.codes == kCodesNone || rows8(out.q, out.ldq)) &&
-                     (out.y == nullptr || rows16(out.y, 2 * out.ldy));
-    if (!vec) {
-        swiglu_any_kernel<<<static_cast<unsigned>(T), kThreads, 0, stream>>>(gu, ldgu, T, F, out);
-        return hipGetLastError();
-    }
+template <bool ANY>
+void launch_rows(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, const RowCodes& out, hipStream_t stream) {
     const bool wave = F <= sched::kRowWaveMax;
     const int64_t blocks = wave ? (T + kWaves - 1) / kWaves : T, per_xcd = (blocks + kXcds - 1) / kXcds;
     const unsigned grid = static_cast<unsigned>(per_xcd * kXcds);
-#define BSFP8_SWIGLU(TPR, NC) swiglu_kernel<TPR, NC><<<grid, kThreads, 0, stream>>>(gu, ldgu, T, F, per_xcd, out)
+#define BSFP8_SWIGLU(TPR, NC) swiglu_kernel<TPR, NC, ANY><<<grid, kThreads, 0, stream>>>(gu, ldgu, T, F, per_xcd, out)
     if (wave) {
         if (F <= 512) BSFP8_SWIGLU(64, 1);
         else BSFP8_SWIGLU(64, 2);
@@ -258,23 +252,30 @@ hipError_t launch_swiglu(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F,
         }
     }
 #undef BSFP8_SWIGLU
+}
+
+}  // namespace
+
+hipError_t launch_swiglu(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, const RowCodes& out, hipStream_t stream) {
+    if (F > sched::kRowMax) swiglu_long_kernel<<<static_cast<unsigned>(T), kThreads, 0, stream>>>(gu, ldgu, T, F, out);
+    else if (F % 8 == 0 && rows16(gu, 2 * ldgu) && whole_codes(out)) launch_rows<false>(gu, ldgu, T, F, out, stream);
+    else launch_rows<true>(gu, ldgu, T, F, out, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_swiglu_dual(const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F, const TileCodes& out, bool fnuz,
                               hipStream_t stream) {
-    const bool vec = F % 8 == 0 && rows16(gu, 2 * ldgu) && tiles_vec(out, T);
-    const dim3 grid = tiles(T, F);
-    if (fnuz && vec) swiglu_dual_kernel<true, true><<<grid, kTileThreads, 0, stream>>>(gu, ldgu, T, F, out);
-    else if (fnuz) swiglu_dual_kernel<true, false><<<grid, kTileThreads, 0, stream>>>(gu, ldgu, T, F, out);
-    else if (vec) swiglu_dual_kernel<false, true><<<grid, kTileThreads, 0, stream>>>(gu, ldgu, T, F, out);
-    else swiglu_dual_kernel<false, false><<<grid, kTileThreads, 0, stream>>>(gu, ldgu, T, F, out);
+    const auto go = [&](auto fz, auto whole) {
+        swiglu_dual_kernel<decltype(fz)::value, decltype(whole)::value><<<tiles(T, F), kTileThreads, 0, stream>>>(gu, ldgu, T, F, out);
+    };
+    if (F % kGroup == 0) fnuz ? go(std::true_type{}, std::true_type{}) : go(std::false_type{}, std::true_type{});
+    else fnuz ? go(std::true_type{}, std::false_type{}) : go(std::false_type{}, std::false_type{});
     return hipGetLastError();
 }
 
 hipError_t launch_swiglu_backward_dual(const uint16_t* dy, int64_t lddy, const uint16_t* gu, int64_t ldgu, int64_t T, int64_t F,
                                        const TileCodes& out, bool fnuz, hipStream_t stream) {
-    if (F % kGroup == 0 && rows16(dy, 2 * lddy) && rows16(gu, 2 * ldgu) && tiles_vec(out, T)) {
+    if (F % kGroup == 0) {
         if (fnuz) swiglu_backward_tiles_kernel<true><<<tiles(T, F), kTileThreads, 0, stream>>>(dy, lddy, gu, ldgu, T, F, out);
         else swiglu_backward_tiles_kernel<false><<<tiles(T, F), kTileThreads, 0, stream>>>(dy, lddy, gu, ldgu, T, F, out);
     } else if (fnuz) {
@@ -289,10 +290,11 @@ hipError_t launch_swiglu_backward(const uint16_t* dy, int64_t lddy, const uint16
                                   uint16_t* dgu, int64_t lddgu, hipStream_t stream) {
     const int64_t chunks = (F + 511) / 512, blocks = (T * chunks + kWaves - 1) / kWaves;
     const unsigned grid = static_cast<unsigned>(blocks);
+    // both halves on whole pieces: F a multiple of 8
     if (F % 8 == 0 && rows16(dy, 2 * lddy) && rows16(gu, 2 * ldgu) && rows16(dgu, 2 * lddgu))
-        swiglu_backward_kernel<true><<<grid, kThreads, 0, stream>>>(dy, lddy, gu, ldgu, T, F, chunks, dgu, lddgu);
-    else
         swiglu_backward_kernel<false><<<grid, kThreads, 0, stream>>>(dy, lddy, gu, ldgu, T, F, chunks, dgu, lddgu);
+    else
+        swiglu_backward_kernel<true><<<grid, kThreads, 0, stream>>>(dy, lddy, gu, ldgu, T, F, chunks, dgu, lddgu);
     return hipGetLastError();
 }
 
