@@ -351,6 +351,8 @@ int validate_route(int dtype, int64_t T, int64_t E, int64_t ld, int score, int64
 // Limits of the operators that take rows of tokens: a workgroup of four waves a row.
 constexpr int64_t kMaxRows = (int64_t{1} << 24) - 16;
 constexpr int64_t kMaxI8K = 131071;  // 2^14 K < 2^31
+// A launch's lanes are counted in 32 bits: 512 for each 128 columns, 1024 for each 16.
+constexpr int64_t kMaxTileColumns = (int64_t{1} << 30) - 128, kMaxBackwardColumns = (int64_t{1} << 26) - 16;
 
 bool dtype_ok(int d) { return d == BSFP8_BF16 || d == BSFP8_F32; }
 bool fp8_codes(int codes) { return codes == BSFP8_CODES_E4M3FN || codes == BSFP8_CODES_E4M3FNUZ; }
@@ -369,7 +371,7 @@ int validate_codes(int64_t T, int64_t H, int codes, const void* q, int64_t ldq, 
 // Outputs in both groupings of a [T, C] tensor.
 int validate_tiles(int64_t T, int64_t C, int codes, const void* q, int64_t ldq, const float* a_s, const void* qT, int64_t ldqT,
                    const float* s) {
-    if (T < 0 || C < 0 || C > 0x7FFFFFFF || cdiv(T, kGroupEdge) > kMaxGridY || !fp8_codes(codes)) return BSFP8_EINVAL;
+    if (T < 0 || C < 0 || C > kMaxTileColumns || cdiv(T, kGroupEdge) > kMaxGridY || !fp8_codes(codes)) return BSFP8_EINVAL;
     if (T == 0 || C == 0) return BSFP8_OK;
     if (q == nullptr || a_s == nullptr || qT == nullptr || s == nullptr || ldq < C || ldqT < T) return BSFP8_EINVAL;
     return BSFP8_OK;
@@ -769,7 +771,7 @@ int rms_norm_quantize(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
 
 int rms_norm_quantize_rhs(const void* h, int h_dtype, int64_t T, int64_t H, int64_t ldh, const void* weight, int w_dtype,
                           const float* rstd, int codes, void* qT, int64_t ldqT, float* s, void* stream) {
-    if (T < 0 || H < 0 || H > 0x7FFFFFFF || cdiv(T, kGroupEdge) > kMaxGridY || !fp8_codes(codes)) return BSFP8_EINVAL;
+    if (T < 0 || H < 0 || H > kMaxTileColumns || cdiv(T, kGroupEdge) > kMaxGridY || !fp8_codes(codes)) return BSFP8_EINVAL;
     if (!dtype_ok(h_dtype) || !dtype_ok(w_dtype)) return BSFP8_EINVAL;
     if (T == 0 || H == 0) return BSFP8_OK;
     if (h == nullptr || weight == nullptr || rstd == nullptr || qT == nullptr || s == nullptr || ldh < H || ldqT < T)
@@ -781,7 +783,7 @@ int rms_norm_quantize_rhs(const void* h, int h_dtype, int64_t T, int64_t H, int6
 }
 
 int64_t rms_norm_backward_workspace(int64_t T, int64_t H) {
-    if (T < 0 || H < 0 || T > kMaxRows || H > 0x7FFFFFFF) return -1;
+    if (T < 0 || H < 0 || T > kMaxRows || H > kMaxBackwardColumns) return -1;
     return bsfp8::sched::norm_backward_blocks(T) * H * static_cast<int64_t>(sizeof(float));
 }
 

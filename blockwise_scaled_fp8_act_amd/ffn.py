@@ -46,7 +46,13 @@ def _layer(weight_norm, w_gate_up, w_down):
 def _rows(name, t, H, dtypes):
     if t.dim() != 2 or t.shape[1] != H or t.dtype not in dtypes:
         raise ValueError(f"expected {name} [T, {H}] of {[str(d) for d in dtypes]}, got {t.dtype} {tuple(t.shape)}")
-    return t.contiguous()
+    return _dense(t, t.dtype, *t.shape)
+
+
+def _dense(t, dtype, T, H):
+    """t as [T, H] of the type, its strides too (a gradient may be expanded, which sizes of 0 and 1 hide)."""
+    t = t.to(dtype).reshape(T, H)
+    return t if t.stride() == (H, 1) else torch.empty((T, H), dtype=dtype, device=t.device).copy_(t)
 
 
 def _weight(w, fmt):
@@ -58,9 +64,12 @@ class _FeedForwardFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight_norm, w_gate_up, w_down, eps, fmt):
         F, H = _layer(weight_norm, w_gate_up, w_down)
-        x = _rows("x", x, H, (torch.bfloat16,))
+        given, ctx.shape = x, x.shape
         if residual is not None:
-            residual = _rows("residual", residual, H, (torch.bfloat16, torch.float32))
+            if residual.shape != x.shape:
+                raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+            residual = _rows("residual", residual.reshape(-1, residual.shape[-1]), H, (torch.bfloat16, torch.float32))
+        x = _rows("x", x.reshape(-1, x.shape[-1]), H, (torch.bfloat16,))
         T, dev = x.shape[0], x.device
         w_gate_up, w_down, weight_norm = w_gate_up.contiguous(), w_down.contiguous(), weight_norm.contiguous()
         q, s, h, _, rstd = _b.rms_norm_quantize(x, weight_norm, residual=residual, eps=eps, fmt=fmt, q=_codes(T, H, dev), want_rstd=True)
@@ -72,18 +81,29 @@ class _FeedForwardFn(torch.autograd.Function):
         y = _b.gemm_1x128_128x128(qa, sa, q2, s2, fmt=fmt)
         ctx.save_for_backward(h, weight_norm, rstd, gu, qaT, saT, q1T, s1, q2T, s2)
         ctx.fmt, ctx.x_dtype = fmt, x.dtype
-        return y, h.view_as(h) if residual is None else h
+        ctx.set_materialize_grads(False)        # an output that nothing was made of has no gradient to read
+        return y.view(ctx.shape), given.view_as(given) if residual is None else h.view(ctx.shape)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dy, dh):
-        h, weight_norm, rstd, gu, qaT, saT, q1T, s1, q2T, s2 = ctx.saved_tensors
-        fmt, dev, T, H, F = ctx.fmt, h.device, *h.shape, gu.shape[1] // 2
-        need_x, need_r, need_n, need_1, need_2 = ctx.needs_input_grad[:5]
-        dy = dy.to(torch.bfloat16).contiguous()
+        # With create_graph the kernels' results must not pass for constants. Else x and the residual get one tensor as
+        # their gradient, and autograd sees that it is one: a leaf copies it instead of keeping memory that another keeps.
+        return _gradients_once(ctx, dy, dh) if torch.is_grad_enabled() else _gradients(ctx, dy, dh)
+
+
+def _gradients(ctx, dy, dh):
+    h, weight_norm, rstd, gu, qaT, saT, q1T, s1, q2T, s2 = ctx.saved_tensors
+    h = h.reshape(-1, h.shape[-1])
+    fmt, dev, T, H, F = ctx.fmt, h.device, *h.shape, gu.shape[1] // 2
+    need_x, need_r, need_n, need_1, need_2 = ctx.needs_input_grad[:5]
+    dx = dw1 = dw2 = dwn = None
+    if dy is None:                              # h alone was used
+        dx = None if dh is None else dh.to(h.dtype)
+    else:
+        dy = _dense(dy, torch.bfloat16, T, H)
         qd, sd, qdT, sdT = _b.quantize_lhs_and_rhs(dy, q=_codes(T, H, dev), qT=_codes(H, T, dev), fmt=fmt)
-        dw2 = _b.gemm_1x128_128x1(qdT, sdT, qaT, saT, fmt=fmt) if need_2 else None
-        dx = dw1 = dwn = None
+        if need_2:
+            dw2 = _b.gemm_1x128_128x1(qdT, sdT, qaT, saT, fmt=fmt)
         if need_x or need_r or need_n or need_1:
             da = _b.gemm_1x128_128x128(qd, sd, q2T, s2, 1, s2.shape[1], fmt=fmt)
             qg, sg, qgT, sgT = _b.swiglu_backward_quantize(da, gu, q=_codes(T, 2 * F, dev), qT=_codes(2 * F, T, dev), fmt=fmt)
@@ -92,14 +112,20 @@ class _FeedForwardFn(torch.autograd.Function):
                 dw1 = _b.gemm_1x128_128x1(qgT, sgT, qn, sn, fmt=fmt)
             if need_x or need_r or need_n:
                 dn = _b.gemm_1x128_128x128(qg, sg, q1T, s1, 1, s1.shape[1], fmt=fmt)
-                dx, dwn = _b.rms_norm_backward(dn, h, weight_norm, rstd, dh=None if dh is None else dh.to(h.dtype).contiguous())
-        return (dx.to(ctx.x_dtype) if need_x else None, dx if need_r else None, dwn if need_n else None, dw1, dw2, None, None)
+                dh = None if dh is None else _dense(dh, h.dtype, T, H)
+                dx, dwn = _b.rms_norm_backward(dn, h, weight_norm, rstd, dh=dh)
+                dx = dx.view(ctx.shape)
+    gx = dx if dx is None or dx.dtype == ctx.x_dtype else dx.to(ctx.x_dtype)
+    return gx if need_x else None, dx if need_r else None, dwn if need_n else None, dw1, dw2, None, None
+
+
+_gradients_once = once_differentiable(_gradients)
 
 
 def blockwise_fp8_feed_forward(x, weight_norm, w_gate_up, w_down, residual=None, eps=1e-6, fmt="e4m3fn"):
-    """The layer for training: x [T, H] bf16, residual [T, H] bf16 or fp32 (None: x is the residual stream),
+    """The layer for training: x [..., H] bf16, residual of x's shape, bf16 or fp32 (None: x is the residual stream),
     weight_norm [H] bf16 or fp32, w_gate_up [2 F, H] (gate rows, then up rows) and w_down [H, F] bf16. Returns
-    (y [T, H] bf16, h [T, H] of the residual's type); gradients of x, residual and all weights. ``fmt``: the FP8 element
+    (y bf16, h of the residual's type), both of x's shape; gradients of x, residual and all weights. ``fmt``: the FP8 element
     format ("e4m3fn", "e4m3fnuz" or the torch float8 dtype)."""
     return _FeedForwardFn.apply(x, residual, weight_norm, w_gate_up, w_down, eps, _b.fp8_format(fmt))
 
@@ -119,10 +145,7 @@ class BlockwiseFp8FeedForward(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
         """(y, h): y of x's shape, h = x + residual."""
-        H = x.shape[-1]
-        y, h = blockwise_fp8_feed_forward(x.reshape(-1, H), self.weight_norm, self.w_gate_up, self.w_down,
-                                          residual=None if residual is None else residual.reshape(-1, H), eps=self.eps, fmt=self.fmt)
-        return y.reshape(x.shape), h.reshape(x.shape)
+        return blockwise_fp8_feed_forward(x, self.weight_norm, self.w_gate_up, self.w_down, residual=residual, eps=self.eps, fmt=self.fmt)
 
 
 def _int8_rows(rows, cols, device):
@@ -155,6 +178,8 @@ class ServingInt8FeedForward:
 def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     """clip_grads of the parameters' gradients, in place; parameters without one are passed over. Returns the norm
     before the clipping, (1,) fp32 on the device, without waiting for it."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
     if not grads:
         raise ValueError("no parameter has a gradient")

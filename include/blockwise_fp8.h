@@ -488,8 +488,9 @@ int gemm_1x128_128x128_routed(const void* a, int64_t lda, const float* a_s, int6
  *                     q = rint(fl32(v * fl32(127 / max(amax, 1e-12f)))), ties to even;
  *   NONE              neither (q and s are NULL): the bf16 output alone.
  * A group (a row, for INT8) that holds a NaN has scale NaN, one that holds an infinity scale infinity; its
- * codes are of no use then, and a product with such a row is NaN. Any alignment and row length are
- * accepted; rows 16-byte aligned (codes 8-byte) of a multiple of 8 columns are read in whole pieces.
+ * codes are of no use then, and a product with such a row is NaN. Rows may begin at any element and have any
+ * length; those 16-byte aligned (codes 8-byte) of a multiple of 8 columns are a little faster. Where T or the
+ * columns are 0 nothing is written (but a weight's gradient over no rows, which is 0).
  */
 enum { BSFP8_CODES_NONE = 0, BSFP8_CODES_E4M3FN = 1, BSFP8_CODES_E4M3FNUZ = 2, BSFP8_CODES_INT8 = 3 };
 
@@ -513,7 +514,7 @@ int rms_norm_quantize(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
  * rms_norm_quantize_rhs: the normed rows in 128x1 groups, transposed (the operand of the weight gradient),
  * formed again from h [T, H] (bf16 or fp32, h_dtype), weight and rstd as rms_norm_quantize gave them.
  *   qT [H, T] fp8, row stride ldqT >= T; s [ceil(T/128), H]: as quantize_rhs of the fp32 values. codes:
- *   E4M3FN or E4M3FNUZ. ceil(T/128) at most 65535.
+ *   E4M3FN or E4M3FNUZ. ceil(T/128) at most 65535, H at most 2^30 - 128.
  */
 int rms_norm_quantize_rhs(const void* h, int h_dtype, int64_t T, int64_t H, int64_t ldh, const void* weight, int w_dtype,
                           const float* rstd, int codes, void* qT, int64_t ldqT, float* s, void* stream);
@@ -527,7 +528,7 @@ int rms_norm_quantize_rhs(const void* h, int h_dtype, int64_t T, int64_t H, int6
  *   dx may be dh itself (same address and stride).
  *   workspace  device memory of rms_norm_backward_workspace(T, H) bytes (-1: invalid sizes), 16-byte
  *              aligned, not in use by another call.
- * T == 0 writes dweight = 0.
+ * T == 0 writes dweight = 0. H at most 2^26 - 16.
  */
 int64_t rms_norm_backward_workspace(int64_t T, int64_t H);
 int rms_norm_backward(const void* dy, int64_t lddy, const void* h, int h_dtype, int64_t ldh, const void* weight, int w_dtype,
@@ -544,7 +545,7 @@ int rms_norm_backward(const void* dy, int64_t lddy, const void* h, int h_dtype, 
  * dup = dy gate sig, with sig = sigmoid(gate).
  * swiglu_backward_quantize: the same gradient in both groupings, as quantize_lhs_and_rhs of its fp32
  * values: q [T, 2 F], a_s, qT [2 F, T], s.
- * ceil(T/128) at most 65535 for the forms with both groupings.
+ * ceil(T/128) at most 65535 and at most 2^30 - 128 code columns for the forms with both groupings.
  */
 int swiglu_quantize(const void* gu, int64_t T, int64_t F, int64_t ldgu, int codes, void* q, int64_t ldq, float* s,
                     void* y, int64_t ldy, void* stream);

@@ -54,6 +54,16 @@ def test_norm_rhs_and_backward_entries(L):
     assert L.rms_norm_backward_workspace(-1, 4) == -1 and L.rms_norm_backward_workspace(4, -1) == -1
 
 
+def test_more_columns_than_a_launch_holds(L):
+    wide = 2 ** 30 - 127
+    assert L.rms_norm_quantize_rhs(P, 0, 4, wide, wide, P, 0, P, 1, P, 4, P, None) == INVALID
+    assert L.swiglu_quantize_lhs_and_rhs(P, 4, wide, 2 * wide, 1, P, wide, P, P, 4, P, None) == INVALID
+    assert L.swiglu_backward_quantize(P, wide, P, 2 * wide, 4, 2 ** 29 - 63, 1, P, 2 * wide, P, P, 4, P, None) == INVALID
+    assert L.rms_norm_backward_workspace(4, 2 ** 26 - 15) == -1 and L.rms_norm_backward_workspace(4, 2 ** 26 - 16) == 4 * 4 * (2 ** 26 - 16)
+    deep = 2 ** 26
+    assert L.rms_norm_backward(P, deep, P, 0, deep, P, 0, P, None, 0, 4, deep, P, deep, P, P, 2 ** 40, None) == INVALID
+
+
 def test_swiglu_entries(L):
     def rows(gu=P, T=4, F=256, ldgu=512, codes=1, q=P, ldq=256, s=P, y=None, ldy=0):
         return L.swiglu_quantize(gu, T, F, ldgu, codes, q, ldq, s, y, ldy, None)

@@ -91,3 +91,98 @@ def test_halves_of_the_gradient_meet_in_a_group():
     # a code is off by half a step, 2^-4, plus what the bf16 value it is compared with is off, 2^-8
     for got, scale in ((rows, a_s.t().double().repeat_interleave(128, 1)[:, :2 * F]), (cols, s.double().repeat_interleave(128, 0)[:T])):
         assert ((got - plain).abs() <= plain.abs() * (2.0 ** -4 + 2.0 ** -7) + scale * least * 1.01).all()
+
+
+@pytest.mark.parametrize("shape", [(50,), (2, 5, 5)])
+def test_layer_with_one_output_used(shape):
+    """Gradients where only y, or only h, goes on; those of x and of the residual are two tensors."""
+    H, F = 136, 72
+    g = torch.Generator(device="cuda:0").manual_seed(1)
+    x, r = (torch.randn(*shape, H, device="cuda:0", generator=g).to(torch.bfloat16).requires_grad_() for _ in range(2))
+    layer = bf.BlockwiseFp8FeedForward(H, F, device="cuda:0")
+    dy = torch.randn(*shape, H, device="cuda:0", generator=g).to(torch.bfloat16)
+    y, h = layer(x, r)
+    assert y.shape == x.shape and h.shape == x.shape
+    torch.autograd.backward([y, h], [dy, torch.zeros_like(h)])
+    both = [t.grad.clone() for t in (x, r, *layer.parameters())]
+    assert x.grad.data_ptr() != r.grad.data_ptr()
+    x.grad = r.grad = None
+    layer.zero_grad()
+    layer(x, r)[0].backward(dy)
+    assert all(torch.equal(a, t.grad) for a, t in zip(both, (x, r, *layer.parameters())))
+    x.grad = r.grad = None
+    layer.zero_grad()
+    layer(x, r)[1].backward(dy)
+    assert torch.equal(x.grad, dy) and torch.equal(r.grad, dy) and all(p.grad is None for p in layer.parameters())
+    assert len({t.data_ptr() for t in (x.grad, r.grad, dy)}) == 3
+    y, h = layer(x, r)
+    first, = torch.autograd.grad(y, x, dy.clone().requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        first.sum().backward()
+
+
+def test_layers_without_tokens():
+    H, F = 136, 72
+    layer = bf.BlockwiseFp8FeedForward(H, F, device="cuda:0")
+    x = torch.empty(0, H, dtype=torch.bfloat16, device="cuda:0", requires_grad=True)
+    y, h = layer(x, torch.empty(0, H, device="cuda:0"))
+    assert y.shape == (0, H) and h.shape == (0, H) and h.dtype == torch.float32
+    (y.float().sum() + h.sum()).backward()
+    assert x.grad.shape == (0, H) and all((p.grad == 0).all() for p in layer.parameters())
+    serve = bf.ServingInt8FeedForward(layer.weight_norm, layer.w_gate_up, layer.w_down)
+    y, h = serve(x.detach(), None)
+    assert y.shape == (0, H) and h.shape == (0, H)
+
+
+def test_clipping_one_parameter():
+    p = torch.nn.Parameter(torch.ones(1001, device="cuda:0"))
+    p.grad = torch.full_like(p, 2.0)
+    norm = bf.clip_grad_norm_(p, 1.0, eps=0.0)
+    assert abs(float(norm) - 2 * 1001 ** 0.5) < 1e-5
+    # c = 1 / norm and the product are rounded once each
+    assert (p.grad.double() * 1001 ** 0.5 - 1).abs().max() <= 2.0 ** -22
+
+
+def test_captured_training_step():
+    """Forward, backward, clipping and the update in one graph, replayed with eager work between; every replay is the eager
+    step's bits. The warm-up's autograd graph is gone before the capture."""
+    torch.manual_seed(3)
+    T, H, F = 77, 256, 200
+    layer, twin = (bf.BlockwiseFp8FeedForward(H, F, device="cuda:0") for _ in range(2))
+    start = [p.detach().clone() for p in layer.parameters()]
+    x, dy = (torch.randn(T, H, device="cuda:0").to(torch.bfloat16) for _ in range(2))
+    r, dh = (torch.randn(T, H, device="cuda:0") for _ in range(2))
+
+    def step(m):
+        for p in m.parameters():
+            p.grad = None
+        torch.autograd.backward(list(m(x, r)), [dy, dh])
+        norm = bf.clip_grad_norm_(m.parameters(), 0.5)
+        with torch.no_grad():
+            for p in m.parameters():
+                p.sub_(p.grad)
+        return norm
+
+    def reset(m):
+        with torch.no_grad():
+            for p, s in zip(m.parameters(), start):
+                p.copy_(s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(layer)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    reset(layer)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = step(layer)
+    reset(layer)
+    reset(twin)
+    for i in range(4):
+        want = step(twin)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.isfinite(norm).all() and torch.equal(norm, want), i
+        assert all(torch.equal(a, b) for a, b in zip(layer.parameters(), twin.parameters())), i
