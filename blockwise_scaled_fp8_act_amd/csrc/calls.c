@@ -9,7 +9,9 @@
  *
  * Why: for few tokens these operators' kernels take 3 to 9 us and the launch 3.3. A call here takes 4.6
  * us (route, outputs given), 4.7 (combine), 5.1 (dispatch) and 5.3 (product); through binding.py's
- * checks and ctypes 6.8, 6.9, 7.4 and 9.1. NORMFIGURES */
+ * checks and ctypes 6.8, 6.9, 7.4 and 9.1. The norm of one token takes 5.4 to 6.2 us a call (9.8 the other
+ * way), the gated activation of 64 rows 5.3 (7.5), int8 rows and product of 1000 rows 10.2 together (14.2),
+ * clipping a layer's four gradients 12.3 (20.9). */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <math.h>

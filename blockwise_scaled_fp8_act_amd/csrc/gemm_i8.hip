@@ -115,6 +115,11 @@ __device__ __forceinline__ void store4(const I8Args& g, int64_t m, int64_t n, ui
 // HBM is the bound: every column of tiles begins with another block, and B is read past the caches (16 rows by
 // 14336 x 4096 14.7 us without both, 13.2 with the second, 11.5 with both, 5.1 TB/s). Else the workgroups of an
 // XCD, which share rows in its L2, begin together (512 x 5120 x 5120 in 64 x 128 tiles 39.8 -> 36.3 us).
+// 64 x 5120 x 5120 12.6 us, 1000 x 1000 x 1288 8.3. What most likely bounds a tile: the loads into LDS, some 32 bytes a cycle and CU. A
+// 128 x 128 tile's block of 32 KB takes 1080 cycles, its products 512; with loads that all lie out of range it takes as
+// long (512 x 5120 x 5120 24.4 us of 31.5, the rest is HBM's). So fragments read half a block ahead (31.6), waves of 64 x 64
+// with half of a block's K each, which read a third less from LDS (32.2), and other orders of the blocks in an XCD (31.2)
+// gain nothing.
 template <int BM, int BN, int WM, int WN, int STAGES, int KS, bool PAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args g, int mt, int nt, int c_vec) {
     constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kMS = WM / 16, kNS = WN / 16;
@@ -215,10 +220,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
 // ---- 256 x 256 tiles, eight waves of 64 x 128 (two a SIMD), two stages of 128 bytes of K. A wave reads the
 // fragments of half a block (64 bytes) while it multiplies the half before, and the one barrier a block comes
 // after its first half: by then every wave has read the whole stage, so the loads of the block after next go
-// there, a block's time before they are needed. 16384 x 5120 x 5120 381 us, 2.25 Pop/s (400 us with reads and
-// products of a block in turn); 4096^3 65 us (67 with all workgroups beginning at one block); 8192^3 437 us, 2.51. Bound by power: the same loop over zeros takes 402. Not
-// better: 32 x 32 x 32 instructions (488), a ring of five half blocks (473, in 6% fewer cycles at a lower
-// clock), four waves of 128 x 128 (550).
+// there, a block's time before they are needed. 16384 x 5120 x 5120 358 to 381 us, 2.25 to 2.4 Pop/s (400 us with reads and
+// products of a block in turn); 4096^3 65 us (67 with all workgroups beginning at one block); 8192^3 437 us, 2.51.
+// Bound by power: the same loop over zeros takes 402. Not better: 32 x 32 x 32 instructions (488), a ring of five half
+// blocks (473, in 6% fewer cycles at a lower clock), four waves of 128 x 128 (550).
 constexpr int kBig = 256;
 __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, int c_vec) {
     constexpr int WM = 64, WN = 128, kMS = WM / 16, kNS = WN / 16, kHalf = kBig * 8, kStage = 2 * kHalf;  // 16-byte units

@@ -1,7 +1,7 @@
 // gfx950 int8 row quantizer: x [T, H] bf16 -> codes with one scale a row (a token's activations, or an
 // output channel's weights): s = max(amax, 1e-12) / 127, q = rint(x * (127 / max(amax, 1e-12))). A row
 // stays in registers between its maximum and its codes (of up to sched::kRowMax values; longer ones are read
-// twice); bound by the memory traffic.
+// twice); bound by the memory traffic, for few rows by the launch: 1000 x 1288 3.3 us.
 #include "row_codes.hpp"
 #include "schedule.hpp"
 
