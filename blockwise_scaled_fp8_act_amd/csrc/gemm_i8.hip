@@ -91,16 +91,41 @@ __device__ __forceinline__ uint2 scaled4(const i32x4& sum, float as, const float
     for (int e = 0; e < 4; ++e) v[e] = (static_cast<float>(sum[e]) * as) * bs[e];
     return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
-__device__ __forceinline__ void store4(const I8Args& g, int64_t m, int64_t n, uint2 w, int c_vec) {
-    uint16_t* c = g.c + m * g.ldc + n;
-    if (c_vec && n + 4 <= g.N) {
-        *reinterpret_cast<uint2*>(c) = w;
-    } else {
-        const uint16_t h[4] = {static_cast<uint16_t>(w.x), static_cast<uint16_t>(w.x >> 16), static_cast<uint16_t>(w.y),
-                               static_cast<uint16_t>(w.y >> 16)};
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Writes a wave's WM x WN block of C, rows from m0 and columns from n0 on, through its own part of LDS, so that a
+// store's lanes write whole runs of a row, wherever rows begin (EPILOGUEFIGURES). 16-byte chunk c of row r lies at c ^ (r %
+// chunks). PAST: past the caches.
+template <int WM, int WN, bool PAST>
+__device__ __forceinline__ void store_block(const I8Args& g, const i32x4 (&acc)[WM / 16][WN / 16], int64_t m0, int64_t n0, uint8_t* own, int lane) {
+    constexpr int kChunks = WN / 8;  // of a row
+    const int l16 = lane & 15, lg = lane >> 4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < g.N) c[e] = h[e];
+    for (int j = 0; j < WN / 16; ++j) {
+        float bs[4];
+        column_scales(g, n0 + 16 * j + 4 * lg, bs);
+#pragma unroll
+        for (int i = 0; i < WM / 16; ++i) {
+            const int r = 16 * i + l16;
+            const float as = g.K > 0 && m0 + r < g.M ? g.a_s[m0 + r] : 0.0f;
+            *reinterpret_cast<uint2*>(own + r * (2 * WN) + (((2 * j + (lg >> 1)) ^ (r & (kChunks - 1))) * 16) + 8 * (lg & 1)) = scaled4(acc[i][j], as, bs);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < (WM * kChunks + 63) / 64; ++p) {
+        const int r = (64 * p + lane) / kChunks, c = lane % kChunks;
+        const int64_t m = m0 + r, n = n0 + 8 * c;
+        if (r >= WM || m >= g.M || n >= g.N) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * (2 * WN) + ((c ^ (r & (kChunks - 1))) * 16));
+        uint16_t* to = g.c + m * g.ldc + n;
+        if (n + 8 <= g.N) {
+            if (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(to));
+            else *reinterpret_cast<u32x4_any*>(to) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (n + e < g.N) to[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+        }
     }
 }
 
@@ -121,7 +146,7 @@ __device__ __forceinline__ void store4(const I8Args& g, int64_t m, int64_t n, ui
 // with half of a block's K each, which read a third less from LDS (32.2), and other orders of the blocks in an XCD (31.2)
 // gain nothing.
 template <int BM, int BN, int WM, int WN, int STAGES, int KS, bool PAST>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args g, int mt, int nt, int c_vec) {
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args g, int mt, int nt) {
     constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kMS = WM / 16, kNS = WN / 16;
     constexpr int kChunks = KS / 16, kRows = 64 / kChunks;  // of a row; rows of one load
     constexpr int kStage = (BM + BN) * kChunks, kLoads = (BM + BN) / kRows / kWaves;
@@ -204,17 +229,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
     }
     wait_loads<0>();  // the last blocks' empty loads: none may land after the workgroup's LDS is given away
 
-#pragma unroll
-    for (int j = 0; j < kNS; ++j) {
-        const int64_t n = n0 + WN * wn + 16 * j + 4 * lg;
-        float bs[4];
-        column_scales(g, n, bs);
-#pragma unroll
-        for (int i = 0; i < kMS; ++i) {
-            const int64_t m = m0 + WM * wm + 16 * i + l16;
-            if (m < g.M) store4(g, m, n, scaled4(acc[i][j], g.K > 0 ? g.a_s[m] : 0.0f, bs), c_vec);
-        }
-    }
+    lds_barrier();    // and no wave reads the stages any more
+    static_assert(STAGES * kStage * 16 >= BM * BN * 2, "the tile of C fits the stages");
+    store_block<WM, WN, false>(g, acc, m0 + WM * wm, n0 + WN * wn, reinterpret_cast<uint8_t*>(smem) + wave * (WM * WN * 2), lane);
 }
 
 // ---- 256 x 256 tiles, eight waves of 64 x 128 (two a SIMD), two stages of 128 bytes of K. A wave reads the
@@ -225,7 +242,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void tile_kernel(I8Args
 // Bound by power: the same loop over zeros takes 402. Not better: 32 x 32 x 32 instructions (488), a ring of five half
 // blocks (473, in 6% fewer cycles at a lower clock), four waves of 128 x 128 (550).
 constexpr int kBig = 256;
-__global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, int c_vec) {
+__global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt) {
     constexpr int WM = 64, WN = 128, kMS = WM / 16, kNS = WN / 16, kHalf = kBig * 8, kStage = 2 * kHalf;  // 16-byte units
     __shared__ u32x4 smem[2 * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -321,37 +338,8 @@ __global__ __launch_bounds__(512, 1) void big_kernel(I8Args g, int mt, int nt, i
         multiply(1);
     }
 
-    // each wave's 64 x 128 block goes through LDS, 16-byte chunk c of row r at c ^ (r % 16), so that a store
-    // writes whole lines; they are not read again here and go past the caches
     lds_barrier();
-    uint8_t* own = reinterpret_cast<uint8_t*>(smem) + wave * (WM * WN * 2);
-#pragma unroll
-    for (int j = 0; j < kNS; ++j) {
-        float bs[4];
-        column_scales(g, n0 + WN * wn + 16 * j + 4 * lg, bs);
-#pragma unroll
-        for (int i = 0; i < kMS; ++i) {
-            const int r = 16 * i + l16;
-            const int64_t m = m0 + WM * wm + r;
-            const float as = g.K > 0 && m < g.M ? g.a_s[m] : 0.0f;
-            *reinterpret_cast<uint2*>(own + r * 256 + (((2 * j + (lg >> 1)) ^ (r & 15)) * 16) + 8 * (lg & 1)) = scaled4(acc[i][j], as, bs);
-        }
-    }
-#pragma unroll
-    for (int p = 0; p < WM / 4; ++p) {
-        const int r = 4 * p + lg;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * 256 + ((l16 ^ (r & 15)) * 16));
-        const int64_t m = m0 + WM * wm + r, n = n0 + WN * wn + 8 * l16;
-        if (m >= g.M) continue;
-        uint16_t* c = g.c + m * g.ldc + n;
-        if (c_vec && n + 8 <= g.N) {
-            __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(c));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n + e < g.N) c[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
-        }
-    }
+    store_block<WM, WN, true>(g, acc, m0 + WM * wm, n0 + WN * wn, reinterpret_cast<uint8_t*>(smem) + wave * (WM * WN * 2), lane);
 }
 
 // ---- One to four rows of A: four columns a workgroup, whose waves take a KB of each in turn, 16 bytes a lane,
@@ -417,14 +405,12 @@ hipError_t launch_gemm_i8(const I8Args& g, int cus, hipStream_t stream) {
     const sched::I8Tile tile = sched::kI8Tiles[kernel];
     const int mt = static_cast<int>(sched::cdiv(g.M, tile.bm)), nt = static_cast<int>(sched::cdiv(g.N, tile.bn));
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(mt) * nt);
-    const int64_t piece = kernel == sched::kI8Big ? 16 : 8;
-    const int c_vec = reinterpret_cast<uintptr_t>(g.c) % piece == 0 && 2 * g.ldc % piece == 0;
     const bool past = sched::i8_reads_once(g.M, g.N, kernel, cus);
 #define BSFP8_TILE(BM, BN, WM, WN, STAGES, KS)                                                                      \
     do {                                                                                                            \
         constexpr int kThreads = 64 * (BM / WM) * (BN / WN);                                                        \
-        if (past) tile_kernel<BM, BN, WM, WN, STAGES, KS, true><<<grid, kThreads, 0, stream>>>(g, mt, nt, c_vec);   \
-        else tile_kernel<BM, BN, WM, WN, STAGES, KS, false><<<grid, kThreads, 0, stream>>>(g, mt, nt, c_vec);       \
+        if (past) tile_kernel<BM, BN, WM, WN, STAGES, KS, true><<<grid, kThreads, 0, stream>>>(g, mt, nt);   \
+        else tile_kernel<BM, BN, WM, WN, STAGES, KS, false><<<grid, kThreads, 0, stream>>>(g, mt, nt);       \
     } while (0)
     switch (kernel) {
         case sched::kI8Rows:
@@ -438,11 +424,11 @@ hipError_t launch_gemm_i8(const I8Args& g, int cus, hipStream_t stream) {
         case sched::kI8Tile32x32: BSFP8_TILE(32, 32, 16, 16, 4, 256); break;
         case sched::kI8Tile32x64: BSFP8_TILE(32, 64, 32, 16, 3, 256); break;
         case sched::kI8Tile64x64: BSFP8_TILE(64, 64, 16, 32, 4, 256); break;
-        case sched::kI8Tile64x128: tile_kernel<64, 128, 32, 32, 3, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
-        case sched::kI8Tile128x128: tile_kernel<128, 128, 32, 64, 4, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
-        case sched::kI8Tile128x128Two: tile_kernel<128, 128, 32, 64, 2, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
-        case sched::kI8Tile128x256: tile_kernel<128, 256, 32, 128, 3, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
-        default: big_kernel<<<grid, 512, 0, stream>>>(g, mt, nt, c_vec); break;
+        case sched::kI8Tile64x128: tile_kernel<64, 128, 32, 32, 3, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt); break;
+        case sched::kI8Tile128x128: tile_kernel<128, 128, 32, 64, 4, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt); break;
+        case sched::kI8Tile128x128Two: tile_kernel<128, 128, 32, 64, 2, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt); break;
+        case sched::kI8Tile128x256: tile_kernel<128, 256, 32, 128, 3, 128, false><<<grid, 512, 0, stream>>>(g, mt, nt); break;
+        default: big_kernel<<<grid, 512, 0, stream>>>(g, mt, nt); break;
     }
 #undef BSFP8_TILE
     return hipGetLastError();
