@@ -324,14 +324,14 @@ inline int64_t grad_blocks(int64_t units) { return units < kGradBlocks ? units :
 // gemm_i8: the kernel of M x N x K. A tile kernel's time goes by rounds: its tiles over the compute units, one or
 // two workgroups on each (those whose LDS lets two in), every round as long as K's blocks of 128 plus what a
 // tile does before and after them. The costs are microseconds a block of a round of up to `cus` tiles, and of
-// up to twice as many, fitted on MI355X to 119 problems of 4 to 8192 rows by 512 to 14336 columns (weights not
-// in the last-level cache); the tiles chosen by them are within 1% of the best ones on average, 11% at most.
-// Times measured (us; 32x32, 64x64, 128x128 with four stages, 256x256): 64 x 4096 x 4096 8.0, 11.9, 19.5, 49;
-// 512 x 5120 x 5120 53, 41, 32, 82 (64x128: 40); 2048 x 4096 x 4096 113, 81, 49, 62 (128x128 twice a CU: 41);
-// 8192 x 5120 x 5120 624, 445, 288, 235. Up to four rows go to the kernel without tiles (1 x 14336 x 4096
-// 10.5, in 32x64 tiles 14.1; 2 x 4096 x 14336 11.9, 17.2).
+// up to twice as many, fitted on MI355X to 632 problems of 48 to 8192 rows by 512 to 14336 columns (weights not
+// in the last-level cache); the tiles chosen by them are within 0.2% of the best ones on average, 15% at most.
+// Times measured (us): 48 x 4096 x 4096 in 32x32 7.8, 32x64 9.7, 64x64 10.9, 64x128 16; 512 x 5120 x 5120 in 64x64 41,
+// 64x128 36, 128x128 with four stages 30.6, twice a CU 44, 256x256 67; 2048 x 4096 x 4096 in the last four 52, 51, 40.3,
+// 53; 8192 x 5120 x 5120 303, 277, 228, 199. Up to four rows go to the kernel without tiles (1 x 14336 x 4096 10.5, in
+// 32x64 tiles 14.1; 2 x 4096 x 14336 11.9, 17.2).
 enum I8Kernel {
-    kI8Rows, kI8Tile32x32, kI8Tile32x64, kI8Tile64x64, kI8Tile64x128, kI8Tile128x128, kI8Tile128x128Two, kI8Tile128x256, kI8Big
+    kI8Rows, kI8Tile32x32, kI8Tile32x64, kI8Tile64x64, kI8Tile64x128, kI8Tile128x128, kI8Tile128x128Two, kI8Big
 };
 struct I8Tile {
     int bm, bn;
@@ -340,7 +340,7 @@ struct I8Tile {
 };
 constexpr I8Tile kI8Tiles[] = {
     {4, 4, 0, 0, 0},           {32, 32, 0.16, 0.27, 3},  {32, 64, 0.25, 0.43, 3},   {64, 64, 0.30, 0, 3},  {64, 128, 0.48, 0.85, 3},
-    {128, 128, 0.65, 0, 5},    {128, 128, 0.90, 1.15, 4}, {128, 256, 1.05, 0, 7},    {256, 256, 1.65, 0, 9},
+    {128, 128, 0.65, 0, 5},    {128, 128, 0.80, 1.14, 3}, {256, 256, 1.45, 0, 6},
 };
 constexpr int64_t kI8RowsColumns = int64_t{1} << 24;  // 2^32 lanes and more beyond
 
