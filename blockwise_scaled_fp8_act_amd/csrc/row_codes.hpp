@@ -151,10 +151,21 @@ template <bool ONCE, typename V>
 __device__ __forceinline__ V load_piece(const V* p) {
     return ONCE ? __builtin_nontemporal_load(p) : *p;
 }
+// Not through load_piece: a deduced type loses the small alignment, and the load would count as 16-byte aligned.
+template <bool ONCE>
+__device__ __forceinline__ rc_u32x4 load_any(const uint16_t* p) {
+    const rc_u32x4_any* q = reinterpret_cast<const rc_u32x4_any*>(p);
+    return ONCE ? __builtin_nontemporal_load(q) : *q;
+}
+template <bool ONCE>
+__device__ __forceinline__ rc_f32x4 load_any(const float* p) {
+    const rc_f32x4_any* q = reinterpret_cast<const rc_f32x4_any*>(p);
+    return ONCE ? __builtin_nontemporal_load(q) : *q;
+}
 template <bool ONCE = false, bool ANY = false>
 __device__ __forceinline__ rc_u32x4 load8_bf16(const uint16_t* p, int64_t n = 8) {
     if (!ANY) return load_piece<ONCE>(reinterpret_cast<const rc_u32x4*>(p));
-    if (n >= 8) return load_piece<ONCE>(reinterpret_cast<const rc_u32x4_any*>(p));
+    if (n >= 8) return load_any<ONCE>(p);
     rc_u32x4 w = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 7; ++j)
@@ -170,8 +181,8 @@ __device__ __forceinline__ void load8_of(const void* p, int64_t at, float (&f)[8
         if (!ANY || n >= 8) {
             rc_f32x4 lo, hi;
             if (ANY) {
-                lo = load_piece<ONCE>(reinterpret_cast<const rc_f32x4_any*>(q));
-                hi = load_piece<ONCE>(reinterpret_cast<const rc_f32x4_any*>(q + 4));
+                lo = load_any<ONCE>(q);
+                hi = load_any<ONCE>(q + 4);
             } else {
                 lo = load_piece<ONCE>(reinterpret_cast<const rc_f32x4*>(q));
                 hi = load_piece<ONCE>(reinterpret_cast<const rc_f32x4*>(q + 4));

@@ -1,0 +1,21 @@
+"""What the compiler is told about the kernels' memory accesses, looked up on the CPU (device code is compiled and not run)."""
+import os
+import subprocess
+
+import pytest
+
+from blockwise_scaled_fp8_act_amd import build
+
+SOURCES = [s for s in build.SOURCES if s.endswith(".hip")]
+
+
+def compile_device(source, *flags):
+    return subprocess.run([build.HIPCC, *build.CFLAGS, "--cuda-device-only", *flags, os.path.join(build.CSRC, source)], capture_output=True, text=True)
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_no_access_claims_more_alignment_than_its_address_has(source):
+    """A pointer to a type of small alignment that goes into a parameter of a larger one: a template's deduced type
+    drops the attribute, and the access behind it counts as aligned."""
+    r = compile_device(source, "-fsyntax-only", "-Werror=align-mismatch", "-Wno-unused-command-line-argument")
+    assert r.returncode == 0, r.stderr[-2000:]
