@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBackwardArg
     constexpr int kRows = kThreads / TPR;
     constexpr bool kAhead = NC <= 2;
     __shared__ float part[2][kWaves];
-    __shared__ float sums[kRows > 1 ? kRows : 1][kRows > 1 ? 8 * TPR * NC : 1];
+    __shared__ alignas(16) float sums[kRows > 1 ? kRows : 1][kRows > 1 ? 8 * TPR * NC : 1];
     const int tid = threadIdx.x % TPR, side = threadIdx.x / TPR;
     float w[NC][8], dw[NC][8];
 #pragma unroll

@@ -19,3 +19,10 @@ def test_no_access_claims_more_alignment_than_its_address_has(source):
     drops the attribute, and the access behind it counts as aligned."""
     r = compile_device(source, "-fsyntax-only", "-Werror=align-mismatch", "-Wno-unused-command-line-argument")
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_shared_rows_of_sums_declare_the_alignment_of_their_stores():
+    """norm_backward_kernel writes them in 16-byte pieces (store8_of of whole pieces)."""
+    with open(os.path.join(build.CSRC, "norm.hip")) as f:
+        text = f.read()
+    assert "store8_of<true>(sums[side]" in text and "__shared__ alignas(16) float sums[" in text
