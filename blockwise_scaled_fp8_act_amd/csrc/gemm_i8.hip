@@ -111,6 +111,7 @@ __device__ __forceinline__ void store_block(const I8Args& g, const i32x4 (&acc)[
             *reinterpret_cast<uint2*>(own + r * (2 * WN) + (((2 * j + (lg >> 1)) ^ (r & (kChunks - 1))) * 16) + 8 * (lg & 1)) = scaled4(acc[i][j], as, bs);
         }
     }
+    wave_lds_fence();  // the pieces read below are other lanes' writes
 #pragma unroll
     for (int p = 0; p < (WM * kChunks + 63) / 64; ++p) {
         const int r = (64 * p + lane) / kChunks, c = lane % kChunks;

@@ -42,12 +42,6 @@ __device__ __forceinline__ F wave_sum(F v) {
     return v;
 }
 
-// Orders one wave's LDS writes before its later LDS reads (no other wave is involved).
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // Below this logit sigmoid scores are formed in 64 bits: 1 / (1 + exp(-z)) in fp32 is 0 from -88.7 on,
 // where exp(-z) overflows, while the score and a floored sum of such still give ordinary weights.
 constexpr float kFarLogit = -80.0f;
