@@ -26,8 +26,8 @@ __device__ __forceinline__ float reciprocal(float d) {
     return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
-// Where |g| <= 80 nothing leaves fp32's ordinary range: with t = exp(-g), sig = 1 / (1 + t) and
-// 1 - sig = t sig, neither with cancellation. Beyond, sig is 1 to fp32, or exp(g) to 2^-115: that leaves
+// Where |g| <= 80 neither sig = 1 / (1 + t) with t = exp(-g) nor 1 - sig = t sig nor g sig leaves fp32's ordinary range,
+// and none is formed with cancellation. Beyond, sig is 1 to fp32, or exp(g) to 2^-115: that leaves
 // fp32's ordinary range while g sig u need not (u is as large as 3e38), so it is taken in 64 bits, from the
 // fourth power of exp(g / 4). Eight values share the test for it.
 constexpr float kFar = 80.0f;
@@ -60,21 +60,38 @@ __device__ __forceinline__ float swiglu(float g, float u) {
     return v[0];
 }
 
-// dg = dy u sig (1 + g (1 - sig)), du = dy g sig
+// dg = (dy u) d with d = sig (1 + g (1 - sig)), |d| < 1.1, and du = (g sig) dy. dy u of two bf16 is whole in fp32 but at its
+// ends: below 2^-126 it is off by 2^-150, which d does not enlarge; beyond kHuge, where it may pass fp32 while dg need
+// not, dg is formed in 64 bits (with u sig (1 + g (1 - sig)) first, u of 3.2e38 and dy of 0.01 gave an infinity, and
+// its group's scale with it, and u of 1e-11 at a gate of -79 lost all but 27 steps before a large dy).
+constexpr float kHuge = 0x1p127f;
+__device__ __forceinline__ float gate_factor(float g, float& sig) {
+    const float t = exp_of(-g);
+    sig = reciprocal(1.0f + t);
+    return sig * fmaf(g, t * sig, 1.0f);
+}
 __device__ __forceinline__ void swiglu_grad8(const float (&dy)[8], const float (&g)[8], const float (&u)[8], float (&dg)[8], float (&du)[8]) {
+    float most = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = exp_of(-g[j]), sig = reciprocal(1.0f + t);
-        dg[j] = (u[j] * (sig * fmaf(g[j], t * sig, 1.0f))) * dy[j];
+        float sig;
+        const float d = gate_factor(g[j], sig);
+        const float p = dy[j] * u[j];
+        most = fmaxf(most, fabsf(p));
+        dg[j] = p * d;
         du[j] = (g[j] * sig) * dy[j];
     }
-    if (__builtin_expect(any_far(g), 0)) {
+    if (__builtin_expect(any_far(g) || most > kHuge, 0)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j) {
             if (fabsf(g[j]) > kFar) {
-                dg[j] = g[j] > 0.0f ? u[j] * dy[j] : far_product(1.0f + g[j], u[j], dy[j], g[j]);
+                dg[j] = g[j] > 0.0f ? dy[j] * u[j] : far_product(1.0f + g[j], u[j], dy[j], g[j]);
                 du[j] = g[j] > 0.0f ? g[j] * dy[j] : far_product(g[j], dy[j], 1.0f, g[j]);
+            } else if (fabsf(dy[j] * u[j]) > kHuge) {
+                float sig;
+                dg[j] = static_cast<float>(static_cast<double>(gate_factor(g[j], sig)) * u[j] * dy[j]);
             }
+        }
     }
 }
 

@@ -542,7 +542,7 @@ int rms_norm_backward(const void* dy, int64_t lddy, const void* h, int h_dtype, 
  * swiglu_quantize_lhs_and_rhs: v in both groupings, as quantize_lhs_and_rhs: q [T, F], a_s column-major
  * [T, ceil(F/128)], qT [F, T], s [ceil(T/128), F]. codes: E4M3FN or E4M3FNUZ.
  * swiglu_backward: dgu [T, 2 F] bf16 of dy [T, F] bf16: dgate = dy up sig (1 + gate (1 - sig)),
- * dup = dy gate sig, with sig = sigmoid(gate).
+ * dup = dy gate sig, with sig = sigmoid(gate). No partial product leaves fp32 where the whole one does not.
  * swiglu_backward_quantize: the same gradient in both groupings, as quantize_lhs_and_rhs of its fp32
  * values: q [T, 2 F], a_s, qT [2 F, T], s.
  * ceil(T/128) at most 65535 and at most 2^30 - 128 code columns for the forms with both groupings.
