@@ -139,9 +139,20 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const double* partial, i
     if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
+// Below 2^-126 by `wide`, in 64 bits, a value a lane: the factor has lost digits in fp32 there, or is 0, while the products of
+// large gradients are ordinary. Rare, so it has no pieces.
 template <bool IN_F32, bool OUT_F32, bool PAST>
-__device__ __forceinline__ void scale(const void* in, void* out, int64_t from, int64_t to, float c) {
+__device__ __forceinline__ void scale(const void* in, void* out, int64_t from, int64_t to, float c, double wide) {
     constexpr bool kWide = !IN_F32 && !OUT_F32;
+    const auto store = [&](int64_t at, float v) {
+        if (OUT_F32) static_cast<float*>(out)[at] = v;
+        else static_cast<uint16_t*>(out)[at] = to_bf16_bits(v);
+    };
+    if (wide < 0x1p-126 && wide > 0.0) {
+        for (int64_t at = from + threadIdx.x; at < to; at += kThreads)
+            store(at, static_cast<float>(static_cast<double>(load_of(in, at, IN_F32)) * wide));
+        return;
+    }
     if ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) % 16 == 0) {
         for (; from + kAhead * kStep <= to; from += kAhead * kStep) {
             float v[kAhead][kVec];
@@ -162,11 +173,7 @@ __device__ __forceinline__ void scale(const void* in, void* out, int64_t from, i
             store_step<OUT_F32, kWide, PAST>(out, from, v);
         }
     }
-    for (int64_t at = from + threadIdx.x; at < to; at += kThreads) {
-        const float v = load_of(in, at, IN_F32) * c;
-        if (OUT_F32) static_cast<float*>(out)[at] = v;
-        else static_cast<uint16_t*>(out)[at] = to_bf16_bits(v);
-    }
+    for (int64_t at = from + threadIdx.x; at < to; at += kThreads) store(at, load_of(in, at, IN_F32) * c);
 }
 
 // 1.6 GB of bf16 into 3.2 GB of fp32: 939 us, 5.1 TB/s, what a copy reaches (976 with the stores through the
@@ -182,11 +189,11 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(GradTable t, const doubl
     for_units(t, [&](int i, int64_t from, int64_t to) {
         if (c == 1.0f && t.in[i] == t.out[i]) return;  // in place: nothing to do
         if (t.in_f32[i]) {
-            if (t.out_f32[i]) scale<true, true, PAST>(t.in[i], t.out[i], from, to, c);
-            else scale<true, false, PAST>(t.in[i], t.out[i], from, to, c);
+            if (t.out_f32[i]) scale<true, true, PAST>(t.in[i], t.out[i], from, to, c, ratio);
+            else scale<true, false, PAST>(t.in[i], t.out[i], from, to, c, ratio);
         } else {
-            if (t.out_f32[i]) scale<false, true, PAST>(t.in[i], t.out[i], from, to, c);
-            else scale<false, false, PAST>(t.in[i], t.out[i], from, to, c);
+            if (t.out_f32[i]) scale<false, true, PAST>(t.in[i], t.out[i], from, to, c, ratio);
+            else scale<false, false, PAST>(t.in[i], t.out[i], from, to, c, ratio);
         }
     });
 }

@@ -581,7 +581,7 @@ int gemm_i8(const void* a, int64_t lda, const float* a_s, const void* b, int64_t
  *   workspace  device memory of grad_workspace(sizes, count) bytes (-1: invalid sizes), 8-byte aligned, not in use
  *              by another call.
  * clip_grads: the same norm, and outs[i] = grads[i] * c in fp32, rounded to out_dtypes[i], with
- * c = min(1, max_norm / (norm + eps)); c = 1 where the norm is not finite, so that the gradients stay as
+ * c = min(1, max_norm / (norm + eps)), in 64 bits where it is below 2^-126; c = 1 where the norm is not finite, so that the gradients stay as
  * they are and norm[0] says so. outs[i] may be grads[i] itself (of one type); any other overlap of an
  * output with a gradient or an output is BSFP8_EINVAL. max_norm >= 0, eps >= 0 and finite.
  * The host is not synchronised; gradients are read in 16-byte pieces where they are so aligned.
