@@ -1301,8 +1301,9 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
 
 def clip_grads(grads, max_norm, out=None, norm=None, eps=1e-6, workspace=None, stream=None):
     """Scales the gradients by min(1, max_norm / (norm + eps)), norm being grad_norm(grads); in place, or into
-    the tensors of ``out`` (of the gradients' shapes and layouts, bf16 or fp32). Where the norm is not finite the
-    gradients are left (copied) as they are. Returns norm (1,) fp32 on the device; the host is not synchronised."""
+    the tensors of ``out`` (of the gradients' shapes and layouts, bf16 or fp32). Gradients that hold an infinity or a
+    NaN are left (copied) as they are. Returns norm (1,) fp32 on the device, not finite then; it is infinite also for
+    finite gradients of a norm beyond fp32, which are clipped. The host is not synchronised."""
     if stream is None and _calls is not None:
         done = _calls.clip_grads(grads, max_norm, out, norm, eps, workspace)
         if done is not None:

@@ -1,7 +1,7 @@
 // gfx950 global gradient norm over many tensors and clipping: norm = sqrt(sum of squares), out = g c with
 // c = min(1, max_norm / (norm + eps)). A launch takes the addresses of up to kGradTensors tensors in its
-// arguments, so a call copies no table to the device. Squares and sums are in 64 bits, in an order that
-// depends on the sizes alone: no gradient overflows its square, and the norm is the same on every call.
+// arguments, so a call copies no table to the device. Squares and sums are in 64 bits, in an order that sizes, types
+// and alignment decide: no gradient overflows its square, and the norm is the same on every call.
 // Bound by the memory traffic: every gradient is read once for the norm and once for the clipped copy.
 #include "row_codes.hpp"
 #include "schedule.hpp"
@@ -183,7 +183,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(GradTable t, const doubl
     __shared__ double part[kWaves];
     const double v = norm_of(partial, count, part);
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(v);
-    // a norm that is not finite leaves the gradients as they are: the caller sees it in the norm
+    // in 64 bits the norm is finite unless a gradient is not: then all stay as they are. Beyond fp32 alone (norm[0] reads
+    // infinity) the gradients are finite, and so are the clipped ones.
     const double ratio = static_cast<double>(max_norm) / (v + static_cast<double>(eps));
     const float c = isfinite(v) && ratio < 1.0 ? static_cast<float>(ratio) : 1.0f;
     for_units(t, [&](int i, int64_t from, int64_t to) {

@@ -177,7 +177,8 @@ class ServingInt8FeedForward:
 
 def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     """clip_grads of the parameters' gradients, in place; parameters without one are passed over. Returns the norm
-    before the clipping, (1,) fp32 on the device, without waiting for it."""
+    before the clipping, (1,) fp32 on the device, without waiting for it. Unlike torch.nn.utils.clip_grad_norm_: no gradient
+    at all is an error, the norm has one dimension, and gradients that hold an infinity or a NaN are left as they are."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]

@@ -575,14 +575,17 @@ int gemm_i8(const void* a, int64_t lda, const float* a_s, const void* b, int64_t
 
 /*
  * grad_norm: norm[0] = sqrt(the sum of the squares of all values of `count` tensors), fp32; squares and sum
- * in 64 bits, in an order that depends on the sizes alone. No tensor: 0.
+ * in 64 bits, in an order that depends on sizes, types and 16-byte alignment alone. No tensor: 0. A finite norm
+ * beyond fp32 (fp32 gradients near its end) reads infinity.
  *   grads, sizes, dtypes   host arrays of `count` device addresses, numbers of values (each tensor dense)
  *                          and types (BSFP8_BF16, BSFP8_F32), read before the call returns.
  *   workspace  device memory of grad_workspace(sizes, count) bytes (-1: invalid sizes), 8-byte aligned, not in use
  *              by another call.
  * clip_grads: the same norm, and outs[i] = grads[i] * c in fp32, rounded to out_dtypes[i], with
- * c = min(1, max_norm / (norm + eps)), in 64 bits where it is below 2^-126; c = 1 where the norm is not finite, so that the gradients stay as
- * they are and norm[0] says so. outs[i] may be grads[i] itself (of one type); any other overlap of an
+ * c = min(1, max_norm / (norm + eps)), in 64 bits where it is below 2^-126. The norm there is the 64-bit one: it is finite
+ * unless a gradient holds an infinity or a NaN, in which case c = 1 and the gradients stay as they are. So NaN in norm[0]
+ * says that they stayed; infinity says that either they hold one and stayed, or they are finite and were clipped.
+ * outs[i] may be grads[i] itself (of one type); any other overlap of an
  * output with a gradient or an output is BSFP8_EINVAL. max_norm >= 0, eps >= 0 and finite.
  * The host is not synchronised; gradients are read in 16-byte pieces where they are so aligned.
  */
