@@ -17,6 +17,9 @@ products take, and the norm's 128x1 codes are formed again from h in the backwar
               codes of n (128x1)    rms_norm_quantize_rhs        dW_gate_up  gemm_1x128_128x1
               dh, dweight_norm      rms_norm_backward
 
+Operands of the backward pass alone (the weights' transposed codes, the activation's 128x1 codes) are written and kept for
+the gradients that are asked for, and not at all without gradients (swiglu_quantize then forms the activation's codes).
+
 Serving (``ServingInt8FeedForward``) keeps the weights in int8 with a scale an output channel; the norm and the
 activation write int8 rows with a scale a token, and both products are gemm_i8.
 """
@@ -55,15 +58,24 @@ def _dense(t, dtype, T, H):
     return t if t.stride() == (H, 1) else torch.empty((T, H), dtype=dtype, device=t.device).copy_(t)
 
 
-def _weight(w, fmt):
+def _weight(w, fmt, transposed):
+    """Codes, transposed codes (None unless the gradient goes through them) and scales."""
     N, K = w.shape
-    return _b.quantize_weight_128x128(w, q=_codes(N, K, w.device), qT=_codes(K, N, w.device), fmt=fmt)
+    return _b.quantize_weight_128x128(w, q=_codes(N, K, w.device), qT=_codes(K, N, w.device) if transposed else None, want_qT=transposed, fmt=fmt)
+
+
+def _reads(needs):
+    """Of the gradients asked for (x, residual, weight_norm, w_gate_up, w_down): whether one goes back through w_gate_up,
+    through w_down, and whether w_down's own is among them."""
+    through_1 = any(needs[:3])
+    return through_1, through_1 or needs[3], needs[4]
 
 
 class _FeedForwardFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, residual, weight_norm, w_gate_up, w_down, eps, fmt):
+    def forward(ctx, x, residual, weight_norm, w_gate_up, w_down, eps, fmt, live):
         F, H = _layer(weight_norm, w_gate_up, w_down)
+        through_1, through_2, own_2 = _reads(ctx.needs_input_grad) if live else (False, False, False)
         given, ctx.shape = x, x.shape
         if residual is not None:
             if residual.shape != x.shape:
@@ -72,15 +84,20 @@ class _FeedForwardFn(torch.autograd.Function):
         x = _rows("x", x.reshape(-1, x.shape[-1]), H, (torch.bfloat16,))
         T, dev = x.shape[0], x.device
         w_gate_up, w_down, weight_norm = w_gate_up.contiguous(), w_down.contiguous(), weight_norm.contiguous()
-        q, s, h, _, rstd = _b.rms_norm_quantize(x, weight_norm, residual=residual, eps=eps, fmt=fmt, q=_codes(T, H, dev), want_rstd=True)
+        q, s, h, _, rstd = _b.rms_norm_quantize(x, weight_norm, residual=residual, eps=eps, fmt=fmt, q=_codes(T, H, dev), want_rstd=through_2)
         h = x if h is None else h
-        q1, q1T, s1 = _weight(w_gate_up, fmt)
-        q2, q2T, s2 = _weight(w_down, fmt)
+        q1, q1T, s1 = _weight(w_gate_up, fmt, through_1)
+        q2, q2T, s2 = _weight(w_down, fmt, through_2)
         gu = _b.gemm_1x128_128x128(q, s, q1, s1, fmt=fmt)
-        qa, sa, qaT, saT = _b.swiglu_quantize_lhs_and_rhs(gu, q=_codes(T, F, dev), qT=_codes(F, T, dev), fmt=fmt)
+        qaT = saT = None
+        if own_2:
+            qa, sa, qaT, saT = _b.swiglu_quantize_lhs_and_rhs(gu, q=_codes(T, F, dev), qT=_codes(F, T, dev), fmt=fmt)
+        else:
+            qa, sa, _ = _b.swiglu_quantize(gu, fmt, q=_codes(T, F, dev))
         y = _b.gemm_1x128_128x128(qa, sa, q2, s2, fmt=fmt)
-        ctx.save_for_backward(h, weight_norm, rstd, gu, qaT, saT, q1T, s1, q2T, s2)
-        ctx.fmt, ctx.x_dtype = fmt, x.dtype
+        # what a gradient that was asked for reads, and no more
+        ctx.save_for_backward(*((h, weight_norm, rstd, gu, q2T, s2) if through_2 else (None,) * 6), q1T, s1 if through_1 else None, qaT, saT)
+        ctx.fmt, ctx.x_dtype, ctx.h_dtype, ctx.sizes = fmt, x.dtype, h.dtype, (T, H, F)
         ctx.set_materialize_grads(False)        # an output that nothing was made of has no gradient to read
         return y.view(ctx.shape), given.view_as(given) if residual is None else h.view(ctx.shape)
 
@@ -92,31 +109,31 @@ class _FeedForwardFn(torch.autograd.Function):
 
 
 def _gradients(ctx, dy, dh):
-    h, weight_norm, rstd, gu, qaT, saT, q1T, s1, q2T, s2 = ctx.saved_tensors
-    h = h.reshape(-1, h.shape[-1])
-    fmt, dev, T, H, F = ctx.fmt, h.device, *h.shape, gu.shape[1] // 2
+    h, weight_norm, rstd, gu, q2T, s2, q1T, s1, qaT, saT = ctx.saved_tensors
+    fmt, T, H, F = ctx.fmt, *ctx.sizes
     need_x, need_r, need_n, need_1, need_2 = ctx.needs_input_grad[:5]
     dx = dw1 = dw2 = dwn = None
     if dy is None:                              # h alone was used
-        dx = None if dh is None else dh.to(h.dtype)
+        dx = None if dh is None else dh.to(ctx.h_dtype)
     else:
-        dy = _dense(dy, torch.bfloat16, T, H)
+        dy, dev = _dense(dy, torch.bfloat16, T, H), dy.device
         qd, sd, qdT, sdT = _b.quantize_lhs_and_rhs(dy, q=_codes(T, H, dev), qT=_codes(H, T, dev), fmt=fmt)
         if need_2:
             dw2 = _b.gemm_1x128_128x1(qdT, sdT, qaT, saT, fmt=fmt)
         if need_x or need_r or need_n or need_1:
             da = _b.gemm_1x128_128x128(qd, sd, q2T, s2, 1, s2.shape[1], fmt=fmt)
             qg, sg, qgT, sgT = _b.swiglu_backward_quantize(da, gu, q=_codes(T, 2 * F, dev), qT=_codes(2 * F, T, dev), fmt=fmt)
+            h = h.reshape(T, H)
             if need_1:
                 qn, sn = _b.rms_norm_quantize_rhs(h, weight_norm, rstd, qT=_codes(H, T, dev), fmt=fmt)
                 dw1 = _b.gemm_1x128_128x1(qgT, sgT, qn, sn, fmt=fmt)
             if need_x or need_r or need_n:
                 dn = _b.gemm_1x128_128x128(qg, sg, q1T, s1, 1, s1.shape[1], fmt=fmt)
-                dh = None if dh is None else _dense(dh, h.dtype, T, H)
+                dh = None if dh is None else _dense(dh, ctx.h_dtype, T, H)
                 dx, dwn = _b.rms_norm_backward(dn, h, weight_norm, rstd, dh=dh)
                 dx = dx.view(ctx.shape)
     gx = dx if dx is None or dx.dtype == ctx.x_dtype else dx.to(ctx.x_dtype)
-    return gx if need_x else None, dx if need_r else None, dwn if need_n else None, dw1, dw2, None, None
+    return gx if need_x else None, dx if need_r else None, dwn if need_n else None, dw1, dw2, None, None, None
 
 
 _gradients_once = once_differentiable(_gradients)
@@ -127,7 +144,7 @@ def blockwise_fp8_feed_forward(x, weight_norm, w_gate_up, w_down, residual=None,
     weight_norm [H] bf16 or fp32, w_gate_up [2 F, H] (gate rows, then up rows) and w_down [H, F] bf16. Returns
     (y bf16, h of the residual's type), both of x's shape; gradients of x, residual and all weights. ``fmt``: the FP8 element
     format ("e4m3fn", "e4m3fnuz" or the torch float8 dtype)."""
-    return _FeedForwardFn.apply(x, residual, weight_norm, w_gate_up, w_down, eps, _b.fp8_format(fmt))
+    return _FeedForwardFn.apply(x, residual, weight_norm, w_gate_up, w_down, eps, _b.fp8_format(fmt), torch.is_grad_enabled())
 
 
 class BlockwiseFp8FeedForward(torch.nn.Module):
