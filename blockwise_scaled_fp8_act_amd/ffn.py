@@ -171,12 +171,12 @@ def _int8_rows(rows, cols, device):
 
 
 class ServingInt8FeedForward:
-    """The layer for inference: weights quantized to int8 once, a scale an output channel; any number of
-    tokens."""
+    """The layer for inference: weights quantized to int8 once, a scale an output channel, and the norm's weight copied with them;
+    any number of tokens."""
 
     def __init__(self, weight_norm: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, eps: float = 1e-6):
         self.F, self.H = _layer(weight_norm, w_gate_up, w_down)
-        self.eps, self.weight_norm = eps, weight_norm.detach().contiguous()
+        self.eps, self.weight_norm = eps, weight_norm.detach().clone(memory_format=torch.contiguous_format)     # as the codes: of now
         with torch.no_grad():
             self.q1, self.s1 = _b.quantize_rows_i8(w_gate_up.contiguous(), q=_int8_rows(2 * self.F, self.H, w_gate_up.device))
             self.q2, self.s2 = _b.quantize_rows_i8(w_down.contiguous(), q=_int8_rows(self.H, self.F, w_down.device))
