@@ -2,8 +2,9 @@
 //   v = g sig(g) u,   dg = dy u sig(g) (1 + g (1 - sig(g))),   du = dy g sig(g),   sig(g) = 1 / (1 + exp(-g)),
 // formed in fp32 and written as e4m3 codes in 1x128 groups (for a training step in both groupings), as int8
 // rows, or in bf16. Bound by the memory traffic: the inputs are read once, the values never leave the
-// registers in a wider type unless they are asked for. Measured: 8192 x 4096 in both groupings 44 us (4.6 TB/s), the
-// gradient in both 66 to 71 (4.7 to 5.1); 64 x 5120 rows 3.7, 1000 x 1408 with a bf16 copy 4.2.
+// registers in a wider type unless they are asked for. Measured: 8192 x 4096 in both groupings 36 to 44 us (4.6 to 5.6 TB/s),
+// the gradient in both 66 to 73 (4.6 to 5.1), in bf16 56 (6.0); 64 x 5120 rows 3.7, as int8 3.6 (16384 x 5120 81, 5.2 TB/s),
+// 1000 x 1408 with a bf16 copy 4.2.
 #include "row_codes.hpp"
 #include "schedule.hpp"
 #include "tile_codes.hpp"
